@@ -282,6 +282,107 @@ fq_status fq_linear_fused(const uint16_t* X, int M, int K, const fq_qparams* act
                           const uint8_t* Wq, const void* s_w, int N, uint16_t* Y,
                           void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged INT4 key/value cache
+ * ------------------------------------------------------------------------
+ * The codes of fq_quant_kv held in pages, so that requests of any length
+ * share one pool of device memory.
+ * pool  uint8 [num_pages][H][page_size * 132], 16-byte aligned: the bytes of
+ *       one page and head are, with p = page_size tokens,
+ *         K codes  [p][64]   at 0        (two signed nibbles per byte)
+ *         V codes  [p][64]   at 64 p
+ *         K scales fp16 [p]  at 128 p
+ *         V scales fp16 [p]  at 130 p
+ *       so that one contiguous copy brings a page of one head.  A cached value is
+ *       code * scale, code in [-8, 7].
+ * page_size 16, 32, 64 or 128; H in [1, 128]; num_pages * page_size < 2^31.
+ * A token's place is its slot = page * page_size + position within the page;
+ * a slot outside [0, num_pages * page_size) (-1 for a padded row) is no place.
+ * Request r's token i lies in page block_table[r][i / page_size]. */
+typedef struct {
+  uint8_t* pool;
+  int num_pages;
+  int page_size;
+  int H;
+} fq_kv_cache;
+
+/* Block tables and slots of one step, on the GPU, from the request lengths:
+ * request r holds len[r] tokens and appends new_tokens[r] (int32 [R] each;
+ * negative counts are taken as 0).  It needs
+ *   ceil((len + new) / page_size) - ceil(len / page_size)
+ * fresh pages, taken from free_pages (int32 [num_free]) in request order from
+ * index *pages_used on.  Writes
+ *   block_table int32 [R][max_pages], in place: the fresh pages' ids after
+ *               the held ones (no other entry is touched);
+ *   len_out     int32 [R]: len + new (may be len itself);
+ *   token_start int32 [R + 1]: exclusive sums of new_tokens, i.e. the first
+ *               row of each request in the step's ragged token batch;
+ *   slots       int32 [max_tokens]: the slot of each of those rows; -1 from
+ *               token_start[R] on, so that a captured step of max_tokens rows
+ *               may hold fewer tokens;
+ *   pages_used_out int32 [1] (may be pages_used itself): pages_used + the pages taken.
+ * A request is refused as a whole, with slots -1, len_out = len and no pages,
+ * when its table row is too short (it asks for no pages then), when its rows
+ * pass max_tokens (nor here), or when it needs pages and the pages asked for up
+ * to and including it pass the free list: once that happens, no later request
+ * that needs pages gets any either.  The sum of new_tokens must stay below 2^31.
+ * R in [1, 16384].  One launch, no workspace; the outputs must not overlap
+ * the inputs except where stated. */
+fq_status fq_kv_plan(const int32_t* len, const int32_t* new_tokens, int R, int page_size, int32_t* block_table,
+                     int max_pages, const int32_t* free_pages, int num_free, const int32_t* pages_used,
+                     int32_t* len_out, int32_t* token_start, int32_t* slots, int max_tokens,
+                     int32_t* pages_used_out, void* stream);
+
+/* New keys and values into the cache: K, V fp16, T rows of H * 128 values,
+ * ldk / ldv elements apart (>= H * 128, a multiple of 8; rows 16-byte aligned), so
+ * that slices of one projection's output are taken as they are.  Each head
+ * vector is quantized as by fq_quant_kv without a transform: s = fp16((max|v|
+ * alpha) / 7), codes clamp(round(v / s), -8, 7), and goes to slots[t] (int32
+ * [T]); rows whose slot is no place are skipped.  The slots of one call must
+ * differ, else a shared slot may hold a mix of its rows.  One launch. */
+fq_status fq_kv_write(const uint16_t* K, long long ldk, const uint16_t* V, long long ldv, int T,
+                      const int32_t* slots, float alpha_k, float alpha_v, const fq_kv_cache* cache, void* stream);
+
+/* Head vectors that fq_quant_kv has quantized (with P_h for the keys, P_v
+ * for the values) into the cache: Kq, Vq uint8 [T, H * 64] (16-byte aligned), Ks, Vs fp16
+ * [T, H].  Slots as in fq_kv_write.  One launch. */
+fq_status fq_kv_store(const uint8_t* Kq, const uint16_t* Ks, const uint8_t* Vq, const uint16_t* Vs, int T,
+                      const int32_t* slots, const fq_kv_cache* cache, void* stream);
+
+/* Cached tokens back to fp16: K, V fp16 [T, H * 128] (16-byte aligned),
+ * fp16(code * scale) of slots[t]; zeros where the slot is no place.  One launch. */
+fq_status fq_kv_read(const fq_kv_cache* cache, const int32_t* slots, int T, uint16_t* K, uint16_t* V, void* stream);
+
+/* Attention of one new token per request over the paged INT4 cache:
+ *   y[r][h] = sum_i p_i v_i,  p = softmax_i(scale * q[r][h] . k_i)
+ * over the request's cached tokens i in [0, len[r]), or, with window > 0,
+ * over the last `window` of them; k_i, v_i = code * scale of key-value head
+ * h / (Hq / H) (float32, not rounded to fp16).  A request with no tokens gives zeros.
+ * Q      fp16, R rows of Hq * 128 values, ldq elements apart (>= Hq * 128, a
+ *        multiple of 8; rows 16-byte aligned).  With keys cached through P_h the
+ *        caller passes q P_h^-T, and with values through P_v folds P_v^-1 into
+ *        the output projection.
+ * len    int32 [R]; block_table int32 [R][max_pages].  len is taken as 0 when
+ *        negative and cut to max_pages * page_size.  Entries beyond a
+ *        request's tokens are not read; an entry outside [0, num_pages) leaves
+ *        its tokens out.  What a page holds behind the last token (NaN scales too)
+ *        has no effect.
+ * Y      fp16 [R, Hq * 128] (16-byte aligned).
+ * Hq a multiple of H, at most 1024; R in [1, 16384].
+ * Arithmetic: products of fp16 queries and integer codes summed in float32, softmax
+ * statistics and sums in float32; the weights p_i * (v scale) enter the second
+ * product rounded to fp16 after scaling (2^-11 relative).  The summation order
+ * is the kernel's, the same on every run for the same sizes and lengths.
+ * workspace / ws_bytes: fq_kv_attn_workspace_size(R, Hq, H) bytes, 256-byte
+ *   aligned, whose first FQ_WORKSPACE_SYNC_BYTES follow the rule of
+ *   fq_w4a4_gemm's workspace (zero before the first call, left zero).
+ * One launch; the work is divided on the GPU from len, so a captured call
+ * follows the lengths of each replay. */
+fq_status fq_kv_attn(const uint16_t* Q, long long ldq, int R, int Hq, const int32_t* len, const int32_t* block_table,
+                     int max_pages, const fq_kv_cache* cache, float scale, int window, uint16_t* Y, void* workspace,
+                     size_t ws_bytes, void* stream);
+size_t fq_kv_attn_workspace_size(int R, int Hq, int H);
+
 /* Scratch sizes in bytes (0 when none is needed).  gran as in the calls. */
 size_t fq_gemm_workspace_size(int M, int N, int K, fq_gran gran);
 size_t fq_linear_workspace_size(int M, int N, int K, fq_gran gran);

@@ -7,12 +7,13 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfq.so")
-SOURCES = ["abi.cu", "quant.cu", "quant_int.cu", "gemm.cu", "linear.cu", "ternary.cu"]
-HEADERS = ["fq_device.cuh", "fq_host.h", os.path.join("..", "..", "include", "fq.h")]
+SOURCES = ["abi.cu", "quant.cu", "quant_int.cu", "gemm.cu", "linear.cu", "ternary.cu", "kv_cache.cu", "kv_attn.cu"]
+HEADERS = ["fq_device.cuh", "fq_host.h", "kv_cache.cuh", os.path.join("..", "..", "include", "fq.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -40,14 +41,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
-    objs = []
-    for s in SOURCES:
-        o = os.path.join(objdir, s.replace(".cu", ".o"))
-        cmd = [_nvcc(), *NVCC_FLAGS, "-c", os.path.join(CSRC, s), "-o", o]
+    newest = max(os.path.getmtime(os.path.join(CSRC, h)) for h in HEADERS)
+    objs = [os.path.join(objdir, s.replace(".cu", ".o")) for s in SOURCES]
+
+    def compile_one(job):
+        src, obj = os.path.join(CSRC, job[0]), job[1]
+        if not force and os.path.exists(obj) and os.path.getmtime(obj) > max(newest, os.path.getmtime(src)):
+            return
+        cmd = [_nvcc(), *NVCC_FLAGS, "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd))
         subprocess.run(cmd, check=True)
-        objs.append(o)
+
+    with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as pool:
+        list(pool.map(compile_one, zip(SOURCES, objs)))
     tmp = LIB + ".tmp"
     cmd = [_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-cudart", "static", "-o", tmp, *objs]
     if verbose:

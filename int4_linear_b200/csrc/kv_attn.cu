@@ -1,0 +1,677 @@
+// Attention of one new token per request over the paged INT4 key/value cache.
+//
+//   s_i = scale q . k_i,  m = max s_i,  l = sum exp(s_i - m),
+//   y = (sum exp(s_i - m) v_i) / l,   k_i, v_i = code * scale
+//
+// The floor is one read of the cache: 132 bytes per token and key-value head
+// against 4 * 128 operations per query head, so the work is a stream of pages
+// with the arithmetic hidden under it.  At the measured 6.55 TB/s an SM has
+// about 5.7 cycles per token and head, i.e. some 23 warp instructions; turning
+// 256 nibbles into operands alone takes 10, so the layout below moves no operand
+// through shuffles or a second pass of shared memory.
+//
+// Division.  The tiles (64 tokens of one request and key-value head) of all
+// requests form one sequence, request-major; every CTA takes an equal contiguous
+// part of it, found on the GPU from the lengths, so ragged batches load every SM
+// alike and a captured launch follows the lengths of its replay.  A part is a run of
+// segments (one request and head each).  A segment that covers its whole
+// request is finished by its CTA; otherwise the CTA leaves (sum, m, l) in the
+// workspace, and the CTA that arrives last adds the parts in their fixed order
+// (the sums come out the same whichever CTA that is).
+//
+// In a CTA one warp brings the pages by bulk copies into an 8-stage ring (a page
+// of one head is one contiguous block), and 8 warps, 4 per tile, take 16 tokens
+// each, with their own m, l and sum, joined per segment through shared memory.
+//
+// Products: mma.m16n8k16 (fp16, float32 sums).  The tensor-memory path needs
+// 128 rows of queries, and a request has G = Hq / H <= 16 of them per head, so its
+// staging of operands would cost more than the product.
+//  - scores: A = 16 tokens x 128 dims of K codes, B = 8 queries.  A lane reads 16
+//    consecutive bytes of a token's row; the order of the dims inside the product is
+//    free, so the queries are arranged once per segment to match the nibbles.  A nibble
+//    becomes the fp16 number 64 + (code + 8) by one logic operation; the constant
+//    72 sum(q) is taken off through the accumulator's initial value (an error of
+//    72 sum|q| 2^-24, 2^-15 of a logit at most for queries and keys of unit size).
+//  - sum: A = 128 dims x 16 tokens of V codes (exact), B = the weights, taken
+//    from the scores' layout by movmatrix.  A lane reads 8 bytes of each of its 4
+//    tokens and pairs two tokens' nibbles by byte permutation.
+// Weights: w = exp2(s - m) * (v scale / largest v scale so far) * 2^8 is
+// rounded to fp16 (2^-11 relative, independent errors that the sum averages; weights below
+// 2^-22 of the largest lose bits, 2^-33 of it at most each).  m is a
+// reference that moves only when a score passes it by 2^7 (checked with one vote
+// per 16 tokens), so the sums are rarely rescaled.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "fq_device.cuh"
+#include "fq_host.h"
+#include "kv_cache.cuh"
+
+namespace fq {
+
+size_t sync_block_bytes();
+
+namespace {
+
+constexpr int kTile = 64;           // tokens per tile
+constexpr int kStages = 8;
+constexpr int kStageBytes = kTile * kKvTokenBytes;
+constexpr int kComputeWarps = 8;
+constexpr int kComputeThreads = kComputeWarps * 32;
+constexpr int kAttnThreads = kComputeThreads + 32;
+constexpr int kHeadPad = 164;       // floats of one head's sums in shared memory (see sum_offset)
+constexpr int kMaxAttnR = 16384;
+constexpr float kSlack = 7.0f;      // log2 of how far a score may pass the reference
+constexpr float kWeightScale = 256.0f;
+constexpr unsigned kErrTimeoutAttn = 0x106;
+
+struct AttnParams {
+  const __half* Q;
+  long long ldq;
+  int R, Hq, G, chunks;             // chunks of at most 8 NT query heads per key-value head
+  const int32_t* len;
+  const int32_t* table;
+  int max_pages;
+  KvView kv;
+  float scale_log2;
+  int window;
+  __half* Y;
+  float* part;                      // [2 * CTAs][8 NT][130]: sums, m, l
+  unsigned* count;                  // one counter per CTA
+  unsigned* err;
+};
+
+struct AttnSmem {
+  uint64_t full[kStages], empty[kStages];
+  uint32_t valid[kStages];          // bit i: tokens [16 i, 16 i + 16) of the tile were loaded
+  long long first, last;            // this CTA's part of the tile sequence
+  long long total;
+  int r0;                           // the request it starts in, and the tiles before that request
+  long long before;
+  long long wsum[kAttnThreads / 32];
+  float m[kComputeWarps][16], l[kComputeWarps][16];
+  int join;
+};
+
+// Tiles [t0, t1) and tokens [lo, hi) of request r.
+struct Span {
+  int lo, hi, t0, t1;
+};
+__device__ __forceinline__ Span span_of(const AttnParams& p, int r) {
+  const long long cap = static_cast<long long>(p.max_pages) << p.kv.page_shift;
+  Span s;
+  s.hi = int(min(static_cast<long long>(max(p.len[r], 0)), cap));
+  s.lo = p.window > 0 ? max(0, s.hi - p.window) : 0;
+  s.t0 = s.lo / kTile;
+  s.t1 = s.hi > s.lo ? (s.hi - 1) / kTile + 1 : s.t0;
+  return s;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// Nibbles at bits 4-7 of each half word (two's complement codes q) -> fp16 72 + q.
+__device__ __forceinline__ uint32_t codes72(uint32_t w) { return (w & 0x00F000F0u) ^ 0x54805480u; }
+// Nibbles at bits 0-3 of each half word -> fp16 1032 + q.
+__device__ __forceinline__ uint32_t codes1032(uint32_t w) { return (w & 0x000F000Fu) ^ 0x64086408u; }
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The token of score row i (0..15): rows 2t, 2t + 1 of one lane's weights.  Bit 0
+// alternates within a row pair (score reads of two rows hit different banks)
+// and with t (the four lanes of a value read hit two bank halves).
+__device__ __forceinline__ int token_of_row(int i) {
+  const int t = (i >> 1) & 3, b = i & 1;
+  return (b ^ (t & 1)) | ((t & 1) << 1) | ((t >> 1) << 2) | (i & 8);
+}
+
+// Where dim 16 g + d of a head's sums lies in shared memory: lanes with
+// consecutive g write, and lanes with consecutive (d / 4, g) read, distinct banks.
+__device__ __forceinline__ int sum_offset(int g, int d) { return d * 8 + (d >> 2) * 8 + g; }
+
+// The CTA whose part holds tile x of the sequence: parts are [total c / C, total (c + 1) / C).
+__device__ __forceinline__ int cta_of_tile(long long x, long long total, int C) {
+  return int(((x + 1) * C - 1) / total);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(const AttnParams p) {
+  constexpr int HB = 8 * NT;
+  extern __shared__ __align__(128) uint8_t dyn[];
+  uint8_t* ring = dyn;
+  float* sums = reinterpret_cast<float*>(dyn + kStages * kStageBytes);  // [warps][8][kHeadPad]
+  __shared__ AttnSmem sm;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, HC = p.kv.H * p.chunks;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 4);
+    }
+    fence_mbar_init();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // ---- this CTA's part: tiles of each thread's run of requests, summed
+  const int run = (p.R + kAttnThreads - 1) / kAttnThreads;
+  const int ra = min(p.R, tid * run), rb = min(p.R, ra + run);
+  long long mine = 0;
+  for (int r = ra; r < rb; ++r) {
+    const Span s = span_of(p, r);
+    mine += s.t1 - s.t0;
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) sm.wsum[warp] = incl;
+  __syncthreads();
+  long long base = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kAttnThreads / 32; ++w) {
+    if (w < warp) base += sm.wsum[w];
+    all += sm.wsum[w];
+  }
+  const long long total = all * HC;
+  // few tiles: fewer CTAs, so that a part is worth its join
+  const int C = int(min(static_cast<long long>(gridDim.x), (total + 1) / 2));
+  // requests without tokens
+  for (int r = cta; r < p.R; r += gridDim.x) {
+    const Span s = span_of(p, r);
+    if (s.t1 == s.t0)
+      for (int i = tid; i < p.Hq * kHeadDim / 8; i += kAttnThreads)
+        reinterpret_cast<uint4*>(p.Y + static_cast<size_t>(r) * p.Hq * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
+  }
+  if (cta >= C) return;
+  const long long first = total * cta / C, last = total * (cta + 1) / C;
+  {
+    const long long e0 = (base + incl - mine) * HC, e1 = (base + incl) * HC;
+    if (e0 <= first && first < e1) {
+      long long acc = e0;
+      for (int r = ra; r < rb; ++r) {
+        const Span s = span_of(p, r);
+        const long long n = static_cast<long long>(s.t1 - s.t0) * HC;
+        if (first < acc + n) {
+          sm.r0 = r;
+          sm.before = acc;
+          break;
+        }
+        acc += n;
+      }
+    }
+  }
+  __syncthreads();
+
+  int r = sm.r0;
+  long long pos = first, before = sm.before;  // next tile; tiles before request r
+  int n = 0;                                  // tiles of this CTA so far
+  if (warp == kComputeWarps) {
+    // ------------------------------------------------------------ pages into the ring
+    const int ps = p.kv.page_shift;
+    const int sub = lane & 3;                  // lane 4 i + sub: copy `sub` of tile i of a batch of 8
+    const int copies = ps == 4 ? 4 : ps == 5 ? 2 : ps == 6 ? 1 : 4;
+    bool bad = false;
+    while (pos < last) {
+      const Span s = span_of(p, r);
+      const int nt = s.t1 - s.t0;
+      const long long len_r = static_cast<long long>(nt) * HC;
+      if (pos >= before + len_r) {
+        before += len_r;
+        ++r;
+        continue;
+      }
+      const int hc = int((pos - before) / nt), ta = int((pos - before) % nt);
+      const int tb = int(min(static_cast<long long>(nt), ta + (last - pos)));
+      const int head = hc / p.chunks;
+      const int32_t* row = p.table + static_cast<size_t>(r) * p.max_pages;
+      // page ids of a batch of 8 tiles, one batch ahead of the copies
+      auto load_id = [&](int t) {
+        const int tok = (s.t0 + t + (lane >> 2)) * kTile + (ps < 6 ? sub << ps : 0);
+        if (t + (lane >> 2) >= tb || sub >= copies || tok >= s.hi) return -1;
+        const int pg = tok >> ps;
+        if (((pg + 1) << ps) <= s.lo) return -1;
+        const int id = __ldg(row + pg);
+        return id >= 0 && id < p.kv.num_pages ? id : -1;
+      };
+      int id = load_id(ta);
+      for (int t = ta; t < tb; t += 8) {
+        const int next = load_id(t + 8);
+        const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
+        for (int i = 0; i < 8 && t + i < tb; ++i, ++n) {
+          const int st = n % kStages;
+          if (!bad && n >= kStages && !warp_wait(&sm.empty[st], ((n / kStages) - 1) & 1)) {
+            if (lane == 0) record_error(p.err, kErrTimeoutAttn);
+            bad = true;
+          }
+          const uint32_t got = bad ? 0u : (have >> (4 * i)) & 15u;
+          if (lane == 0) {
+            uint32_t v = 0, bytes = 0;
+            if (ps == 4) {
+              v = got;
+              bytes = __popc(got) * (16 * kKvTokenBytes);
+            } else if (ps == 5) {
+              v = (got & 1u ? 3u : 0u) | (got & 2u ? 12u : 0u);
+              bytes = __popc(got) * (32 * kKvTokenBytes);
+            } else if (got) {
+              v = 15u;
+              bytes = kStageBytes;
+            }
+            sm.valid[st] = v;
+            mbar_arrive_expect_tx(&sm.full[st], bytes);
+          }
+          __syncwarp();
+          if ((lane >> 2) == i && id >= 0 && !bad) {
+            const uint8_t* src = p.kv.block(id, head);
+            uint8_t* dst = ring + st * kStageBytes;
+            if (ps <= 6) {
+              bulk_load(dst + (sub * kKvTokenBytes << ps), src, uint32_t(kKvTokenBytes << ps), &sm.full[st]);
+            } else {
+              // half of a page of 128, laid out as a page of 64
+              const int half = (s.t0 + t + i) & 1;
+              const int which = sub & 1;
+              if (sub < 2)
+                bulk_load(dst + which * kTile * kKvRowBytes, src + p.kv.codes(which) + half * kTile * kKvRowBytes,
+                          kTile * kKvRowBytes, &sm.full[st]);
+              else
+                bulk_load(dst + 2 * kTile * kKvRowBytes + which * kTile * 2,
+                          src + p.kv.scales(which) + half * kTile * 2, kTile * 2, &sm.full[st]);
+            }
+          }
+        }
+        id = next;
+      }
+      pos += tb - ta;
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- scores and sums
+  const int g = lane >> 2, t4 = lane & 3;
+  const int grp = warp >> 2, quarter = warp & 3;
+  const int psub = min(p.kv.page_shift, 6);                      // log2 of a ring block's tokens
+  const int blk = ((quarter * 16) >> psub) * (kKvTokenBytes << psub);
+  const int off = (quarter * 16) & ((1 << psub) - 1);
+  // byte offsets inside a stage of this lane's operands
+  const int row0 = token_of_row(g);                              // score rows g and g + 8: tokens row0, row0 + 8
+  const int k_off = blk + (off + row0) * kKvRowBytes + t4 * 16;
+  const int ks_off = blk + (2 * kKvRowBytes << psub) + 2 * (off + row0);
+  const int vs_off = blk + ((2 * kKvRowBytes + 2) << psub) + 2 * (off + row0);
+  const int va = token_of_row(2 * t4), vb = token_of_row(2 * t4 + 1);
+  const int v_off = blk + (kKvRowBytes << psub) + off * kKvRowBytes + 8 * g;
+  bool bad = false;
+  while (pos < last) {
+    const Span s = span_of(p, r);
+    const int nt = s.t1 - s.t0;
+    const long long len_r = static_cast<long long>(nt) * HC;
+    if (pos >= before + len_r) {
+      before += len_r;
+      ++r;
+      continue;
+    }
+    const int hc = int((pos - before) / nt), ta = int((pos - before) % nt);
+    const int tb = int(min(static_cast<long long>(nt), ta + (last - pos)));
+    const int head = hc / p.chunks, q0 = head * p.G + (hc % p.chunks) * HB;  // first query head
+    const int heads = min(HB, p.G - (hc % p.chunks) * HB);
+
+    // queries of this segment, in the order of the nibbles: lane (g, t4) holds head g, dims [32 t4, 32 t4 + 32)
+    uint32_t qf[NT][16];
+    float c0[NT][2];
+#pragma unroll
+    for (int nn = 0; nn < NT; ++nn) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (nn * 8 + g < heads)
+          w = *reinterpret_cast<const uint4*>(p.Q + static_cast<long long>(r) * p.ldq +
+                                              (q0 + nn * 8 + g) * kHeadDim + 32 * t4 + 8 * j);
+        qf[nn][4 * j + 0] = __byte_perm(w.x, w.z, 0x5410);  // dims 0, 4
+        qf[nn][4 * j + 1] = __byte_perm(w.x, w.z, 0x7632);  // dims 1, 5
+        qf[nn][4 * j + 2] = __byte_perm(w.y, w.w, 0x5410);  // dims 2, 6
+        qf[nn][4 * j + 3] = __byte_perm(w.y, w.w, 0x7632);  // dims 3, 7
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&qf[nn][4 * j + k]));
+          sum += f.x + f.y;
+        }
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      c0[nn][0] = -72.0f * __shfl_sync(0xffffffffu, sum, 8 * t4);
+      c0[nn][1] = -72.0f * __shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
+    }
+    float o[NT][8][4];
+    float m[NT][2], l[NT][2];
+    float vcap = 0.f, vinv = 0.f;  // largest v scale so far, and 2^8 over it
+#pragma unroll
+    for (int nn = 0; nn < NT; ++nn) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[nn][i][k] = 0.f;
+      m[nn][0] = m[nn][1] = -INFINITY;
+      l[nn][0] = l[nn][1] = 0.f;
+    }
+
+    for (int t = ta; t < tb; ++t, ++n) {
+      if ((n & 1) != grp) continue;
+      const int st = n % kStages;
+      if (!bad && !warp_wait(&sm.full[st], (n / kStages) & 1)) {
+        if (lane == 0) record_error(p.err, kErrTimeoutAttn);
+        bad = true;
+      }
+      const int pos0 = (s.t0 + t) * kTile + quarter * 16;
+      if (((sm.valid[st] >> quarter) & 1u) && pos0 < s.hi && pos0 + 16 > s.lo) {
+        const uint8_t* sp = ring + st * kStageBytes;
+        const uint4 k0 = *reinterpret_cast<const uint4*>(sp + k_off);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(sp + k_off + 8 * kKvRowBytes);
+        const float ks0 = __half2float(*reinterpret_cast<const __half*>(sp + ks_off)) * p.scale_log2;
+        const float ks1 = __half2float(*reinterpret_cast<const __half*>(sp + ks_off + 16)) * p.scale_log2;
+        float vs0 = __half2float(*reinterpret_cast<const __half*>(sp + vs_off));
+        float vs1 = __half2float(*reinterpret_cast<const __half*>(sp + vs_off + 16));
+        const bool ok0 = pos0 + row0 >= s.lo && pos0 + row0 < s.hi;
+        const bool ok1 = pos0 + row0 + 8 >= s.lo && pos0 + row0 + 8 < s.hi;
+        if (!ok0) vs0 = 0.f;
+        if (!ok1) vs1 = 0.f;
+        float sc[NT][4];
+#pragma unroll
+        for (int nn = 0; nn < NT; ++nn) {
+          sc[nn][0] = sc[nn][2] = c0[nn][0];
+          sc[nn][1] = sc[nn][3] = c0[nn][1];
+        }
+        const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a[4] = {codes72(kw0[j] << 4), codes72(kw1[j] << 4), codes72(kw0[j]), codes72(kw1[j])};
+          const uint32_t b[4] = {codes72(kw0[j] >> 4), codes72(kw1[j] >> 4), codes72(kw0[j] >> 8),
+                                 codes72(kw1[j] >> 8)};
+#pragma unroll
+          for (int nn = 0; nn < NT; ++nn) {
+            mma_f16(sc[nn], a, qf[nn][4 * j], qf[nn][4 * j + 1]);
+            mma_f16(sc[nn], b, qf[nn][4 * j + 2], qf[nn][4 * j + 3]);
+          }
+        }
+        // scores in units of log2; what is masked is -inf whatever its scale holds
+        bool move = fmaxf(vs0, vs1) > vcap;
+#pragma unroll
+        for (int nn = 0; nn < NT; ++nn) {
+          sc[nn][0] = ok0 ? sc[nn][0] * ks0 : -INFINITY;
+          sc[nn][1] = ok0 ? sc[nn][1] * ks0 : -INFINITY;
+          sc[nn][2] = ok1 ? sc[nn][2] * ks1 : -INFINITY;
+          sc[nn][3] = ok1 ? sc[nn][3] * ks1 : -INFINITY;
+          move |= fmaxf(sc[nn][0], sc[nn][2]) > m[nn][0] + kSlack;
+          move |= fmaxf(sc[nn][1], sc[nn][3]) > m[nn][1] + kSlack;
+        }
+        if (__any_sync(0xffffffffu, move)) {
+          // new references: the largest score of each head, the largest v scale
+          float vm = fmaxf(fmaxf(vs0, vs1), vcap);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, x));
+          const float vf = vm > 0.f ? vcap / vm : 0.f;
+          vcap = vm;
+          vinv = vm > 0.f ? kWeightScale / vm : 0.f;
+#pragma unroll
+          for (int nn = 0; nn < NT; ++nn) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float mx = fmaxf(m[nn][k], fmaxf(sc[nn][k], sc[nn][k + 2]));
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+              const float f = m[nn][k] == -INFINITY ? 0.f : exp2_approx(m[nn][k] - mx);
+              m[nn][k] = mx;
+              l[nn][k] *= f;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                o[nn][i][k] *= f * vf;
+                o[nn][i][k + 2] *= f * vf;
+              }
+            }
+          }
+        }
+        uint32_t w0[NT], w1[NT];
+        const float v0 = vs0 * vinv, v1 = vs1 * vinv;
+#pragma unroll
+        for (int nn = 0; nn < NT; ++nn) {
+          const float ma = m[nn][0] == -INFINITY ? 0.f : m[nn][0], mb = m[nn][1] == -INFINITY ? 0.f : m[nn][1];
+          const float p0 = exp2_approx(sc[nn][0] - ma), p1 = exp2_approx(sc[nn][1] - mb);
+          const float p2 = exp2_approx(sc[nn][2] - ma), p3 = exp2_approx(sc[nn][3] - mb);
+          l[nn][0] += p0 + p2;
+          l[nn][1] += p1 + p3;
+          const __half2 a = __floats2half2_rn(p0 * v0, p1 * v0), b = __floats2half2_rn(p2 * v1, p3 * v1);
+          w0[nn] = transpose8x8(*reinterpret_cast<const uint32_t*>(&a));
+          w1[nn] = transpose8x8(*reinterpret_cast<const uint32_t*>(&b));
+        }
+        // values: lane (g, t4) holds dims [16 g, 16 g + 16) of its four tokens
+        const uint2 x0 = *reinterpret_cast<const uint2*>(sp + v_off + va * kKvRowBytes);
+        const uint2 x1 = *reinterpret_cast<const uint2*>(sp + v_off + vb * kKvRowBytes);
+        const uint2 x2 = *reinterpret_cast<const uint2*>(sp + v_off + (va + 8) * kKvRowBytes);
+        const uint2 x3 = *reinterpret_cast<const uint2*>(sp + v_off + (vb + 8) * kKvRowBytes);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // four dims: half word j of the 16 dims
+          const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+          const uint32_t y0 = __byte_perm(j < 2 ? x0.x : x0.y, j < 2 ? x1.x : x1.y, sel);
+          const uint32_t y1 = __byte_perm(j < 2 ? x2.x : x2.y, j < 2 ? x3.x : x3.y, sel);
+          const uint32_t a[4] = {hsub2(codes1032(y0), 0x64086408u), hsub2(codes72(y0), 0x54805480u),
+                                 hsub2(codes1032(y1), 0x64086408u), hsub2(codes72(y1), 0x54805480u)};
+          const uint32_t z0 = y0 >> 8, z1 = y1 >> 8;
+          const uint32_t b[4] = {hsub2(codes1032(z0), 0x64086408u), hsub2(codes72(z0), 0x54805480u),
+                                 hsub2(codes1032(z1), 0x64086408u), hsub2(codes72(z1), 0x54805480u)};
+#pragma unroll
+          for (int nn = 0; nn < NT; ++nn) {
+            mma_f16(o[nn][2 * j], a, w0[nn], w1[nn]);      // dims 4 j (rows g), 4 j + 1 (rows g + 8)
+            mma_f16(o[nn][2 * j + 1], b, w0[nn], w1[nn]);  // dims 4 j + 2, 4 j + 3
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[st]);
+    }
+
+    // ---- the eight warps' parts of the segment
+#pragma unroll
+    for (int nn = 0; nn < NT; ++nn)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float v = l[nn][k];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+        if (g == 0) {
+          sm.m[warp][nn * 8 + 2 * t4 + k] = m[nn][k];
+          sm.l[warp][nn * 8 + 2 * t4 + k] = v;
+        }
+      }
+    named_barrier(1, kComputeThreads);
+    const long long item0 = before + static_cast<long long>(hc) * nt;  // the request and head's tiles in the sequence
+    const bool whole = ta == 0 && tb == nt;
+    const int c_first = cta_of_tile(item0, total, C);
+    const int parts = cta_of_tile(item0 + nt - 1, total, C) - c_first + 1;
+    const int slot = 2 * cta + (ta == 0 ? 1 : 0);
+    float* part = p.part + static_cast<size_t>(slot) * HB * (kHeadDim + 2);
+#pragma unroll
+    for (int nn = 0; nn < NT; ++nn) {
+      // 1. every warp's sums at the common reference
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kComputeWarps; ++w) mx = fmaxf(mx, sm.m[w][nn * 8 + 2 * t4 + k]);
+        const float f = m[nn][k] == -INFINITY ? 0.f : exp2_approx(m[nn][k] - mx) * (vcap * (1.0f / kWeightScale));
+        float* dst = sums + (warp * 8 + 2 * t4 + k) * kHeadPad;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int d = 4 * (i >> 1) + 2 * (i & 1);
+          dst[sum_offset(g, d)] = o[nn][i][k] * f;
+          dst[sum_offset(g, d + 1)] = o[nn][i][k + 2] * f;
+        }
+      }
+      named_barrier(1, kComputeThreads);
+      // 2. added over the warps: this thread takes head `warp`, dims 16 (lane % 8) + 4 (lane / 8) + 0..3
+      const int hh = nn * 8 + warp;
+      const int gg = lane & 7, d4 = lane >> 3;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      float mx = -INFINITY, ls = 0.f;
+#pragma unroll
+      for (int w = 0; w < kComputeWarps; ++w) {
+        const float* src = sums + (w * 8 + warp) * kHeadPad;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] += src[sum_offset(gg, 4 * d4 + k)];
+        mx = fmaxf(mx, sm.m[w][hh]);
+      }
+#pragma unroll
+      for (int w = 0; w < kComputeWarps; ++w)
+        if (sm.m[w][hh] != -INFINITY) ls += sm.l[w][hh] * exp2_approx(sm.m[w][hh] - mx);
+      if (hh < heads) {
+        const int dim = 16 * gg + 4 * d4;
+        if (whole) {
+          const float inv = ls > 0.f ? 1.0f / ls : 0.f;
+          const __half2 a = __floats2half2_rn(acc[0] * inv, acc[1] * inv);
+          const __half2 b = __floats2half2_rn(acc[2] * inv, acc[3] * inv);
+          *reinterpret_cast<uint2*>(p.Y + (static_cast<size_t>(r) * p.Hq + q0 + hh) * kHeadDim + dim) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+        } else {
+          *reinterpret_cast<float4*>(part + hh * kHeadDim + dim) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          if (lane == 0) {
+            part[HB * kHeadDim + hh] = mx;
+            part[HB * kHeadDim + HB + hh] = ls;
+          }
+        }
+      }
+      if (nn + 1 < NT) named_barrier(1, kComputeThreads);
+    }
+    if (!whole) {
+      // 3. the CTA that arrives last joins the parts, in the order of the CTAs
+      __threadfence();
+      named_barrier(1, kComputeThreads);
+      if (tid == 0) sm.join = atomicInc(&p.count[c_first], unsigned(parts - 1)) == unsigned(parts - 1);
+      named_barrier(1, kComputeThreads);
+      if (sm.join) {
+        __threadfence();
+        const size_t stride = static_cast<size_t>(HB) * (kHeadDim + 2);
+        for (int hh = warp; hh < heads; hh += kComputeWarps) {
+          float mx = -INFINITY;
+          for (int c = 0; c < parts; ++c)
+            mx = fmaxf(mx, __ldcg(p.part + (2 * (c_first + c) + (c == 0)) * stride + HB * kHeadDim + hh));
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          float ls = 0.f;
+          for (int c = 0; c < parts; ++c) {
+            const float* src = p.part + (2 * (c_first + c) + (c == 0)) * stride;
+            const float mc = __ldcg(src + HB * kHeadDim + hh);
+            const float f = mc == -INFINITY ? 0.f : exp2_approx(mc - mx);
+            ls += __ldcg(src + HB * kHeadDim + HB + hh) * f;
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + hh * kHeadDim) + lane);
+            acc.x += v.x * f;
+            acc.y += v.y * f;
+            acc.z += v.z * f;
+            acc.w += v.w * f;
+          }
+          const float inv = ls > 0.f ? 1.0f / ls : 0.f;
+          const __half2 a = __floats2half2_rn(acc.x * inv, acc.y * inv);
+          const __half2 b = __floats2half2_rn(acc.z * inv, acc.w * inv);
+          *reinterpret_cast<uint2*>(p.Y + (static_cast<size_t>(r) * p.Hq + q0 + hh) * kHeadDim + 4 * lane) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+        }
+      }
+    }
+    pos += tb - ta;
+    // the next segment's writes to sm.m follow every warp's reads above
+    named_barrier(1, kComputeThreads);
+  }
+}
+
+template <int NT>
+constexpr size_t attn_smem() {
+  return size_t(kStages) * kStageBytes + size_t(kComputeWarps) * 8 * kHeadPad * sizeof(float);
+}
+
+// CTAs of a launch: two per SM with one tile of 8 queries, one with two (their
+// registers hold 16 queries' sums).
+int attn_nt(int G) { return G > 8 ? 2 : 1; }
+int attn_grid(int nt) { return sm_count() * (nt == 1 ? 2 : 1); }
+
+template <int NT>
+fq_status launch_attn(const AttnParams& p, cudaStream_t stream) {
+  auto kern = kv_attn_kernel<NT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(attn_smem<NT>())) != cudaSuccess)
+    return fail(FQ_ERR_CUDA, "cannot reserve %zu bytes of shared memory", attn_smem<NT>());
+  launch_pdl(kern, dim3(attn_grid(NT)), dim3(kAttnThreads), attn_smem<NT>(), stream, p);
+  return check_launch("kv_attn_kernel");
+}
+
+}  // namespace
+}  // namespace fq
+
+extern "C" {
+
+size_t fq_kv_attn_workspace_size(int R, int Hq, int H) {
+  if (R < 1 || R > fq::kMaxAttnR || H < 1 || H > 128 || Hq < H || Hq % H || Hq > 1024) return 0;
+  const int nt = fq::attn_nt(Hq / H);
+  return fq::sync_block_bytes() + size_t(2) * fq::attn_grid(nt) * 8 * nt * (fq::kHeadDim + 2) * sizeof(float);
+}
+
+fq_status fq_kv_attn(const uint16_t* Q, long long ldq, int R, int Hq, const int32_t* len, const int32_t* block_table,
+                     int max_pages, const fq_kv_cache* cache, float scale, int window, uint16_t* Y, void* workspace,
+                     size_t ws_bytes, void* stream) {
+  fq::clear_error();
+  const fq_status st = fq::check_kv_cache(cache);
+  if (st != FQ_OK) return st;
+  FQ_CHECK_ARG(R >= 1 && R <= fq::kMaxAttnR, "R = %d must lie in [1, %d]", R, fq::kMaxAttnR);
+  FQ_CHECK_ARG(Hq >= cache->H && Hq % cache->H == 0 && Hq <= 1024,
+               "Hq = %d must be a multiple of H = %d, at most 1024", Hq, cache->H);
+  FQ_CHECK_ARG(Q && Y && fq::aligned(Q, 16) && fq::aligned(Y, 16), "Q and Y must be non-NULL and 16-byte aligned");
+  FQ_CHECK_ARG(ldq >= static_cast<long long>(Hq) * fq::kHeadDim && ldq % 8 == 0,
+               "ldq = %lld must be a multiple of 8 and at least Hq * 128 = %d", ldq, Hq * fq::kHeadDim);
+  FQ_CHECK_ARG(len && block_table && fq::aligned(len, 4) && fq::aligned(block_table, 4),
+               "len and block_table must be non-NULL and 4-byte aligned");
+  FQ_CHECK_ARG(max_pages >= 1 && static_cast<long long>(max_pages) * cache->page_size < (1ll << 31),
+               "max_pages = %d: at least 1, and fewer than 2^31 tokens", max_pages);
+  FQ_CHECK_ARG(window >= 0, "window = %d must not be negative", window);
+  FQ_CHECK_ARG(scale == scale && scale - scale == 0.f, "scale must be finite");
+  const size_t need = fq_kv_attn_workspace_size(R, Hq, cache->H);
+  if (!workspace || ws_bytes < need || !fq::aligned(workspace, 256))
+    return fq::fail(FQ_ERR_INVALID, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, ws_bytes);
+  unsigned* err = fq::device_error_word();
+  if (!err) return fq::fail(FQ_ERR_CUDA, "device error word unavailable");
+  fq::AttnParams p{};
+  p.Q = reinterpret_cast<const __half*>(Q);
+  p.ldq = ldq;
+  p.R = R;
+  p.Hq = Hq;
+  p.G = Hq / cache->H;
+  const int nt = fq::attn_nt(p.G);
+  p.chunks = (p.G + 8 * nt - 1) / (8 * nt);
+  p.len = len;
+  p.table = block_table;
+  p.max_pages = max_pages;
+  p.kv = fq::kv_view(cache);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.window = window;
+  p.Y = reinterpret_cast<__half*>(Y);
+  p.count = static_cast<unsigned*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + fq::sync_block_bytes());
+  p.err = err;
+  return nt == 1 ? fq::launch_attn<1>(p, static_cast<cudaStream_t>(stream))
+                 : fq::launch_attn<2>(p, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -7,6 +7,7 @@ arithmetic runs in the library's CUDA kernels; there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -65,6 +66,53 @@ class Transform:
         return t
 
 
+class _KVCache(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("H", ctypes.c_int)]
+
+
+KV_TOKEN_BYTES = 132  # per token and head: K and V codes (64 bytes each), two fp16 scales
+
+
+@dataclass
+class KVCache:
+    """A paged INT4 key/value cache: pool uint8 [num_pages, H, page_size * 132]
+    (the bytes of a page and head: see fq_kv_cache in fq.h).  Make an empty one
+    with kv_cache()."""
+    pool: torch.Tensor
+
+    @property
+    def num_pages(self) -> int:
+        return self.pool.shape[0]
+
+    @property
+    def heads(self) -> int:
+        return self.pool.shape[1]
+
+    @property
+    def page_size(self) -> int:
+        return self.pool.shape[2] // KV_TOKEN_BYTES
+
+    def views(self):
+        """(K codes [P, H, page, 64], V codes, K scales fp16 [P, H, page], V scales): views of the pool."""
+        n = self.page_size
+        parts = self.pool.split([64 * n, 64 * n, 2 * n, 2 * n], dim=-1)
+        kq, vq = (x.unflatten(-1, (n, 64)) for x in parts[:2])
+        ks, vs = (x.view(torch.float16) for x in parts[2:])
+        return kq, vq, ks, vs
+
+    def as_c(self) -> _KVCache:
+        _check(self.pool, torch.uint8, "pool")
+        if self.pool.dim() != 3 or self.pool.shape[2] % KV_TOKEN_BYTES:
+            raise ValueError("pool must be [num_pages, H, page_size * 132]")
+        return _KVCache(self.pool.data_ptr(), self.num_pages, self.page_size, self.heads)
+
+
+def kv_cache(num_pages: int, heads: int, page_size: int, device="cuda") -> KVCache:
+    """An empty cache of num_pages pages of page_size (16, 32, 64 or 128) tokens."""
+    return KVCache(torch.zeros(num_pages, heads, page_size * KV_TOKEN_BYTES, dtype=torch.uint8, device=device))
+
+
 def qparams(gran: int = ROW, alpha: float = 1.0, bits: int = 4, zero_point: int = 8,
             group_size: int = GROUP_SIZE) -> QParams:
     return QParams(bits, zero_point, gran, group_size, alpha)
@@ -82,7 +130,8 @@ def lib():
         raise FqError(FQ_ERR_CUDA, f"{LIB_PATH} is missing: build it with python -m int4_linear_b200.build")
     L = ctypes.CDLL(LIB_PATH)
     vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
-    qp, tp = ctypes.POINTER(QParams), ctypes.POINTER(_Transform)
+    ll = ctypes.c_longlong
+    qp, tp, kc = ctypes.POINTER(QParams), ctypes.POINTER(_Transform), ctypes.POINTER(_KVCache)
     sigs = {
         "fq_quant_weight": [vp, i, i, qp, tp, vp, vp, vp, vp],
         "fq_quant_act": [vp, i, i, qp, tp, vp, vp, vp, vp],
@@ -95,6 +144,11 @@ def lib():
         "fq_ternary_linear": [vp, i, i, vp, vp, vp, i, vp, vp],
         "fq_quant_kv": [vp, i, i, vp, ctypes.c_float, vp, vp, vp],
         "fq_ternary_pack": [vp, i, i, vp, vp],
+        "fq_kv_plan": [vp, vp, i, i, vp, i, vp, i, vp, vp, vp, vp, i, vp, vp],
+        "fq_kv_write": [vp, ll, vp, ll, i, vp, ctypes.c_float, ctypes.c_float, kc, vp],
+        "fq_kv_store": [vp, vp, vp, vp, i, vp, kc, vp],
+        "fq_kv_read": [kc, vp, i, vp, vp, vp],
+        "fq_kv_attn": [vp, ll, i, i, vp, vp, i, kc, ctypes.c_float, i, vp, vp, sz, vp],
         "fq_check_device_error": [vp],
         "fq_debug_wait_timeout": [ctypes.c_uint, vp],
     }
@@ -106,6 +160,8 @@ def lib():
         f = getattr(L, name)
         f.argtypes = [i, i, i, i]
         f.restype = sz
+    L.fq_kv_attn_workspace_size.argtypes = [i, i, i]
+    L.fq_kv_attn_workspace_size.restype = sz
     L.fq_status_string.argtypes = [ctypes.c_int]
     L.fq_status_string.restype = ctypes.c_char_p
     L.fq_last_error.argtypes = []
@@ -139,6 +195,46 @@ def _s(stream):
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+@contextlib.contextmanager
+def _on(stream, *tensors):
+    """The device of `tensors` (all on one) made current and, where a stream is given, that
+    stream, so that what is allocated inside belongs to the stream that uses it.  Yields the
+    stream's handle."""
+    dev = {t.device for t in tensors if t is not None}
+    if len(dev) != 1:
+        raise ValueError(f"the tensors lie on {len(dev)} devices, not on one")
+    dev = dev.pop()
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield torch.cuda.current_stream(dev).cuda_stream
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(stream, device=dev)
+            elif stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _check_shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _check_rows(t, name, width):
+    """fp16 rows of `width` values, any distance apart: [T, width] or [T, H, 128] with dense rows.
+    Returns (T, the distance in elements)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float16:
+        raise ValueError(f"{name} must be torch.float16, got {t.dtype}")
+    if t.dim() < 2 or t.shape[0] < 1 or t[0].numel() != width:
+        raise ValueError(f"{name} must have rows of {width} values, got shape {tuple(t.shape)}")
+    if not t[0].is_contiguous():
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.shape[0], (t.stride(0) if t.shape[0] > 1 else width)
 
 
 def _scales_out(gran, rows, k, dev, zero_point=8):
@@ -303,6 +399,124 @@ def fq_quant_kv(KV, P_h, alpha: float = 1.0, Q=None, scales=None, stream=None):
     _raise(lib().fq_quant_kv(KV.data_ptr(), t, h, P_h.data_ptr(), alpha, Q.data_ptr(), scales.data_ptr(),
                              _s(stream)))
     return Q, scales
+
+
+def fq_kv_plan(lens, new_tokens, block_table, free_pages, pages_used, page_size: int, max_tokens: int,
+               lens_out=None, token_start=None, slots=None, pages_used_out=None, stream=None):
+    """Block tables and slots of one step from the request lengths: lens, new_tokens int32 [R],
+    block_table int32 [R, max_pages] (updated in place), free_pages int32 [F], pages_used int32 [1].
+    Returns (lens_out [R], token_start [R + 1], slots [max_tokens], pages_used_out [1])."""
+    for t, name in ((lens, "lens"), (new_tokens, "new_tokens"), (block_table, "block_table"),
+                    (free_pages, "free_pages"), (pages_used, "pages_used"), (lens_out, "lens_out"),
+                    (token_start, "token_start"), (slots, "slots"), (pages_used_out, "pages_used_out")):
+        _check(t, torch.int32, name)
+    r = lens.shape[0]
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [R, max_pages]")
+    _check_shape(new_tokens, (r,), "new_tokens")
+    _check_shape(block_table, (r, block_table.shape[1]), "block_table")
+    _check_shape(pages_used, (1,), "pages_used")
+    with _on(stream, lens, new_tokens, block_table, free_pages, pages_used, lens_out, token_start, slots,
+             pages_used_out) as s:
+        dev = lens.device
+        lens_out = torch.empty(r, dtype=torch.int32, device=dev) if lens_out is None else lens_out
+        token_start = torch.empty(r + 1, dtype=torch.int32, device=dev) if token_start is None else token_start
+        slots = torch.empty(max_tokens, dtype=torch.int32, device=dev) if slots is None else slots
+        pages_used_out = torch.empty(1, dtype=torch.int32, device=dev) if pages_used_out is None else pages_used_out
+        _check_shape(lens_out, (r,), "lens_out")
+        _check_shape(token_start, (r + 1,), "token_start")
+        _check_shape(slots, (max_tokens,), "slots")
+        _check_shape(pages_used_out, (1,), "pages_used_out")
+        _raise(lib().fq_kv_plan(lens.data_ptr(), new_tokens.data_ptr(), r, page_size, block_table.data_ptr(),
+                                block_table.shape[1], free_pages.data_ptr() or None, free_pages.numel(),
+                                pages_used.data_ptr(), lens_out.data_ptr(), token_start.data_ptr(),
+                                slots.data_ptr() or None, max_tokens, pages_used_out.data_ptr(), s))
+    return lens_out, token_start, slots, pages_used_out
+
+
+def fq_kv_write(K, V, slots, cache: KVCache, alpha_k: float = 1.0, alpha_v: float = 1.0, stream=None):
+    """New keys and values (fp16 [T, H, 128] or [T, H * 128], rows any distance apart) into the
+    cache's slots (int32 [T], -1: skipped) as INT4."""
+    c = cache.as_c()
+    t, ldk = _check_rows(K, "K", c.H * 128)
+    tv, ldv = _check_rows(V, "V", c.H * 128)
+    _check(slots, torch.int32, "slots")
+    _check_shape(slots, (t,), "slots")
+    if tv != t:
+        raise ValueError(f"K has {t} rows, V {tv}")
+    with _on(stream, K, V, slots, cache.pool) as s:
+        _raise(lib().fq_kv_write(K.data_ptr(), ldk, V.data_ptr(), ldv, t, slots.data_ptr(), alpha_k, alpha_v,
+                                 ctypes.byref(c), s))
+
+
+def fq_kv_store(Kq, Ks, Vq, Vs, slots, cache: KVCache, stream=None):
+    """Codes and scales that fq_quant_kv returned (uint8 [T, H * 64], fp16 [T, H]) into the cache's slots."""
+    c = cache.as_c()
+    t = slots.shape[0]
+    for x, dt, w, name in ((Kq, torch.uint8, c.H * 64, "Kq"), (Ks, torch.float16, c.H, "Ks"),
+                           (Vq, torch.uint8, c.H * 64, "Vq"), (Vs, torch.float16, c.H, "Vs")):
+        _check(x, dt, name)
+        _check_shape(x, (t, w), name)
+    _check(slots, torch.int32, "slots")
+    with _on(stream, Kq, Ks, Vq, Vs, slots, cache.pool) as s:
+        _raise(lib().fq_kv_store(Kq.data_ptr(), Ks.data_ptr(), Vq.data_ptr(), Vs.data_ptr(), t, slots.data_ptr(),
+                                 ctypes.byref(c), s))
+
+
+def fq_kv_read(cache: KVCache, slots, K=None, V=None, stream=None):
+    """The cached tokens of `slots` (int32 [T]) as fp16 (K, V), each [T, H, 128]; zeros where a slot is no place."""
+    c = cache.as_c()
+    _check(slots, torch.int32, "slots")
+    shape = (slots.shape[0], c.H, 128)
+    with _on(stream, slots, cache.pool, K, V) as s:
+        K = torch.empty(shape, dtype=torch.float16, device=slots.device) if K is None else K
+        V = torch.empty(shape, dtype=torch.float16, device=slots.device) if V is None else V
+        for x, name in ((K, "K"), (V, "V")):
+            _check(x, torch.float16, name)
+            _check_shape(x, shape, name)
+        _raise(lib().fq_kv_read(ctypes.byref(c), slots.data_ptr(), shape[0], K.data_ptr(), V.data_ptr(), s))
+    return K, V
+
+
+def fq_kv_attn_workspace_size(R: int, Hq: int, H: int) -> int:
+    return lib().fq_kv_attn_workspace_size(R, Hq, H)
+
+
+def fq_kv_attn_workspace(R: int, Hq: int, H: int, device="cuda"):
+    """A zeroed workspace for fq_kv_attn.  Calls that may overlap on the GPU need one each."""
+    with torch.cuda.device(device):
+        return torch.zeros(fq_kv_attn_workspace_size(R, Hq, H), dtype=torch.uint8, device=device)
+
+
+def fq_kv_attn(Q, lens, block_table, cache: KVCache, scale: float | None = None, window: int = 0, Y=None,
+               workspace=None, stream=None):
+    """Attention of one new token per request over the paged cache: Q fp16 [R, Hq, 128] or
+    [R, Hq * 128] (rows any distance apart), lens int32 [R], block_table int32 [R, max_pages];
+    scale defaults to 128^-0.5, window > 0 keeps the last `window` tokens.  Returns Y fp16 [R, Hq * 128]."""
+    c = cache.as_c()
+    _check(lens, torch.int32, "lens")
+    _check(block_table, torch.int32, "block_table")
+    r = lens.shape[0]
+    if block_table.dim() != 2 or Q.dim() < 2:
+        raise ValueError("block_table must be [R, max_pages] and Q [R, Hq, 128] or [R, Hq * 128]")
+    _check_shape(block_table, (r, block_table.shape[1]), "block_table")
+    width = Q[0].numel() if Q.shape[0] else 0
+    rows, ldq = _check_rows(Q, "Q", width)
+    if rows != r or width < 128 or width % 128:
+        raise ValueError(f"Q must have {r} rows of Hq * 128 values, got shape {tuple(Q.shape)}")
+    hq = width // 128
+    with _on(stream, Q, lens, block_table, cache.pool, Y, workspace) as s:
+        Y = torch.empty(r, hq * 128, dtype=torch.float16, device=Q.device) if Y is None else Y
+        _check(Y, torch.float16, "Y")
+        if Y.numel() != r * hq * 128:
+            raise ValueError(f"Y must hold {r} x {hq * 128} values, got shape {tuple(Y.shape)}")
+        if workspace is None:
+            workspace = fq_kv_attn_workspace(r, hq, c.H, Q.device)
+        _check(workspace, torch.uint8, "workspace")
+        _raise(lib().fq_kv_attn(Q.data_ptr(), ldq, r, hq, lens.data_ptr(), block_table.data_ptr(),
+                                block_table.shape[1], ctypes.byref(c), 128 ** -0.5 if scale is None else scale,
+                                window, Y.data_ptr(), workspace.data_ptr(), workspace.numel(), s))
+    return Y
 
 
 def fq_ternary_pack(T, Tq=None, stream=None):
