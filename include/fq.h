@@ -383,6 +383,60 @@ fq_status fq_kv_attn(const uint16_t* Q, long long ldq, int R, int Hq, const int3
                      size_t ws_bytes, void* stream);
 size_t fq_kv_attn_workspace_size(int R, int Hq, int H);
 
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (E2M1 codes, one scale per block along K)
+ * ------------------------------------------------------------------------
+ * Codes: sign and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0..7; bit 3 is the
+ * sign), two per byte, element 2j in bits 0-3 of byte j.
+ * Scales: one byte per row and block, in tiles of 128 rows x 4 blocks (512
+ * bytes), the tiles of one row block consecutive along K: scale (r, b) is byte
+ *   ((r / 128) * (B / 4) + b / 4) * 512 + (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4
+ * with B = K / block; rows are padded to a multiple of 128 (the padding bytes
+ * are not written and have no effect). */
+typedef enum {
+  FQ_MXFP4 = 0, /* blocks of 32, E8M0 scale 2^e, e = floor(log2 max|v|) - 2 (max = 0: e = -127) */
+  FQ_NVFP4 = 1  /* blocks of 16, E4M3 scale s = e4m3(max|v| / (6 g)), saturated at 448, with a
+                   float32 scale g per tensor */
+} fq_mx_format;
+
+/* Bytes of the scales of a [rows, K] tensor, padding included (0 for sizes out of range). */
+size_t fq_mx_scale_bytes(int rows, int K, fq_mx_format fmt);
+
+/* Quantization: X fp16, R rows of K values, ldx elements apart (>= K, a
+ * multiple of 8; rows 16-byte aligned); g device float32 [1], positive (FQ_NVFP4) or NULL
+ * (g = 1; FQ_MXFP4 takes NULL only).  Every code is E2M1 round-to-nearest, ties to the even
+ * code, saturated at 6, of v / d with d = 2^e (FQ_MXFP4) or the float32
+ * product s g (FQ_NVFP4, a float32 division; 6 g and max / (6 g) are float32 too; codes 0
+ * when s = 0).  A block that holds Inf or NaN gets a NaN scale (0xFF, 0x7F) and codes 0, so that the
+ * outputs it enters are NaN.
+ * Q uint8 [R, K/2], S uint8 [fq_mx_scale_bytes] (both 16-byte aligned).
+ * K a multiple of 128 in [128, 65536].  One launch. */
+fq_status fq_mx_quant(const uint16_t* X, long long ldx, int R, int K, fq_mx_format fmt, const float* g, uint8_t* Q,
+                      uint8_t* S, void* stream);
+
+/* The values back: X fp16 [R, K] (16-byte aligned) = fp16(code * d), d as above
+ * and the product in float32. */
+fq_status fq_mx_dequant(const uint8_t* Q, const uint8_t* S, int R, int K, fq_mx_format fmt, const float* g,
+                        uint16_t* X, void* stream);
+
+/* Block-scaled product: Y fp16 [M, N] (16-byte aligned) = fp16(acc * (g_x * g_w)),
+ * acc = sum over blocks of (s_x s_w sum of code products), in float32 on the
+ * tensor cores; g_x, g_w device float32 [1] or NULL (1).  Xq [M, K/2], Wq [N, K/2] and their
+ * scales as fq_mx_quant writes them.  M >= 1, N % 8 == 0, K a multiple of 128 in [128, 65536].
+ * workspace: fq_mx_gemm_workspace_size() bytes, 256-byte aligned, by the rule of
+ * fq_w4a4_gemm's workspace (may be NULL when that size is 0). */
+fq_status fq_mx_gemm(const uint8_t* Xq, const uint8_t* Sx, const float* g_x, const uint8_t* Wq, const uint8_t* Sw,
+                     const float* g_w, int M, int N, int K, fq_mx_format fmt, uint16_t* Y, void* workspace,
+                     size_t ws_bytes, void* stream);
+
+/* The linear layer: fq_mx_quant of X (fp16 [M, K], rows ldx apart) into the
+ * workspace, then fq_mx_gemm, on one stream.  workspace: fq_mx_linear_workspace_size() bytes. */
+fq_status fq_mx_linear(const uint16_t* X, long long ldx, int M, int K, fq_mx_format fmt, const float* g_x,
+                       const uint8_t* Wq, const uint8_t* Sw, const float* g_w, int N, uint16_t* Y, void* workspace,
+                       size_t ws_bytes, void* stream);
+size_t fq_mx_gemm_workspace_size(int M, int N, int K, fq_mx_format fmt);
+size_t fq_mx_linear_workspace_size(int M, int N, int K, fq_mx_format fmt);
+
 /* Scratch sizes in bytes (0 when none is needed).  gran as in the calls. */
 size_t fq_gemm_workspace_size(int M, int N, int K, fq_gran gran);
 size_t fq_linear_workspace_size(int M, int N, int K, fq_gran gran);

@@ -12,8 +12,9 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfq.so")
-SOURCES = ["abi.cu", "quant.cu", "quant_int.cu", "gemm.cu", "linear.cu", "ternary.cu", "kv_cache.cu", "kv_attn.cu"]
-HEADERS = ["fq_device.cuh", "fq_host.h", "kv_cache.cuh", os.path.join("..", "..", "include", "fq.h")]
+SOURCES = ["abi.cu", "quant.cu", "quant_int.cu", "gemm.cu", "linear.cu", "ternary.cu", "kv_cache.cu", "kv_attn.cu",
+           "mx.cu", "mx_gemm.cu"]
+HEADERS = ["fq_device.cuh", "fq_host.h", "kv_cache.cuh", "mx.cuh", os.path.join("..", "..", "include", "fq.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -1,0 +1,558 @@
+// Block-scaled product of microscaled 4-bit operands on the tensor cores
+// (tcgen05.mma kind::mxf4 / kind::mxf4nvf4 .block_scale), and the linear layer.
+//
+//   y[m][n] = fp16(g_x g_w sum_b s_x[m][b] s_w[n][b] sum_{k in b} x[m][k] w[n][k])
+//
+// The weights are the 128-row operand (tensor-memory lanes), the tokens the N
+// operand (BN = 16..256 columns), so that few tokens still fill the lanes. One CTA per SM:
+// warp 0 brings stages of 256 values along K (128 bytes per row: one swizzle
+// row) and their scales, which lie in memory as the 512-byte tiles that
+// tcgen05.cp spreads over tensor memory; one thread of warp 1 issues the scale copies and
+// the four MMAs of a stage; warps 4-7 drain finished tiles. A copy of scales is
+// ordered before the MMAs issued after it, and every stage has its own scale
+// columns, so the stage's barriers guard both.
+//
+// Work: whole tiles dealt to the CTAs in turn, or, where the tiles do not fill
+// the SMs evenly and K is what there is to divide, equal contiguous parts of
+// the (tile, stage) sequence; the CTA that arrives last at a divided tile adds
+// the float32 parts in the CTAs' order.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "fq_device.cuh"
+#include "fq_host.h"
+#include "mx.cuh"
+
+namespace fq {
+
+size_t sync_block_bytes();
+
+namespace {
+
+constexpr int kStageK = 256;                    // values along K per stage
+constexpr int kRowB = kStageK / 2;              // 128 bytes per row
+constexpr int kTileN = 128;                     // weight rows per tile
+constexpr int kMxGemmThreads = 256;
+constexpr int kStoreRows = 16;                  // tokens per output block
+constexpr int kStoreBytes = kStoreRows * 32 * 2;  // one warp's 16 x 32 outputs
+
+struct MxGemmParams {
+  const uint8_t *Sx, *Sw;
+  const float *gx, *gw;
+  int M, N, K;
+  int mt, tiles, ks;       // token tiles, tiles, stages per tile
+  int split;               // 1: equal parts of the (tile, stage) sequence
+  float* part;             // [2 * CTAs][BN][128]
+  unsigned* count;
+  unsigned* err;
+};
+
+template <int FMT, int BN>
+struct MxCfg {
+  static constexpr int SB = FMT == FQ_NVFP4 ? 4 : 2;      // scale tiles along K per stage
+  static constexpr int NBT = (BN + 127) / 128;            // scale tiles along the tokens
+  static constexpr int A_BYTES = kTileN * kRowB, B_BYTES = BN * kRowB;
+  static constexpr int SA_BYTES = SB * kMxTileBytes, SX_BYTES = SB * NBT * kMxTileBytes;
+  static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES + SX_BYTES;
+  static constexpr int AB = BN <= 128 ? 2 : 1;            // accumulators
+  static constexpr int ACC = BN < 32 ? 32 : BN;           // columns of one
+  static constexpr int SF0 = AB * ACC;                    // first scale column
+  static constexpr int SFA = SB * 4, SFX = SB * 4 * NBT;  // scale columns per stage
+  static constexpr int OUT = 8 * kStoreBytes;             // two output blocks per epilogue warp
+  static constexpr int BUDGET = 227 * 1024 - 1024 - OUT - 512;
+  static constexpr int S0 = BUDGET / STAGE;
+  static constexpr int S1 = (512 - SF0) / (SFA + SFX);
+  static constexpr int S = S0 < S1 ? (S0 < 12 ? S0 : 12) : (S1 < 12 ? S1 : 12);
+  // B's tile must start on a swizzle atom: A and B first, scales behind them
+  static constexpr int OFF_SA = S * (A_BYTES + B_BYTES);
+  static constexpr int OFF_OUT = OFF_SA + S * (SA_BYTES + SX_BYTES);
+  static constexpr int OFF_BAR = OFF_OUT + OUT;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static_assert((A_BYTES + B_BYTES) % 1024 == 0 && A_BYTES % 1024 == 0, "swizzle atoms");
+  static_assert(SF0 + S * (SFA + SFX) <= 512, "tensor memory");
+  static_assert(SMEM <= 227 * 1024 && (2 * S + 5) * 8 + 8 <= 256, "shared memory");
+};
+
+// 32 rows of 16 bytes (8-row groups 128 bytes apart, no swizzle) -> 4 columns of 32
+// lanes, repeated in each quarter of the lanes.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
+  const uint64_t d = uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(128u >> 4) << 32) | (uint64_t(1) << 46);
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+// Instruction descriptor of kind::mxf4 / mxf4nvf4: A = B = E2M1 K-major, M = 128, N = n,
+// scale type E8M0 or E4M3, scale byte (0 or 2) of both operands' 32-bit columns.
+template <int FMT>
+__host__ __device__ constexpr uint32_t idesc_mx(int n, uint32_t sf) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | ((FMT == FQ_MXFP4 ? 1u : 0u) << 23) |
+         (uint32_t(128 >> 4) << 24) | (sf << 29);
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                       uint32_t accumulate) {
+  if (FMT == FQ_MXFP4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+
+// This CTA's segments: (tile, stages [k0, k1)), the same sequence for every role.
+struct MxWalk {
+  long long u, u1;
+  int ks, step, split;
+  int tile, k0, k1;
+  __device__ __forceinline__ MxWalk(const MxGemmParams& p, int cta, int ctas) : ks(p.ks), step(ctas), split(p.split) {
+    const long long total = static_cast<long long>(p.tiles) * p.ks;
+    if (split) {
+      u = total * cta / ctas;
+      u1 = total * (cta + 1) / ctas;
+    } else {
+      u = cta;
+      u1 = p.tiles;
+    }
+  }
+  __device__ __forceinline__ bool next() {
+    if (u >= u1) return false;
+    if (split) {
+      tile = int(u / ks);
+      k0 = int(u % ks);
+      k1 = int(min(static_cast<long long>(ks), k0 + (u1 - u)));
+      u += k1 - k0;
+    } else {
+      tile = int(u);
+      k0 = 0;
+      k1 = ks;
+      u += step;
+    }
+    return true;
+  }
+};
+
+template <int FMT, int BN>
+__global__ void __launch_bounds__(kMxGemmThreads, 1)
+    mx_gemm_kernel(const MxGemmParams p, const __grid_constant__ CUtensorMap tmW,
+                   const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY) {
+  using C = MxCfg<FMT, BN>;
+  constexpr int S = C::S;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;      // [2]
+  uint64_t* acc_empty = acc_full + 2;  // [2]
+  uint64_t* done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  int* join = reinterpret_cast<int*>(done + 1) + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 4);
+    }
+    mbar_init(done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int kbt = p.K / kStageK * C::SB + (p.K % kStageK ? C::SB / 2 : 0);  // scale tiles along K
+  MxWalk walk(p, blockIdx.x, gridDim.x);
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tensormap(&tmW);
+      prefetch_tensormap(&tmX);
+      const uint64_t pol = policy_evict_last();  // the tokens are read by every CTA
+      const int rt = (p.M + kMxTileRows - 1) / kMxTileRows;
+      int it = 0;
+      bool ok = true;
+      while (ok && walk.next()) {
+        const int nt = walk.tile / p.mt, mt = walk.tile % p.mt;
+        const int nb = min(C::NBT, rt - mt * BN / kMxTileRows);
+        for (int k = walk.k0; k < walk.k1; ++k, ++it) {
+          const int s = it % S;
+          if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1)) {
+            record_error(p.err, kErrTimeoutProducer);
+            ok = false;
+            break;
+          }
+          const uint32_t sfb = min(C::SB, kbt - k * C::SB) * kMxTileBytes;  // the last stage may be half a stage
+          mbar_arrive_expect_tx(&full[s], C::A_BYTES + C::B_BYTES + sfb * (1 + nb));
+          uint8_t* ab = smem + s * (C::A_BYTES + C::B_BYTES);
+          uint8_t* sf = smem + C::OFF_SA + s * (C::SA_BYTES + C::SX_BYTES);
+          tma_load_2d(ab, &tmW, &full[s], k * kRowB, nt * kTileN);
+          tma_load_2d_hint(ab + C::A_BYTES, &tmX, &full[s], k * kRowB, mt * BN, pol);
+          bulk_load(sf, p.Sw + (size_t(nt) * kbt + size_t(k) * C::SB) * kMxTileBytes, sfb, &full[s]);
+          for (int b = 0; b < nb; ++b)
+            bulk_load(sf + C::SA_BYTES * (1 + b),
+                      p.Sx + (size_t(mt * BN / kMxTileRows + b) * kbt + size_t(k) * C::SB) * kMxTileBytes, sfb,
+                      &full[s]);
+        }
+      }
+      // every copy has landed before the CTA may leave
+      for (int i = max(0, it - S); i < it; ++i)
+        if (!mbar_wait(&full[i % S], (i / S) & 1)) {
+          record_error(p.err, kErrTimeoutDrain);
+          break;
+        }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ scale copies and MMAs
+    if (lane == 0) {
+      int it = 0, seg = 0;
+      bool ok = true;
+      while (ok && walk.next()) {
+        const int buf = seg % C::AB;
+        if (!mbar_wait(&acc_empty[buf], ((seg / C::AB) & 1) ^ 1)) {
+          record_error(p.err, kErrTimeoutMma);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + uint32_t(buf * C::ACC);
+        for (int k = walk.k0; k < walk.k1; ++k, ++it) {
+          const int s = it % S;
+          if (!mbar_wait(&full[s], (it / S) & 1)) {
+            record_error(p.err, kErrTimeoutMma);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ab = smem_u32(smem + s * (C::A_BYTES + C::B_BYTES));
+          const uint32_t sf = smem_u32(smem + C::OFF_SA + s * (C::SA_BYTES + C::SX_BYTES));
+          const uint32_t ta = tmem + uint32_t(C::SF0 + s * (C::SFA + C::SFX)), tx = ta + uint32_t(C::SFA);
+          const bool half = (k + 1) * kStageK > p.K;  // 128 values in the last stage
+          const int sb = half ? C::SB / 2 : C::SB;
+#pragma unroll
+          for (int b = 0; b < C::SB; ++b) {
+            if (b >= sb) break;
+            copy_scales(ta + 4 * b, sf + b * kMxTileBytes);
+#pragma unroll
+            for (int j = 0; j < C::NBT; ++j)
+              copy_scales(tx + 4 * (b * C::NBT + j), sf + C::SA_BYTES * (1 + j) + b * kMxTileBytes);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (half && q >= 2) break;
+            const int b = FMT == FQ_NVFP4 ? q : q / 2;
+            constexpr uint32_t i0 = idesc_mx<FMT>(BN, 0), i2 = idesc_mx<FMT>(BN, 2);
+            mma_mx<FMT>(d, sdesc_k128_sw128(ab + 32 * q), sdesc_k128_sw128(ab + C::A_BYTES + 32 * q),
+                        FMT == FQ_MXFP4 && (q & 1) ? i2 : i0, ta + 4 * b, tx + 4 * b * C::NBT,
+                        uint32_t(k > walk.k0 || q > 0));
+          }
+          mma_commit(&empty[s]);
+        }
+        mma_commit(&acc_full[buf]);
+        ++seg;
+      }
+      // nothing issued may still run when tensor memory is freed
+      mma_commit(done);
+      if (!mbar_wait(done, 0)) record_error(p.err, kErrTimeoutDrain);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ finished tiles
+    const int w = warp & 3;  // lanes 32 w .. 32 w + 31: weight rows of the tile
+    const uint32_t lanes = uint32_t(32 * w) << 16;
+    uint8_t* out = smem + C::OFF_OUT + w * 2 * kStoreBytes;
+    const float g = (p.gx ? *p.gx : 1.0f) * (p.gw ? *p.gw : 1.0f);
+    int seg = 0, stored = 0;
+    bool bad = false;
+    // 16 tokens (columns col0..) of this warp's 32 rows: to shared memory as rows of tokens, out by one copy
+    auto emit = [&](int nt, int mt, int col0, const uint32_t(&h)[kStoreRows / 2]) {
+      const int x = nt * kTileN + 32 * w, y = mt * BN + col0;
+      if (x >= p.N || y >= p.M) return;
+      uint8_t* blk = out + (stored & 1) * kStoreBytes;
+      if (lane == 0) bulk_wait_group_read<1>();
+      __syncwarp();
+      __half* row = reinterpret_cast<__half*>(blk) + lane;
+#pragma unroll
+      for (int j = 0; j < kStoreRows / 2; ++j) {
+        const __half2 v = *reinterpret_cast<const __half2*>(&h[j]);
+        row[(2 * j) * 32] = __low2half(v);
+        row[(2 * j + 1) * 32] = __high2half(v);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(&tmY, blk, x, y);
+        bulk_commit_group();
+      }
+      ++stored;
+    };
+    auto pack = [&](float a, float b) {
+      const __half2 v = __floats2half2_rn(a * g, b * g);
+      return *reinterpret_cast<const uint32_t*>(&v);
+    };
+    constexpr int CH = BN < 32 ? 16 : 32;  // columns per tensor-memory load
+    while (walk.next()) {
+      const int nt = walk.tile / p.mt, mt = walk.tile % p.mt;
+      const int buf = seg % C::AB;
+      const uint32_t d = tmem + uint32_t(buf * C::ACC) + lanes;
+      if (!bad && !warp_wait(&acc_full[buf], (seg / C::AB) & 1)) {
+        if (lane == 0) record_error(p.err, kErrTimeoutEpilogue);
+        bad = true;
+      }
+      tc_fence_after();
+      ++seg;
+      if (walk.k0 == 0 && walk.k1 == p.ks) {
+        uint32_t h[BN / 2];
+#pragma unroll
+        for (int c = 0; c < BN; c += CH) {
+          uint32_t v[32];
+          if (CH == 32)
+            tmem_ld_32x32(d + c, v);
+          else
+            tmem_ld_32x16(d + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < CH / 2; ++j)
+            h[c / 2 + j] = pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+        }
+        // the accumulator goes back before the outputs are on their way
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        if (!bad) {
+#pragma unroll
+          for (int c = 0; c < BN; c += kStoreRows) {
+            uint32_t hh[kStoreRows / 2];
+#pragma unroll
+            for (int j = 0; j < kStoreRows / 2; ++j) hh[j] = h[c / 2 + j];
+            emit(nt, mt, c, hh);
+          }
+        }
+        continue;
+      }
+      // a part of a tile: float32 sums to this CTA's slot, [column][128]
+      const long long total = static_cast<long long>(p.tiles) * p.ks, t0 = static_cast<long long>(walk.tile) * p.ks;
+      const int G = gridDim.x;
+      const int c_first = int(((t0 + 1) * G - 1) / total);
+      const int parts = int(((t0 + p.ks) * G - 1) / total) - c_first + 1;
+      const size_t slot_floats = size_t(BN) * kTileN;
+      const int cols = min(BN, p.M - mt * BN);
+      float* dst = p.part + (2 * size_t(blockIdx.x) + (walk.k0 == 0 ? 1 : 0)) * slot_floats + 32 * w + lane;
+#pragma unroll
+      for (int c = 0; c < BN; c += CH) {
+        uint32_t v[32];
+        if (CH == 32)
+          tmem_ld_32x32(d + c, v);
+        else
+          tmem_ld_32x16(d + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+          if (c + j < cols) dst[size_t(c + j) * kTileN] = __uint_as_float(v[j]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      __threadfence();
+      named_barrier(1, 128);
+      if (threadIdx.x == 128) *join = atomicInc(&p.count[c_first], unsigned(parts - 1)) == unsigned(parts - 1);
+      named_barrier(1, 128);
+      const bool mine = *join && !bad;
+      if (mine) {
+        __threadfence();
+        for (int c = 0; c < cols; c += kStoreRows) {
+          float acc[kStoreRows];
+#pragma unroll
+          for (int j = 0; j < kStoreRows; ++j) acc[j] = 0.f;
+          for (int i = 0; i < parts; ++i) {
+            const float* src = p.part + (2 * size_t(c_first + i) + (i == 0)) * slot_floats + 32 * w + lane;
+#pragma unroll
+            for (int j = 0; j < kStoreRows; ++j)
+              if (c + j < cols) acc[j] += __ldcg(src + size_t(c + j) * kTileN);
+          }
+          uint32_t hh[kStoreRows / 2];
+#pragma unroll
+          for (int j = 0; j < kStoreRows / 2; ++j) hh[j] = pack(acc[2 * j], acc[2 * j + 1]);
+          emit(nt, mt, c, hh);
+        }
+      }
+      named_barrier(1, 128);  // join is read before the next tile's flag
+    }
+    if (lane == 0) bulk_wait_group<0>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Tokens per tile, tiles and whether K is divided, from the sizes alone.
+struct MxPlan {
+  int bn, mt, tiles, ks, split, grid;
+};
+
+MxPlan mx_plan(int M, int N, int K) {
+  MxPlan q;
+  const int sms = sm_count();
+  q.ks = (K + kStageK - 1) / kStageK;
+  const int nt = (N + kTileN - 1) / kTileN;
+  if (M <= 128) {
+    q.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  } else {
+    const long long t128 = static_cast<long long>(nt) * ((M + 127) / 128), t256 = static_cast<long long>(nt) * ((M + 255) / 256);
+    const long long w128 = (t128 + sms - 1) / sms, w256 = (t256 + sms - 1) / sms;
+    q.bn = w128 * 11 < w256 * 20 ? 128 : 256;
+  }
+  q.mt = (M + q.bn - 1) / q.bn;
+  q.tiles = nt * q.mt;
+  q.split = q.bn <= 64 || (q.tiles < sms && q.ks > 1);
+  const long long units = static_cast<long long>(q.tiles) * q.ks;
+  q.grid = int(std::min<long long>(sms, q.split ? units : q.tiles));
+  return q;
+}
+
+template <int FMT, int BN>
+fq_status launch_mx(const MxGemmParams& p, const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& y, int grid,
+                    cudaStream_t stream) {
+  using C = MxCfg<FMT, BN>;
+  auto kern = mx_gemm_kernel<FMT, BN>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return fail(FQ_ERR_CUDA, "cannot reserve %d bytes of shared memory", C::SMEM);
+  launch_pdl(kern, dim3(grid), dim3(kMxGemmThreads), C::SMEM, stream, p, w, x, y);
+  return check_launch("mx_gemm_kernel");
+}
+
+template <int FMT>
+fq_status launch_mx_bn(int bn, const MxGemmParams& p, const CUtensorMap& w, const CUtensorMap& x,
+                       const CUtensorMap& y, int grid, cudaStream_t stream) {
+  switch (bn) {
+    case 16: return launch_mx<FMT, 16>(p, w, x, y, grid, stream);
+    case 32: return launch_mx<FMT, 32>(p, w, x, y, grid, stream);
+    case 64: return launch_mx<FMT, 64>(p, w, x, y, grid, stream);
+    case 128: return launch_mx<FMT, 128>(p, w, x, y, grid, stream);
+    default: return launch_mx<FMT, 256>(p, w, x, y, grid, stream);
+  }
+}
+
+bool mx_sizes_ok(int M, int N, int K, fq_mx_format fmt) {
+  return M >= 1 && N >= 8 && N % 8 == 0 && K >= kGroup && K <= kMaxK && K % kGroup == 0 &&
+         (fmt == FQ_MXFP4 || fmt == FQ_NVFP4);
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace fq
+
+extern "C" {
+
+size_t fq_mx_gemm_workspace_size(int M, int N, int K, fq_mx_format fmt) {
+  if (!fq::mx_sizes_ok(M, N, K, fmt)) return 0;
+  const fq::MxPlan q = fq::mx_plan(M, N, K);
+  if (!q.split) return 0;
+  return fq::sync_block_bytes() + size_t(2) * q.grid * q.bn * fq::kTileN * sizeof(float);
+}
+
+size_t fq_mx_linear_workspace_size(int M, int N, int K, fq_mx_format fmt) {
+  if (!fq::mx_sizes_ok(M, N, K, fmt)) return 0;
+  return fq::up256(std::max(fq::sync_block_bytes(), fq_mx_gemm_workspace_size(M, N, K, fmt))) +
+         fq::up256(size_t(M) * (K / 2)) + fq_mx_scale_bytes(M, K, fmt);
+}
+
+fq_status fq_mx_gemm(const uint8_t* Xq, const uint8_t* Sx, const float* g_x, const uint8_t* Wq, const uint8_t* Sw,
+                     const float* g_w, int M, int N, int K, fq_mx_format fmt, uint16_t* Y, void* workspace,
+                     size_t ws_bytes, void* stream) {
+  fq::clear_error();
+  if (fmt != FQ_MXFP4 && fmt != FQ_NVFP4)
+    return fq::fail(FQ_ERR_UNSUPPORTED, "format %d is not provided", int(fmt));
+  FQ_CHECK_ARG(fq::mx_sizes_ok(M, N, K, fmt),
+               "sizes M = %d, N = %d, K = %d: M >= 1, N a multiple of 8, K a multiple of 128 in [128, %d]", M, N, K,
+               fq::kMaxK);
+  for (const void* q : {static_cast<const void*>(Xq), static_cast<const void*>(Sx), static_cast<const void*>(Wq),
+                        static_cast<const void*>(Sw), static_cast<const void*>(Y)})
+    FQ_CHECK_ARG(q && fq::aligned(q, 16), "Xq, Sx, Wq, Sw and Y must be non-NULL and 16-byte aligned");
+  FQ_CHECK_ARG(fq::aligned(g_x, 4) && fq::aligned(g_w, 4), "g_x and g_w must be 4-byte aligned");
+  FQ_CHECK_ARG(fmt == FQ_NVFP4 || (!g_x && !g_w), "FQ_MXFP4 has no tensor scales: g_x and g_w must be NULL");
+  const size_t need = fq_mx_gemm_workspace_size(M, N, K, fmt);
+  if (need && (!workspace || ws_bytes < need || !fq::aligned(workspace, 256)))
+    return fq::fail(FQ_ERR_INVALID, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, ws_bytes);
+  const fq::MxPlan q = fq::mx_plan(M, N, K);
+  FQ_CHECK_ARG(static_cast<long long>((N + 127) / 128) * q.mt < (1ll << 31), "M = %d and N = %d: too many tiles", M, N);
+  unsigned* err = fq::device_error_word();
+  if (!err) return fq::fail(FQ_ERR_CUDA, "device error word unavailable");
+  CUtensorMap w, x, y;
+  fq_status st = fq::make_tmap_2d(&w, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, N, K / 2, fq::kRowB, fq::kTileN,
+                                  CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == FQ_OK)
+    st = fq::make_tmap_2d(&x, Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, M, K / 2, fq::kRowB, q.bn,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == FQ_OK)
+    st = fq::make_tmap_2d(&y, Y, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, N, M, size_t(N) * 2, 32, fq::kStoreRows);
+  if (st != FQ_OK) return st;
+  fq::MxGemmParams p{};
+  p.Sx = Sx;
+  p.Sw = Sw;
+  p.gx = g_x;
+  p.gw = g_w;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.mt = q.mt;
+  p.tiles = q.tiles;
+  p.ks = q.ks;
+  p.split = q.split;
+  p.count = static_cast<unsigned*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + fq::sync_block_bytes());
+  p.err = err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return fmt == FQ_MXFP4 ? fq::launch_mx_bn<FQ_MXFP4>(q.bn, p, w, x, y, q.grid, s)
+                         : fq::launch_mx_bn<FQ_NVFP4>(q.bn, p, w, x, y, q.grid, s);
+}
+
+fq_status fq_mx_linear(const uint16_t* X, long long ldx, int M, int K, fq_mx_format fmt, const float* g_x,
+                       const uint8_t* Wq, const uint8_t* Sw, const float* g_w, int N, uint16_t* Y, void* workspace,
+                       size_t ws_bytes, void* stream) {
+  fq::clear_error();
+  if (fmt != FQ_MXFP4 && fmt != FQ_NVFP4)
+    return fq::fail(FQ_ERR_UNSUPPORTED, "format %d is not provided", int(fmt));
+  FQ_CHECK_ARG(fq::mx_sizes_ok(M, N, K, fmt),
+               "sizes M = %d, N = %d, K = %d: M >= 1, N a multiple of 8, K a multiple of 128 in [128, %d]", M, N, K,
+               fq::kMaxK);
+  // everything the second launch checks, before the first
+  FQ_CHECK_ARG(Wq && Sw && Y && fq::aligned(Wq, 16) && fq::aligned(Sw, 16) && fq::aligned(Y, 16),
+               "Wq, Sw and Y must be non-NULL and 16-byte aligned");
+  FQ_CHECK_ARG(fq::aligned(g_x, 4) && fq::aligned(g_w, 4), "g_x and g_w must be 4-byte aligned");
+  FQ_CHECK_ARG(fmt == FQ_NVFP4 || (!g_x && !g_w), "FQ_MXFP4 has no tensor scales: g_x and g_w must be NULL");
+  const size_t need = fq_mx_linear_workspace_size(M, N, K, fmt);
+  if (!workspace || ws_bytes < need || !fq::aligned(workspace, 256))
+    return fq::fail(FQ_ERR_INVALID, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, ws_bytes);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  const size_t gws = fq::up256(std::max(fq::sync_block_bytes(), fq_mx_gemm_workspace_size(M, N, K, fmt)));
+  uint8_t* xq = base + gws;
+  uint8_t* sx = xq + fq::up256(size_t(M) * (K / 2));
+  const fq_status st = fq_mx_quant(X, ldx, M, K, fmt, g_x, xq, sx, stream);
+  if (st != FQ_OK) return st;
+  return fq_mx_gemm(xq, sx, g_x, Wq, Sw, g_w, M, N, K, fmt, Y, base, gws, stream);
+}
+
+}  // extern "C"

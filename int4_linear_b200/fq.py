@@ -17,6 +17,7 @@ import torch
 ROW, GROUP, STATIC, ROW_ZP, STATIC_RESIDUAL = 0, 1, 2, 3, 4  # fq_gran
 SYNC_BYTES = 16384  # FQ_WORKSPACE_SYNC_BYTES: leading workspace bytes kept zero between calls
 GROUP_SIZE = 128
+MXFP4, NVFP4 = 0, 1  # fq_mx_format
 ZERO_POINT_MINMAX = -1                   # fq_qparams.zero_point: per-row min-max (asymmetric) quantizer
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -149,6 +150,10 @@ def lib():
         "fq_kv_store": [vp, vp, vp, vp, i, vp, kc, vp],
         "fq_kv_read": [kc, vp, i, vp, vp, vp],
         "fq_kv_attn": [vp, ll, i, i, vp, vp, i, kc, ctypes.c_float, i, vp, vp, sz, vp],
+        "fq_mx_quant": [vp, ll, i, i, i, vp, vp, vp, vp],
+        "fq_mx_dequant": [vp, vp, i, i, i, vp, vp, vp],
+        "fq_mx_gemm": [vp, vp, vp, vp, vp, vp, i, i, i, i, vp, vp, sz, vp],
+        "fq_mx_linear": [vp, ll, i, i, i, vp, vp, vp, vp, i, vp, vp, sz, vp],
         "fq_check_device_error": [vp],
         "fq_debug_wait_timeout": [ctypes.c_uint, vp],
     }
@@ -156,10 +161,13 @@ def lib():
         f = getattr(L, name)
         f.argtypes = args
         f.restype = ctypes.c_int
-    for name in ("fq_gemm_workspace_size", "fq_linear_workspace_size"):
+    for name in ("fq_gemm_workspace_size", "fq_linear_workspace_size", "fq_mx_gemm_workspace_size",
+                 "fq_mx_linear_workspace_size"):
         f = getattr(L, name)
         f.argtypes = [i, i, i, i]
         f.restype = sz
+    L.fq_mx_scale_bytes.argtypes = [i, i, i]
+    L.fq_mx_scale_bytes.restype = sz
     L.fq_kv_attn_workspace_size.argtypes = [i, i, i]
     L.fq_kv_attn_workspace_size.restype = sz
     L.fq_status_string.argtypes = [ctypes.c_int]
@@ -516,6 +524,106 @@ def fq_kv_attn(Q, lens, block_table, cache: KVCache, scale: float | None = None,
         _raise(lib().fq_kv_attn(Q.data_ptr(), ldq, r, hq, lens.data_ptr(), block_table.data_ptr(),
                                 block_table.shape[1], ctypes.byref(c), 128 ** -0.5 if scale is None else scale,
                                 window, Y.data_ptr(), workspace.data_ptr(), workspace.numel(), s))
+    return Y
+
+
+def fq_mx_scale_bytes(rows: int, k: int, fmt: int) -> int:
+    """Bytes of the tiled scales of a [rows, K] tensor, padding included."""
+    return lib().fq_mx_scale_bytes(rows, k, fmt)
+
+
+def _check_mx(Q, S, fmt, name):
+    _check(Q, torch.uint8, name + "q")
+    _check(S, torch.uint8, "S" + name.lower())
+    if Q.dim() != 2:
+        raise ValueError(f"{name}q must be [rows, K/2]")
+    need = fq_mx_scale_bytes(Q.shape[0], 2 * Q.shape[1], fmt)
+    if S.numel() != need:
+        raise ValueError(f"S{name.lower()} must hold {need} bytes, got {S.numel()}")
+
+
+def fq_mx_quant(X, fmt: int, g=None, Q=None, S=None, stream=None):
+    """fp16 [R, K] (rows any distance apart) to microscaled 4-bit codes: (Q uint8 [R, K/2], S uint8, the
+    tiled scales).  fmt MXFP4 or NVFP4 (g: its float32 [1] tensor scale on the device, None: 1)."""
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError("X must be a CUDA tensor [R, K]")
+    r, ldx = _check_rows(X, "X", X.shape[1])
+    k = X.shape[1]
+    _check(g, torch.float32, "g")
+    with _on(stream, X, g, Q, S) as s:
+        Q = torch.empty(r, k // 2, dtype=torch.uint8, device=X.device) if Q is None else Q
+        S = torch.empty(fq_mx_scale_bytes(r, k, fmt), dtype=torch.uint8, device=X.device) if S is None else S
+        if fq_mx_scale_bytes(r, k, fmt):
+            _check_shape(Q, (r, k // 2), "Q")
+            _check_mx(Q, S, fmt, "X")
+        _raise(lib().fq_mx_quant(X.data_ptr(), ldx, r, k, fmt, _p(g), Q.data_ptr(), S.data_ptr(), s))
+    return Q, S
+
+
+def fq_mx_dequant(Q, S, fmt: int, g=None, X=None, stream=None):
+    """Microscaled codes back to fp16 [R, K]."""
+    _check_mx(Q, S, fmt, "X")
+    _check(g, torch.float32, "g")
+    r, k = Q.shape[0], 2 * Q.shape[1]
+    with _on(stream, Q, S, g, X) as s:
+        X = torch.empty(r, k, dtype=torch.float16, device=Q.device) if X is None else X
+        _check(X, torch.float16, "X")
+        _check_shape(X, (r, k), "X")
+        _raise(lib().fq_mx_dequant(Q.data_ptr(), S.data_ptr(), r, k, fmt, _p(g), X.data_ptr(), s))
+    return X
+
+
+def fq_mx_gemm_workspace_size(m: int, n: int, k: int, fmt: int) -> int:
+    return lib().fq_mx_gemm_workspace_size(m, n, k, fmt)
+
+
+def fq_mx_linear_workspace_size(m: int, n: int, k: int, fmt: int) -> int:
+    return lib().fq_mx_linear_workspace_size(m, n, k, fmt)
+
+
+def fq_mx_linear_workspace(m: int, n: int, k: int, fmt: int, device="cuda"):
+    """A zeroed workspace for fq_mx_linear.  Calls that may overlap on the GPU need one each."""
+    with torch.cuda.device(device):
+        return torch.zeros(fq_mx_linear_workspace_size(m, n, k, fmt), dtype=torch.uint8, device=device)
+
+
+def fq_mx_gemm(Xq, Sx, Wq, Sw, fmt: int, g_x=None, g_w=None, Y=None, workspace=None, stream=None):
+    """Y fp16 [M, N] = the block-scaled product of microscaled activations and weights
+    (codes and scales as fq_mx_quant returns them), times g_x g_w."""
+    _check_mx(Xq, Sx, fmt, "X")
+    _check_mx(Wq, Sw, fmt, "W")
+    _check(g_x, torch.float32, "g_x")
+    _check(g_w, torch.float32, "g_w")
+    m, k, n = Xq.shape[0], 2 * Xq.shape[1], Wq.shape[0]
+    _check_shape(Wq, (n, k // 2), "Wq")
+    with _on(stream, Xq, Sx, Wq, Sw, g_x, g_w, Y, workspace) as s:
+        Y = torch.empty(m, n, dtype=torch.float16, device=Xq.device) if Y is None else Y
+        _check(Y, torch.float16, "Y")
+        _check_shape(Y, (m, n), "Y")
+        ws, wsb = _workspace(fq_mx_gemm_workspace_size(m, n, k, fmt), Xq.device, workspace)
+        _raise(lib().fq_mx_gemm(Xq.data_ptr(), Sx.data_ptr(), _p(g_x), Wq.data_ptr(), Sw.data_ptr(), _p(g_w), m, n, k,
+                                fmt, Y.data_ptr(), _p(ws), wsb, s))
+    return Y
+
+
+def fq_mx_linear(X, fmt: int, Wq, Sw, g_x=None, g_w=None, Y=None, workspace=None, stream=None):
+    """Y fp16 [M, N]: X fp16 [M, K] (rows any distance apart) quantized to microscaled 4-bit,
+    times the microscaled weights Wq [N, K/2], Sw, on one stream."""
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError("X must be a CUDA tensor [M, K]")
+    m, ldx = _check_rows(X, "X", X.shape[1])
+    k, n = X.shape[1], Wq.shape[0]
+    _check_mx(Wq, Sw, fmt, "W")
+    _check_shape(Wq, (n, k // 2), "Wq")
+    _check(g_x, torch.float32, "g_x")
+    _check(g_w, torch.float32, "g_w")
+    with _on(stream, X, Wq, Sw, g_x, g_w, Y, workspace) as s:
+        Y = torch.empty(m, n, dtype=torch.float16, device=X.device) if Y is None else Y
+        _check(Y, torch.float16, "Y")
+        _check_shape(Y, (m, n), "Y")
+        ws, wsb = _workspace(fq_mx_linear_workspace_size(m, n, k, fmt), X.device, workspace)
+        _raise(lib().fq_mx_linear(X.data_ptr(), ldx, m, k, fmt, _p(g_x), Wq.data_ptr(), Sw.data_ptr(), _p(g_w), n,
+                                  Y.data_ptr(), _p(ws), wsb, s))
     return Y
 
 
