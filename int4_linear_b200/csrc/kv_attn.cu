@@ -19,9 +19,9 @@
 // workspace, and the CTA that arrives last adds the parts in their fixed order
 // (the sums come out the same whichever CTA that is).
 //
-// In a CTA one warp brings the pages by bulk copies into an 8-stage ring (a page
-// of one head is one contiguous block), and 8 warps, 4 per tile, take 16 tokens
-// each, with their own m, l and sum, joined per segment through shared memory.
+// In a CTA eight warps take 16 tokens each in turn, each with its own m, l and sum,
+// joined per segment through shared memory.  A warp brings its own tokens
+// with 16-byte asynchronous copies several turns ahead and waits for nobody else's.
 //
 // Products: mma.m16n8k16 (fp16, float32 sums).  The tensor-memory path needs
 // 128 rows of queries, and a request has G = Hq / H <= 16 of them per head, so its
@@ -54,17 +54,18 @@ size_t sync_block_bytes();
 
 namespace {
 
-constexpr int kTile = 64;           // tokens per tile
-constexpr int kStages = 8;
-constexpr int kStageBytes = kTile * kKvTokenBytes;
-constexpr int kComputeWarps = 8;
-constexpr int kComputeThreads = kComputeWarps * 32;
-constexpr int kAttnThreads = kComputeThreads + 32;
+constexpr int kTile = 64;           // tokens per tile of the division
+constexpr int kStep = 16;           // tokens per warp and turn
+constexpr int kStepBytes = kStep * kKvTokenBytes;  // K codes, V codes, K scales, V scales
+constexpr int kStepV = kStep * kKvRowBytes, kStepKs = 2 * kStepV, kStepVs = kStepKs + 2 * kStep;
+constexpr int kDepth = 6;           // turns in flight per warp
+constexpr int kWarps = 8;
+constexpr int kAttnThreads = kWarps * 32;
 constexpr int kHeadPad = 164;       // floats of one head's sums in shared memory (see sum_offset)
 constexpr int kMaxAttnR = 16384;
 constexpr float kSlack = 7.0f;      // log2 of how far a score may pass the reference
+constexpr float kLowest = -1e30f;   // the reference before the first score
 constexpr float kWeightScale = 256.0f;
-constexpr unsigned kErrTimeoutAttn = 0x106;
 
 struct AttnParams {
   const __half* Q;
@@ -79,18 +80,13 @@ struct AttnParams {
   __half* Y;
   float* part;                      // [2 * CTAs][8 NT][130]: sums, m, l
   unsigned* count;                  // one counter per CTA
-  unsigned* err;
 };
 
 struct AttnSmem {
-  uint64_t full[kStages], empty[kStages];
-  uint32_t valid[kStages];          // bit i: tokens [16 i, 16 i + 16) of the tile were loaded
-  long long first, last;            // this CTA's part of the tile sequence
-  long long total;
-  int r0;                           // the request it starts in, and the tiles before that request
+  int r0;                           // the request this CTA starts in, and the tiles before that request
   long long before;
-  long long wsum[kAttnThreads / 32];
-  float m[kComputeWarps][16], l[kComputeWarps][16];
+  long long wsum[kWarps];
+  float m[kWarps][16], l[kWarps][16];
   int join;
 };
 
@@ -126,10 +122,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
+// (a & b) ^ c in one logic operation.
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
 // Nibbles at bits 4-7 of each half word (two's complement codes q) -> fp16 72 + q.
-__device__ __forceinline__ uint32_t codes72(uint32_t w) { return (w & 0x00F000F0u) ^ 0x54805480u; }
+__device__ __forceinline__ uint32_t codes72(uint32_t w) { return and_xor(w, 0x00F000F0u, 0x54805480u); }
 // Nibbles at bits 0-3 of each half word -> fp16 1032 + q.
-__device__ __forceinline__ uint32_t codes1032(uint32_t w) { return (w & 0x000F000Fu) ^ 0x64086408u; }
+__device__ __forceinline__ uint32_t codes1032(uint32_t w) { return and_xor(w, 0x000F000Fu, 0x64086408u); }
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -147,6 +149,15 @@ __device__ __forceinline__ int token_of_row(int i) {
 // consecutive g write, and lanes with consecutive (d / 4, g) read, distinct banks.
 __device__ __forceinline__ int sum_offset(int g, int d) { return d * 8 + (d >> 2) * 8 + g; }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // The CTA whose part holds tile x of the sequence: parts are [total c / C, total (c + 1) / C).
 __device__ __forceinline__ int cta_of_tile(long long x, long long total, int C) {
   return int(((x + 1) * C - 1) / total);
@@ -155,19 +166,12 @@ __device__ __forceinline__ int cta_of_tile(long long x, long long total, int C) 
 template <int NT>
 __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(const AttnParams p) {
   constexpr int HB = 8 * NT;
+  // the warps' turns in flight; between segments the eight warps' sums, [warps][8][kHeadPad]
   extern __shared__ __align__(128) uint8_t dyn[];
-  uint8_t* ring = dyn;
-  float* sums = reinterpret_cast<float*>(dyn + kStages * kStageBytes);  // [warps][8][kHeadPad]
+  float* sums = reinterpret_cast<float*>(dyn);
   __shared__ AttnSmem sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, HC = p.kv.H * p.chunks;
-  if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], 4);
-    }
-    fence_mbar_init();
-  }
   pdl_launch_dependents();
   pdl_wait();
 
@@ -189,7 +193,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   __syncthreads();
   long long base = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kAttnThreads / 32; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) base += sm.wsum[w];
     all += sm.wsum[w];
   }
@@ -225,101 +229,18 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
 
   int r = sm.r0;
   long long pos = first, before = sm.before;  // next tile; tiles before request r
-  int n = 0;                                  // tiles of this CTA so far
-  if (warp == kComputeWarps) {
-    // ------------------------------------------------------------ pages into the ring
-    const int ps = p.kv.page_shift;
-    const int sub = lane & 3;                  // lane 4 i + sub: copy `sub` of tile i of a batch of 8
-    const int copies = ps == 4 ? 4 : ps == 5 ? 2 : ps == 6 ? 1 : 4;
-    bool bad = false;
-    while (pos < last) {
-      const Span s = span_of(p, r);
-      const int nt = s.t1 - s.t0;
-      const long long len_r = static_cast<long long>(nt) * HC;
-      if (pos >= before + len_r) {
-        before += len_r;
-        ++r;
-        continue;
-      }
-      const int hc = int((pos - before) / nt), ta = int((pos - before) % nt);
-      const int tb = int(min(static_cast<long long>(nt), ta + (last - pos)));
-      const int head = hc / p.chunks;
-      const int32_t* row = p.table + static_cast<size_t>(r) * p.max_pages;
-      // page ids of a batch of 8 tiles, one batch ahead of the copies
-      auto load_id = [&](int t) {
-        const int tok = (s.t0 + t + (lane >> 2)) * kTile + (ps < 6 ? sub << ps : 0);
-        if (t + (lane >> 2) >= tb || sub >= copies || tok >= s.hi) return -1;
-        const int pg = tok >> ps;
-        if (((pg + 1) << ps) <= s.lo) return -1;
-        const int id = __ldg(row + pg);
-        return id >= 0 && id < p.kv.num_pages ? id : -1;
-      };
-      int id = load_id(ta);
-      for (int t = ta; t < tb; t += 8) {
-        const int next = load_id(t + 8);
-        const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
-        for (int i = 0; i < 8 && t + i < tb; ++i, ++n) {
-          const int st = n % kStages;
-          if (!bad && n >= kStages && !warp_wait(&sm.empty[st], ((n / kStages) - 1) & 1)) {
-            if (lane == 0) record_error(p.err, kErrTimeoutAttn);
-            bad = true;
-          }
-          const uint32_t got = bad ? 0u : (have >> (4 * i)) & 15u;
-          if (lane == 0) {
-            uint32_t v = 0, bytes = 0;
-            if (ps == 4) {
-              v = got;
-              bytes = __popc(got) * (16 * kKvTokenBytes);
-            } else if (ps == 5) {
-              v = (got & 1u ? 3u : 0u) | (got & 2u ? 12u : 0u);
-              bytes = __popc(got) * (32 * kKvTokenBytes);
-            } else if (got) {
-              v = 15u;
-              bytes = kStageBytes;
-            }
-            sm.valid[st] = v;
-            mbar_arrive_expect_tx(&sm.full[st], bytes);
-          }
-          __syncwarp();
-          if ((lane >> 2) == i && id >= 0 && !bad) {
-            const uint8_t* src = p.kv.block(id, head);
-            uint8_t* dst = ring + st * kStageBytes;
-            if (ps <= 6) {
-              bulk_load(dst + (sub * kKvTokenBytes << ps), src, uint32_t(kKvTokenBytes << ps), &sm.full[st]);
-            } else {
-              // half of a page of 128, laid out as a page of 64
-              const int half = (s.t0 + t + i) & 1;
-              const int which = sub & 1;
-              if (sub < 2)
-                bulk_load(dst + which * kTile * kKvRowBytes, src + p.kv.codes(which) + half * kTile * kKvRowBytes,
-                          kTile * kKvRowBytes, &sm.full[st]);
-              else
-                bulk_load(dst + 2 * kTile * kKvRowBytes + which * kTile * 2,
-                          src + p.kv.scales(which) + half * kTile * 2, kTile * 2, &sm.full[st]);
-            }
-          }
-        }
-        id = next;
-      }
-      pos += tb - ta;
-    }
-    return;
-  }
-
-  // -------------------------------------------------------------- scores and sums
+  const int ps = p.kv.page_shift;
   const int g = lane >> 2, t4 = lane & 3;
-  const int grp = warp >> 2, quarter = warp & 3;
-  const int psub = min(p.kv.page_shift, 6);                      // log2 of a ring block's tokens
-  const int blk = ((quarter * 16) >> psub) * (kKvTokenBytes << psub);
-  const int off = (quarter * 16) & ((1 << psub) - 1);
-  // byte offsets inside a stage of this lane's operands
-  const int row0 = token_of_row(g);                              // score rows g and g + 8: tokens row0, row0 + 8
-  const int k_off = blk + (off + row0) * kKvRowBytes + t4 * 16;
-  const int ks_off = blk + (2 * kKvRowBytes << psub) + 2 * (off + row0);
-  const int vs_off = blk + ((2 * kKvRowBytes + 2) << psub) + 2 * (off + row0);
-  const int va = token_of_row(2 * t4), vb = token_of_row(2 * t4 + 1);
-  const int v_off = blk + (kKvRowBytes << psub) + off * kKvRowBytes + 8 * g;
-  bool bad = false;
+  // what this lane copies of a turn: 16-byte pieces `lane` and 32 + lane of the K and of the V codes
+  // and (lanes 0-3) a piece of the scales
+  const uint32_t my_ring = smem_u32(dyn) + uint32_t(warp * kDepth * kStepBytes);
+  const int sc_off = (2 * kKvRowBytes << ps) + (lane & 1) * 16 + ((lane >> 1) & 1) * (2 << ps);
+  // byte offsets inside a turn of this lane's operands
+  const int row0 = token_of_row(g);           // score rows g and g + 8: tokens row0, row0 + 8
+  const uint8_t* ring = dyn + warp * kDepth * kStepBytes;
+  const int k_off = row0 * kKvRowBytes + t4 * 16;
+  const int va_off = kStepV + token_of_row(2 * t4) * kKvRowBytes + 8 * g;
+  const int vb_off = kStepV + token_of_row(2 * t4 + 1) * kKvRowBytes + 8 * g;
   while (pos < last) {
     const Span s = span_of(p, r);
     const int nt = s.t1 - s.t0;
@@ -333,6 +254,43 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
     const int tb = int(min(static_cast<long long>(nt), ta + (last - pos)));
     const int head = hc / p.chunks, q0 = head * p.G + (hc % p.chunks) * HB;  // first query head
     const int heads = min(HB, p.G - (hc % p.chunks) * HB);
+
+    // ---- this warp's turns: 16 tokens at tok0 + 128 i
+    const int tok0 = (s.t0 + ta) * kTile + warp * kStep;
+    const int tok_end = min(s.hi, (s.t0 + tb) * kTile);
+    const int turns = tok0 < tok_end ? (tok_end - 1 - tok0) / (kWarps * kStep) + 1 : 0;
+    const int32_t* row = p.table + static_cast<size_t>(r) * p.max_pages;
+    auto page_id = [&](int i) {
+      const int t = tok0 + i * (kWarps * kStep);
+      return i < turns && t + kStep > s.lo ? __ldg(row + (t >> ps)) : -1;
+    };
+    uint32_t loaded = 0;  // bit j: the turn fetched j turns ago has its tokens
+    auto fetch = [&](int i, int id, int slot) {
+      const bool ok = id >= 0 && id < p.kv.num_pages;
+      if (ok) {
+        const int off = (tok0 + i * (kWarps * kStep)) & ((1 << ps) - 1);
+        const uint8_t* src = p.kv.block(id, head);
+        const uint32_t dst = my_ring + uint32_t(slot * kStepBytes) + lane * 16;
+        const uint8_t* k = src + off * kKvRowBytes + lane * 16;
+        const uint8_t* v = k + (kKvRowBytes << ps);
+        copy16(dst, k);
+        copy16(dst + 512, k + 512);
+        copy16(dst + kStepV, v);
+        copy16(dst + kStepV + 512, v + 512);
+        if (lane < 4) copy16(dst + kStepKs, src + sc_off + 2 * off);
+      }
+      loaded = (loaded << 1) | uint32_t(ok);
+      copy_commit();
+    };
+    int next_id;
+    {
+      int id[kDepth - 1];
+#pragma unroll
+      for (int i = 0; i < kDepth - 1; ++i) id[i] = page_id(i);
+      next_id = page_id(kDepth - 1);
+#pragma unroll
+      for (int i = 0; i < kDepth - 1; ++i) fetch(i, id[i], i);
+    }
 
     // queries of this segment, in the order of the nibbles: lane (g, t4) holds head g, dims [32 t4, 32 t4 + 32)
     uint32_t qf[NT][16];
@@ -370,123 +328,136 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[nn][i][k] = 0.f;
-      m[nn][0] = m[nn][1] = -INFINITY;
+      m[nn][0] = m[nn][1] = kLowest;
       l[nn][0] = l[nn][1] = 0.f;
     }
 
-    for (int t = ta; t < tb; ++t, ++n) {
-      if ((n & 1) != grp) continue;
-      const int st = n % kStages;
-      if (!bad && !warp_wait(&sm.full[st], (n / kStages) & 1)) {
-        if (lane == 0) record_error(p.err, kErrTimeoutAttn);
-        bad = true;
+    int slot = 0;
+    for (int i = 0; i < turns; ++i) {
+      copy_wait<kDepth - 2>();
+      __syncwarp();  // every lane's copies of this turn, and every lane is done with the last one
+      {
+        const int id = next_id;
+        next_id = page_id(i + kDepth);
+        fetch(i + kDepth - 1, id, slot == 0 ? kDepth - 1 : slot - 1);
       }
-      const int pos0 = (s.t0 + t) * kTile + quarter * 16;
-      if (((sm.valid[st] >> quarter) & 1u) && pos0 < s.hi && pos0 + 16 > s.lo) {
-        const uint8_t* sp = ring + st * kStageBytes;
-        const uint4 k0 = *reinterpret_cast<const uint4*>(sp + k_off);
-        const uint4 k1 = *reinterpret_cast<const uint4*>(sp + k_off + 8 * kKvRowBytes);
-        const float ks0 = __half2float(*reinterpret_cast<const __half*>(sp + ks_off)) * p.scale_log2;
-        const float ks1 = __half2float(*reinterpret_cast<const __half*>(sp + ks_off + 16)) * p.scale_log2;
-        float vs0 = __half2float(*reinterpret_cast<const __half*>(sp + vs_off));
-        float vs1 = __half2float(*reinterpret_cast<const __half*>(sp + vs_off + 16));
-        const bool ok0 = pos0 + row0 >= s.lo && pos0 + row0 < s.hi;
-        const bool ok1 = pos0 + row0 + 8 >= s.lo && pos0 + row0 + 8 < s.hi;
-        if (!ok0) vs0 = 0.f;
-        if (!ok1) vs1 = 0.f;
-        float sc[NT][4];
+      const uint8_t* sp = ring + slot * kStepBytes;
+      slot = slot == kDepth - 1 ? 0 : slot + 1;
+      if (!((loaded >> (kDepth - 1)) & 1u)) continue;
+      const uint4 k0 = *reinterpret_cast<const uint4*>(sp + k_off);
+      const uint4 k1 = *reinterpret_cast<const uint4*>(sp + k_off + 8 * kKvRowBytes);
+      float ks0 = __half2float(*reinterpret_cast<const __half*>(sp + kStepKs + 2 * row0)) * p.scale_log2;
+      float ks1 = __half2float(*reinterpret_cast<const __half*>(sp + kStepKs + 2 * row0 + 16)) * p.scale_log2;
+      float vs0 = __half2float(*reinterpret_cast<const __half*>(sp + kStepVs + 2 * row0));
+      float vs1 = __half2float(*reinterpret_cast<const __half*>(sp + kStepVs + 2 * row0 + 16));
+      float sc[NT][4];
+#pragma unroll
+      for (int nn = 0; nn < NT; ++nn) {
+        sc[nn][0] = sc[nn][2] = c0[nn][0];
+        sc[nn][1] = sc[nn][3] = c0[nn][1];
+      }
+      const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a[4] = {codes72(kw0[j] << 4), codes72(kw1[j] << 4), codes72(kw0[j]), codes72(kw1[j])};
+        const uint32_t b[4] = {codes72(kw0[j] >> 4), codes72(kw1[j] >> 4), codes72(kw0[j] >> 8), codes72(kw1[j] >> 8)};
 #pragma unroll
         for (int nn = 0; nn < NT; ++nn) {
-          sc[nn][0] = sc[nn][2] = c0[nn][0];
-          sc[nn][1] = sc[nn][3] = c0[nn][1];
+          mma_f16(sc[nn], a, qf[nn][4 * j], qf[nn][4 * j + 1]);
+          mma_f16(sc[nn], b, qf[nn][4 * j + 2], qf[nn][4 * j + 3]);
         }
-        const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a[4] = {codes72(kw0[j] << 4), codes72(kw1[j] << 4), codes72(kw0[j]), codes72(kw1[j])};
-          const uint32_t b[4] = {codes72(kw0[j] >> 4), codes72(kw1[j] >> 4), codes72(kw0[j] >> 8),
-                                 codes72(kw1[j] >> 8)};
-#pragma unroll
-          for (int nn = 0; nn < NT; ++nn) {
-            mma_f16(sc[nn], a, qf[nn][4 * j], qf[nn][4 * j + 1]);
-            mma_f16(sc[nn], b, qf[nn][4 * j + 2], qf[nn][4 * j + 3]);
-          }
-        }
-        // scores in units of log2; what is masked is -inf whatever its scale holds
-        bool move = fmaxf(vs0, vs1) > vcap;
+      }
+      const int at = tok0 + i * (kWarps * kStep);
+      if (at < s.lo || at + kStep > s.hi) {
+        // what is masked scores -inf and weighs 0, whatever its scales hold
+        const bool ok0 = at + row0 >= s.lo && at + row0 < s.hi;
+        const bool ok1 = at + row0 + 8 >= s.lo && at + row0 + 8 < s.hi;
+        ks0 = ok0 ? ks0 : 1.0f;
+        ks1 = ok1 ? ks1 : 1.0f;
+        vs0 = ok0 ? vs0 : 0.0f;
+        vs1 = ok1 ? vs1 : 0.0f;
 #pragma unroll
         for (int nn = 0; nn < NT; ++nn) {
-          sc[nn][0] = ok0 ? sc[nn][0] * ks0 : -INFINITY;
-          sc[nn][1] = ok0 ? sc[nn][1] * ks0 : -INFINITY;
-          sc[nn][2] = ok1 ? sc[nn][2] * ks1 : -INFINITY;
-          sc[nn][3] = ok1 ? sc[nn][3] * ks1 : -INFINITY;
-          move |= fmaxf(sc[nn][0], sc[nn][2]) > m[nn][0] + kSlack;
-          move |= fmaxf(sc[nn][1], sc[nn][3]) > m[nn][1] + kSlack;
+          sc[nn][0] = ok0 ? sc[nn][0] : -INFINITY;
+          sc[nn][1] = ok0 ? sc[nn][1] : -INFINITY;
+          sc[nn][2] = ok1 ? sc[nn][2] : -INFINITY;
+          sc[nn][3] = ok1 ? sc[nn][3] : -INFINITY;
         }
-        if (__any_sync(0xffffffffu, move)) {
-          // new references: the largest score of each head, the largest v scale
-          float vm = fmaxf(fmaxf(vs0, vs1), vcap);
+      }
+      // log2 of the weights before the v scale, and whether one passes its reference by too much
+      float x[NT][4];
+      bool move = fmaxf(vs0, vs1) > vcap;
 #pragma unroll
-          for (int x = 4; x < 32; x <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, x));
-          const float vf = vm > 0.f ? vcap / vm : 0.f;
-          vcap = vm;
-          vinv = vm > 0.f ? kWeightScale / vm : 0.f;
+      for (int nn = 0; nn < NT; ++nn) {
+        x[nn][0] = __fmaf_rn(sc[nn][0], ks0, -m[nn][0]);
+        x[nn][1] = __fmaf_rn(sc[nn][1], ks0, -m[nn][1]);
+        x[nn][2] = __fmaf_rn(sc[nn][2], ks1, -m[nn][0]);
+        x[nn][3] = __fmaf_rn(sc[nn][3], ks1, -m[nn][1]);
+        move |= fmaxf(fmaxf(x[nn][0], x[nn][1]), fmaxf(x[nn][2], x[nn][3])) > kSlack;
+      }
+      if (__any_sync(0xffffffffu, move)) {
+        // new references: the largest score of each head, the largest v scale
+        float vm = fmaxf(fmaxf(vs0, vs1), vcap);
 #pragma unroll
-          for (int nn = 0; nn < NT; ++nn) {
+        for (int d = 4; d < 32; d <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, d));
+        const float vf = vm > 0.f ? vcap / vm : 0.f;
+        vcap = vm;
+        vinv = vm > 0.f ? kWeightScale / vm : 0.f;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float mx = fmaxf(m[nn][k], fmaxf(sc[nn][k], sc[nn][k + 2]));
+        for (int nn = 0; nn < NT; ++nn) {
 #pragma unroll
-              for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-              const float f = m[nn][k] == -INFINITY ? 0.f : exp2_approx(m[nn][k] - mx);
-              m[nn][k] = mx;
-              l[nn][k] *= f;
+          for (int k = 0; k < 2; ++k) {
+            float mx = fmaxf(m[nn][k], fmaxf(sc[nn][k] * ks0, sc[nn][k + 2] * ks1));
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                o[nn][i][k] *= f * vf;
-                o[nn][i][k + 2] *= f * vf;
-              }
+            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float f = exp2_approx(m[nn][k] - mx);
+            m[nn][k] = mx;
+            x[nn][k] = __fmaf_rn(sc[nn][k], ks0, -mx);
+            x[nn][k + 2] = __fmaf_rn(sc[nn][k + 2], ks1, -mx);
+            l[nn][k] *= f;
+#pragma unroll
+            for (int i8 = 0; i8 < 8; ++i8) {
+              o[nn][i8][k] *= f * vf;
+              o[nn][i8][k + 2] *= f * vf;
             }
           }
         }
-        uint32_t w0[NT], w1[NT];
-        const float v0 = vs0 * vinv, v1 = vs1 * vinv;
+      }
+      uint32_t w0[NT], w1[NT];
+      const float v0 = vs0 * vinv, v1 = vs1 * vinv;
+#pragma unroll
+      for (int nn = 0; nn < NT; ++nn) {
+        const float p0 = exp2_approx(x[nn][0]), p1 = exp2_approx(x[nn][1]);
+        const float p2 = exp2_approx(x[nn][2]), p3 = exp2_approx(x[nn][3]);
+        l[nn][0] += p0 + p2;
+        l[nn][1] += p1 + p3;
+        const __half2 a = __floats2half2_rn(p0 * v0, p1 * v0), b = __floats2half2_rn(p2 * v1, p3 * v1);
+        w0[nn] = transpose8x8(*reinterpret_cast<const uint32_t*>(&a));
+        w1[nn] = transpose8x8(*reinterpret_cast<const uint32_t*>(&b));
+      }
+      // values: lane (g, t4) holds dims [16 g, 16 g + 16) of its four tokens
+      const uint2 x0 = *reinterpret_cast<const uint2*>(sp + va_off);
+      const uint2 x1 = *reinterpret_cast<const uint2*>(sp + vb_off);
+      const uint2 x2 = *reinterpret_cast<const uint2*>(sp + va_off + 8 * kKvRowBytes);
+      const uint2 x3 = *reinterpret_cast<const uint2*>(sp + vb_off + 8 * kKvRowBytes);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // four dims: half word j of the 16 dims
+        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+        const uint32_t y0 = __byte_perm(j < 2 ? x0.x : x0.y, j < 2 ? x1.x : x1.y, sel);
+        const uint32_t y1 = __byte_perm(j < 2 ? x2.x : x2.y, j < 2 ? x3.x : x3.y, sel);
+        const uint32_t a[4] = {hsub2(codes1032(y0), 0x64086408u), hsub2(codes72(y0), 0x54805480u),
+                               hsub2(codes1032(y1), 0x64086408u), hsub2(codes72(y1), 0x54805480u)};
+        const uint32_t z0 = y0 >> 8, z1 = y1 >> 8;
+        const uint32_t b[4] = {hsub2(codes1032(z0), 0x64086408u), hsub2(codes72(z0), 0x54805480u),
+                               hsub2(codes1032(z1), 0x64086408u), hsub2(codes72(z1), 0x54805480u)};
 #pragma unroll
         for (int nn = 0; nn < NT; ++nn) {
-          const float ma = m[nn][0] == -INFINITY ? 0.f : m[nn][0], mb = m[nn][1] == -INFINITY ? 0.f : m[nn][1];
-          const float p0 = exp2_approx(sc[nn][0] - ma), p1 = exp2_approx(sc[nn][1] - mb);
-          const float p2 = exp2_approx(sc[nn][2] - ma), p3 = exp2_approx(sc[nn][3] - mb);
-          l[nn][0] += p0 + p2;
-          l[nn][1] += p1 + p3;
-          const __half2 a = __floats2half2_rn(p0 * v0, p1 * v0), b = __floats2half2_rn(p2 * v1, p3 * v1);
-          w0[nn] = transpose8x8(*reinterpret_cast<const uint32_t*>(&a));
-          w1[nn] = transpose8x8(*reinterpret_cast<const uint32_t*>(&b));
-        }
-        // values: lane (g, t4) holds dims [16 g, 16 g + 16) of its four tokens
-        const uint2 x0 = *reinterpret_cast<const uint2*>(sp + v_off + va * kKvRowBytes);
-        const uint2 x1 = *reinterpret_cast<const uint2*>(sp + v_off + vb * kKvRowBytes);
-        const uint2 x2 = *reinterpret_cast<const uint2*>(sp + v_off + (va + 8) * kKvRowBytes);
-        const uint2 x3 = *reinterpret_cast<const uint2*>(sp + v_off + (vb + 8) * kKvRowBytes);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // four dims: half word j of the 16 dims
-          const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-          const uint32_t y0 = __byte_perm(j < 2 ? x0.x : x0.y, j < 2 ? x1.x : x1.y, sel);
-          const uint32_t y1 = __byte_perm(j < 2 ? x2.x : x2.y, j < 2 ? x3.x : x3.y, sel);
-          const uint32_t a[4] = {hsub2(codes1032(y0), 0x64086408u), hsub2(codes72(y0), 0x54805480u),
-                                 hsub2(codes1032(y1), 0x64086408u), hsub2(codes72(y1), 0x54805480u)};
-          const uint32_t z0 = y0 >> 8, z1 = y1 >> 8;
-          const uint32_t b[4] = {hsub2(codes1032(z0), 0x64086408u), hsub2(codes72(z0), 0x54805480u),
-                                 hsub2(codes1032(z1), 0x64086408u), hsub2(codes72(z1), 0x54805480u)};
-#pragma unroll
-          for (int nn = 0; nn < NT; ++nn) {
-            mma_f16(o[nn][2 * j], a, w0[nn], w1[nn]);      // dims 4 j (rows g), 4 j + 1 (rows g + 8)
-            mma_f16(o[nn][2 * j + 1], b, w0[nn], w1[nn]);  // dims 4 j + 2, 4 j + 3
-          }
+          mma_f16(o[nn][2 * j], a, w0[nn], w1[nn]);      // dims 4 j (rows g), 4 j + 1 (rows g + 8)
+          mma_f16(o[nn][2 * j + 1], b, w0[nn], w1[nn]);  // dims 4 j + 2, 4 j + 3
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.empty[st]);
     }
+    copy_wait<0>();
 
     // ---- the eight warps' parts of the segment
 #pragma unroll
@@ -495,28 +466,27 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       for (int k = 0; k < 2; ++k) {
         float v = l[nn][k];
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+        for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
         if (g == 0) {
           sm.m[warp][nn * 8 + 2 * t4 + k] = m[nn][k];
           sm.l[warp][nn * 8 + 2 * t4 + k] = v;
         }
       }
-    named_barrier(1, kComputeThreads);
+    __syncthreads();  // also: every warp is done with its turns, whose bytes the sums take
     const long long item0 = before + static_cast<long long>(hc) * nt;  // the request and head's tiles in the sequence
     const bool whole = ta == 0 && tb == nt;
     const int c_first = cta_of_tile(item0, total, C);
     const int parts = cta_of_tile(item0 + nt - 1, total, C) - c_first + 1;
-    const int slot = 2 * cta + (ta == 0 ? 1 : 0);
-    float* part = p.part + static_cast<size_t>(slot) * HB * (kHeadDim + 2);
+    float* part = p.part + static_cast<size_t>(2 * cta + (ta == 0 ? 1 : 0)) * HB * (kHeadDim + 2);
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn) {
       // 1. every warp's sums at the common reference
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float mx = -INFINITY;
+        float mx = kLowest;
 #pragma unroll
-        for (int w = 0; w < kComputeWarps; ++w) mx = fmaxf(mx, sm.m[w][nn * 8 + 2 * t4 + k]);
-        const float f = m[nn][k] == -INFINITY ? 0.f : exp2_approx(m[nn][k] - mx) * (vcap * (1.0f / kWeightScale));
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm.m[w][nn * 8 + 2 * t4 + k]);
+        const float f = exp2_approx(m[nn][k] - mx) * (vcap * (1.0f / kWeightScale));
         float* dst = sums + (warp * 8 + 2 * t4 + k) * kHeadPad;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -525,22 +495,21 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
           dst[sum_offset(g, d + 1)] = o[nn][i][k + 2] * f;
         }
       }
-      named_barrier(1, kComputeThreads);
+      __syncthreads();
       // 2. added over the warps: this thread takes head `warp`, dims 16 (lane % 8) + 4 (lane / 8) + 0..3
       const int hh = nn * 8 + warp;
       const int gg = lane & 7, d4 = lane >> 3;
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      float mx = -INFINITY, ls = 0.f;
+      float mx = kLowest, ls = 0.f;
 #pragma unroll
-      for (int w = 0; w < kComputeWarps; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float* src = sums + (w * 8 + warp) * kHeadPad;
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[k] += src[sum_offset(gg, 4 * d4 + k)];
         mx = fmaxf(mx, sm.m[w][hh]);
       }
 #pragma unroll
-      for (int w = 0; w < kComputeWarps; ++w)
-        if (sm.m[w][hh] != -INFINITY) ls += sm.l[w][hh] * exp2_approx(sm.m[w][hh] - mx);
+      for (int w = 0; w < kWarps; ++w) ls += sm.l[w][hh] * exp2_approx(sm.m[w][hh] - mx);
       if (hh < heads) {
         const int dim = 16 * gg + 4 * d4;
         if (whole) {
@@ -557,27 +526,26 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
           }
         }
       }
-      if (nn + 1 < NT) named_barrier(1, kComputeThreads);
+      if (nn + 1 < NT) __syncthreads();
     }
     if (!whole) {
       // 3. the CTA that arrives last joins the parts, in the order of the CTAs
       __threadfence();
-      named_barrier(1, kComputeThreads);
+      __syncthreads();
       if (tid == 0) sm.join = atomicInc(&p.count[c_first], unsigned(parts - 1)) == unsigned(parts - 1);
-      named_barrier(1, kComputeThreads);
+      __syncthreads();
       if (sm.join) {
         __threadfence();
         const size_t stride = static_cast<size_t>(HB) * (kHeadDim + 2);
-        for (int hh = warp; hh < heads; hh += kComputeWarps) {
-          float mx = -INFINITY;
+        for (int hh = warp; hh < heads; hh += kWarps) {
+          float mx = kLowest;
           for (int c = 0; c < parts; ++c)
             mx = fmaxf(mx, __ldcg(p.part + (2 * (c_first + c) + (c == 0)) * stride + HB * kHeadDim + hh));
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           float ls = 0.f;
           for (int c = 0; c < parts; ++c) {
             const float* src = p.part + (2 * (c_first + c) + (c == 0)) * stride;
-            const float mc = __ldcg(src + HB * kHeadDim + hh);
-            const float f = mc == -INFINITY ? 0.f : exp2_approx(mc - mx);
+            const float f = exp2_approx(__ldcg(src + HB * kHeadDim + hh) - mx);
             ls += __ldcg(src + HB * kHeadDim + HB + hh) * f;
             const float4 v = __ldcg(reinterpret_cast<const float4*>(src + hh * kHeadDim) + lane);
             acc.x += v.x * f;
@@ -594,15 +562,13 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       }
     }
     pos += tb - ta;
-    // the next segment's writes to sm.m follow every warp's reads above
-    named_barrier(1, kComputeThreads);
+    // the next segment's copies and writes to sm follow every warp's reads above
+    __syncthreads();
   }
 }
 
-template <int NT>
-constexpr size_t attn_smem() {
-  return size_t(kStages) * kStageBytes + size_t(kComputeWarps) * 8 * kHeadPad * sizeof(float);
-}
+constexpr size_t kAttnSmem = size_t(kWarps) * kDepth * kStepBytes;
+static_assert(kAttnSmem >= size_t(kWarps) * 8 * kHeadPad * sizeof(float), "the sums take the turns' bytes");
 
 // CTAs of a launch: two per SM with one tile of 8 queries, one with two (their
 // registers hold 16 queries' sums).
@@ -612,9 +578,9 @@ int attn_grid(int nt) { return sm_count() * (nt == 1 ? 2 : 1); }
 template <int NT>
 fq_status launch_attn(const AttnParams& p, cudaStream_t stream) {
   auto kern = kv_attn_kernel<NT>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(attn_smem<NT>())) != cudaSuccess)
-    return fail(FQ_ERR_CUDA, "cannot reserve %zu bytes of shared memory", attn_smem<NT>());
-  launch_pdl(kern, dim3(attn_grid(NT)), dim3(kAttnThreads), attn_smem<NT>(), stream, p);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kAttnSmem)) != cudaSuccess)
+    return fail(FQ_ERR_CUDA, "cannot reserve %zu bytes of shared memory", kAttnSmem);
+  launch_pdl(kern, dim3(attn_grid(NT)), dim3(kAttnThreads), kAttnSmem, stream, p);
   return check_launch("kv_attn_kernel");
 }
 
@@ -650,8 +616,6 @@ fq_status fq_kv_attn(const uint16_t* Q, long long ldq, int R, int Hq, const int3
   const size_t need = fq_kv_attn_workspace_size(R, Hq, cache->H);
   if (!workspace || ws_bytes < need || !fq::aligned(workspace, 256))
     return fq::fail(FQ_ERR_INVALID, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, ws_bytes);
-  unsigned* err = fq::device_error_word();
-  if (!err) return fq::fail(FQ_ERR_CUDA, "device error word unavailable");
   fq::AttnParams p{};
   p.Q = reinterpret_cast<const __half*>(Q);
   p.ldq = ldq;
@@ -669,7 +633,6 @@ fq_status fq_kv_attn(const uint16_t* Q, long long ldq, int R, int Hq, const int3
   p.Y = reinterpret_cast<__half*>(Y);
   p.count = static_cast<unsigned*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + fq::sync_block_bytes());
-  p.err = err;
   return nt == 1 ? fq::launch_attn<1>(p, static_cast<cudaStream_t>(stream))
                  : fq::launch_attn<2>(p, static_cast<cudaStream_t>(stream));
 }

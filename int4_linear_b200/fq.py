@@ -205,25 +205,46 @@ def _s(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-@contextlib.contextmanager
+class _On:
+    """`with` block in which a device and a stream are current (see _on)."""
+    __slots__ = ("handle", "stack")
+
+    def __init__(self, handle, stack=None):
+        self.handle, self.stack = handle, stack
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.stack is not None:
+            self.stack.close()
+        return False
+
+
 def _on(stream, *tensors):
     """The device of `tensors` (all on one) made current and, where a stream is given, that
     stream, so that what is allocated inside belongs to the stream that uses it.  Yields the
-    stream's handle."""
-    dev = {t.device for t in tensors if t is not None}
-    if len(dev) != 1:
-        raise ValueError(f"the tensors lie on {len(dev)} devices, not on one")
-    dev = dev.pop()
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield torch.cuda.current_stream(dev).cuda_stream
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(stream, device=dev)
-            elif stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+    stream's handle.  The usual case, the current device and stream, enters nothing."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if dev < 0:
+                dev = d
+            elif d != dev:
+                raise ValueError(f"the tensors lie on cuda:{dev} and cuda:{d}, not on one device")
+    if stream is None and dev == torch.cuda.current_device():
+        return _On(torch._C._cuda_getCurrentRawStream(dev))
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        elif stream.device.index != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(dev))
+    if stream is not None:
+        stack.enter_context(torch.cuda.stream(stream))
+    return _On(torch._C._cuda_getCurrentRawStream(dev), stack)
 
 
 def _check_shape(t, shape, name):
@@ -238,11 +259,17 @@ def _check_rows(t, name, width):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.float16:
         raise ValueError(f"{name} must be torch.float16, got {t.dtype}")
-    if t.dim() < 2 or t.shape[0] < 1 or t[0].numel() != width:
-        raise ValueError(f"{name} must have rows of {width} values, got shape {tuple(t.shape)}")
-    if not t[0].is_contiguous():
+    shape, strides = t.shape, t.stride()
+    n = 1
+    dense = True
+    for d in range(len(shape) - 1, 0, -1):
+        dense = dense and (strides[d] == n or shape[d] == 1)
+        n *= shape[d]
+    if len(shape) < 2 or shape[0] < 1 or n != width:
+        raise ValueError(f"{name} must have rows of {width} values, got shape {tuple(shape)}")
+    if not dense:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.shape[0], (t.stride(0) if t.shape[0] > 1 else width)
+    return shape[0], (strides[0] if shape[0] > 1 else width)
 
 
 def _scales_out(gran, rows, k, dev, zero_point=8):
@@ -427,6 +454,10 @@ def fq_kv_plan(lens, new_tokens, block_table, free_pages, pages_used, page_size:
     with _on(stream, lens, new_tokens, block_table, free_pages, pages_used, lens_out, token_start, slots,
              pages_used_out) as s:
         dev = lens.device
+        if lens_out is None and token_start is None and slots is None and pages_used_out is None:
+            # one allocation for the four
+            lens_out, token_start, slots, pages_used_out = torch.empty(
+                2 * r + 2 + max_tokens, dtype=torch.int32, device=dev).split([r, r + 1, max_tokens, 1])
         lens_out = torch.empty(r, dtype=torch.int32, device=dev) if lens_out is None else lens_out
         token_start = torch.empty(r + 1, dtype=torch.int32, device=dev) if token_start is None else token_start
         slots = torch.empty(max_tokens, dtype=torch.int32, device=dev) if slots is None else slots
@@ -508,7 +539,7 @@ def fq_kv_attn(Q, lens, block_table, cache: KVCache, scale: float | None = None,
     if block_table.dim() != 2 or Q.dim() < 2:
         raise ValueError("block_table must be [R, max_pages] and Q [R, Hq, 128] or [R, Hq * 128]")
     _check_shape(block_table, (r, block_table.shape[1]), "block_table")
-    width = Q[0].numel() if Q.shape[0] else 0
+    width = Q.shape[-1] * (Q.shape[1] if Q.dim() == 3 else 1)
     rows, ldq = _check_rows(Q, "Q", width)
     if rows != r or width < 128 or width % 128:
         raise ValueError(f"Q must have {r} rows of Hq * 128 values, got shape {tuple(Q.shape)}")
