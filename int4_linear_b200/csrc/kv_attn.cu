@@ -55,10 +55,10 @@ size_t sync_block_bytes();
 namespace {
 
 constexpr int kTile = 64;           // tokens per tile of the division
-constexpr int kStep = 16;           // tokens per warp and turn
-constexpr int kStepBytes = kStep * kKvTokenBytes;  // K codes, V codes, K scales, V scales
+constexpr int kStep = 32;           // tokens per warp and turn, taken as two halves of 16
 constexpr int kStepV = kStep * kKvRowBytes, kStepKs = 2 * kStepV, kStepVs = kStepKs + 2 * kStep;
-constexpr int kDepth = 6;           // turns in flight per warp
+constexpr int kStepBytes = kStepVs + 2 * kStep;  // K codes, V codes, K scales, V scales
+constexpr int kDepth = 3;           // turns in flight per warp
 constexpr int kWarps = 8;
 constexpr int kAttnThreads = kWarps * 32;
 constexpr int kHeadPad = 164;       // floats of one head's sums in shared memory (see sum_offset)
@@ -110,10 +110,18 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1, const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
@@ -128,14 +136,10 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) 
   asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-// Nibbles at bits 4-7 of each half word (two's complement codes q) -> fp16 72 + q.
-__device__ __forceinline__ uint32_t codes72(uint32_t w) { return and_xor(w, 0x00F000F0u, 0x54805480u); }
-// Nibbles at bits 0-3 of each half word -> fp16 1032 + q.
-__device__ __forceinline__ uint32_t codes1032(uint32_t w) { return and_xor(w, 0x000F000Fu, 0x64086408u); }
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
+// Nibbles of each half word (two's complement codes q) at bits 0-3 and 4-7 -> the fp16 numbers
+// (q + 8) 2^-24 and (q + 8) 2^-20 (subnormal: the nibble is the mantissa).
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return and_xor(w, 0x000F000Fu, 0x00080008u); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return and_xor(w, 0x00F000F0u, 0x00800080u); }
 
 // The token of score row i (0..15): rows 2t, 2t + 1 of one lane's weights.  Bit 0
 // alternates within a row pair (score reads of two rows hit different banks)
@@ -163,7 +167,8 @@ __device__ __forceinline__ int cta_of_tile(long long x, long long total, int C) 
   return int(((x + 1) * C - 1) / total);
 }
 
-template <int NT>
+// NT: tiles of 8 query heads; P16: pages of 16 tokens, so that a turn spans two.
+template <int NT, bool P16>
 __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(const AttnParams p) {
   constexpr int HB = 8 * NT;
   // the warps' turns in flight; between segments the eight warps' sums, [warps][8][kHeadPad]
@@ -231,12 +236,16 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   long long pos = first, before = sm.before;  // next tile; tiles before request r
   const int ps = p.kv.page_shift;
   const int g = lane >> 2, t4 = lane & 3;
-  // what this lane copies of a turn: 16-byte pieces `lane` and 32 + lane of the K and of the V codes
-  // and (lanes 0-3) a piece of the scales
+  // what this lane copies of a turn: every 32nd 16-byte piece of the K and of the V codes, and lanes
+  // 0-7 (pages of 16: 0-3 of each page) a piece of the scales
+  constexpr int kHalves = P16 ? 2 : 1;
+  constexpr int kPieces = P16 ? 2 : 4;        // 512-byte pieces of one kind of codes per page taken
+  constexpr int kScalePieces = P16 ? 2 : 4;   // 16-byte pieces of one kind of scales per page taken
   const uint32_t my_ring = smem_u32(dyn) + uint32_t(warp * kDepth * kStepBytes);
-  const int sc_off = (2 * kKvRowBytes << ps) + (lane & 1) * 16 + ((lane >> 1) & 1) * (2 << ps);
+  const int sc_src = (2 * kKvRowBytes << ps) + (lane % kScalePieces) * 16 + (lane / kScalePieces & 1) * (2 << ps);
+  const uint32_t sc_dst = kStepKs + (lane % kScalePieces) * 16 + (lane / kScalePieces & 1) * (2 * kStep);
   // byte offsets inside a turn of this lane's operands
-  const int row0 = token_of_row(g);           // score rows g and g + 8: tokens row0, row0 + 8
+  const int row0 = token_of_row(g);           // score rows g and g + 8 of a half: tokens row0, row0 + 8
   const uint8_t* ring = dyn + warp * kDepth * kStepBytes;
   const int k_off = row0 * kKvRowBytes + t4 * 16;
   const int va_off = kStepV + token_of_row(2 * t4) * kKvRowBytes + 8 * g;
@@ -255,69 +264,101 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
     const int head = hc / p.chunks, q0 = head * p.G + (hc % p.chunks) * HB;  // first query head
     const int heads = min(HB, p.G - (hc % p.chunks) * HB);
 
-    // ---- this warp's turns: 16 tokens at tok0 + 128 i
+    // ---- this warp's turns: 32 tokens at tok0 + 256 i
     const int tok0 = (s.t0 + ta) * kTile + warp * kStep;
     const int tok_end = min(s.hi, (s.t0 + tb) * kTile);
     const int turns = tok0 < tok_end ? (tok_end - 1 - tok0) / (kWarps * kStep) + 1 : 0;
     const int32_t* row = p.table + static_cast<size_t>(r) * p.max_pages;
-    auto page_id = [&](int i) {
-      const int t = tok0 + i * (kWarps * kStep);
-      return i < turns && t + kStep > s.lo ? __ldg(row + (t >> ps)) : -1;
+    struct Ids {
+      int id[kHalves];
     };
-    uint32_t loaded = 0;  // bit j: the turn fetched j turns ago has its tokens
-    auto fetch = [&](int i, int id, int slot) {
-      const bool ok = id >= 0 && id < p.kv.num_pages;
-      if (ok) {
-        const int off = (tok0 + i * (kWarps * kStep)) & ((1 << ps) - 1);
-        const uint8_t* src = p.kv.block(id, head);
-        const uint32_t dst = my_ring + uint32_t(slot * kStepBytes) + lane * 16;
-        const uint8_t* k = src + off * kKvRowBytes + lane * 16;
-        const uint8_t* v = k + (kKvRowBytes << ps);
-        copy16(dst, k);
-        copy16(dst + 512, k + 512);
-        copy16(dst + kStepV, v);
-        copy16(dst + kStepV + 512, v + 512);
-        if (lane < 4) copy16(dst + kStepKs, src + sc_off + 2 * off);
+    auto page_ids = [&](int i) {
+      Ids v;
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        const int t = tok0 + i * (kWarps * kStep) + 16 * h;
+        const bool in = i < turns && t + (P16 ? 16 : kStep) > s.lo && t < tok_end;
+        v.id[h] = in ? __ldg(row + (t >> ps)) : -1;
       }
-      loaded = (loaded << 1) | uint32_t(ok);
-      copy_commit();
+      return v;
     };
-    int next_id;
-    {
-      int id[kDepth - 1];
+    uint32_t loaded = 0;  // bits 2 j, 2 j + 1: the halves of the turn fetched j turns ago have their tokens
+    auto fetch = [&](int i, const Ids& ids, int slot) {
+      loaded <<= 2;
 #pragma unroll
-      for (int i = 0; i < kDepth - 1; ++i) id[i] = page_id(i);
-      next_id = page_id(kDepth - 1);
+      for (int h = 0; h < kHalves; ++h) {
+        if (ids.id[h] >= 0 && ids.id[h] < p.kv.num_pages) {
+          const int off = P16 ? 0 : (tok0 + i * (kWarps * kStep)) & ((1 << ps) - 1);
+          const uint8_t* src = p.kv.block(ids.id[h], head);
+          const uint32_t dst = my_ring + uint32_t(slot * kStepBytes);
+          const uint8_t* k = src + off * kKvRowBytes + lane * 16;
+          const uint8_t* v = k + (kKvRowBytes << ps);
+          const uint32_t d = dst + h * 1024 + lane * 16;
 #pragma unroll
-      for (int i = 0; i < kDepth - 1; ++i) fetch(i, id[i], i);
-    }
-
-    // queries of this segment, in the order of the nibbles: lane (g, t4) holds head g, dims [32 t4, 32 t4 + 32)
-    uint32_t qf[NT][16];
-    float c0[NT][2];
-#pragma unroll
-    for (int nn = 0; nn < NT; ++nn) {
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (nn * 8 + g < heads)
-          w = *reinterpret_cast<const uint4*>(p.Q + static_cast<long long>(r) * p.ldq +
-                                              (q0 + nn * 8 + g) * kHeadDim + 32 * t4 + 8 * j);
-        qf[nn][4 * j + 0] = __byte_perm(w.x, w.z, 0x5410);  // dims 0, 4
-        qf[nn][4 * j + 1] = __byte_perm(w.x, w.z, 0x7632);  // dims 1, 5
-        qf[nn][4 * j + 2] = __byte_perm(w.y, w.w, 0x5410);  // dims 2, 6
-        qf[nn][4 * j + 3] = __byte_perm(w.y, w.w, 0x7632);  // dims 3, 7
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&qf[nn][4 * j + k]));
-          sum += f.x + f.y;
+          for (int c = 0; c < kPieces; ++c) {
+            copy16(d + 512 * c, k + 512 * c);
+            copy16(d + kStepV + 512 * c, v + 512 * c);
+          }
+          if (lane < 2 * kScalePieces) copy16(dst + sc_dst + h * 32, src + sc_src + 2 * off);
+          loaded |= P16 ? 1u << h : 3u;
         }
       }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      c0[nn][0] = -72.0f * __shfl_sync(0xffffffffu, sum, 8 * t4);
-      c0[nn][1] = -72.0f * __shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
+      copy_commit();
+    };
+    Ids next_ids;
+    {
+      Ids ids[kDepth - 1];
+#pragma unroll
+      for (int i = 0; i < kDepth - 1; ++i) ids[i] = page_ids(i);
+      next_ids = page_ids(kDepth - 1);
+#pragma unroll
+      for (int i = 0; i < kDepth - 1; ++i) fetch(i, ids[i], i);
+    }
+
+    // queries of this segment in 16-bit fixed point, two signed bytes: q = unit (256 hi + lo).  Lane
+    // (g, t4) holds head g, dims [32 t4, 32 t4 + 32): the even dims of 8 in one word, the odd ones in the next
+    uint32_t qf[NT][2][8];
+    float unit[NT][2];  // of heads 2 t4, 2 t4 + 1, times the score's scale and 1/16 (a nibble is taken 16-fold)
+#pragma unroll
+    for (int nn = 0; nn < NT; ++nn) {
+      uint4 w[4];
+      __half2 m2 = __float2half2_rn(0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = make_uint4(0, 0, 0, 0);
+        if (nn * 8 + g < heads)
+          w[j] = *reinterpret_cast<const uint4*>(p.Q + static_cast<long long>(r) * p.ldq +
+                                                 (q0 + nn * 8 + g) * kHeadDim + 32 * t4 + 8 * j);
+        const __half2* h2 = reinterpret_cast<const __half2*>(&w[j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m2 = __hmax2(m2, __habs2(h2[k]));
+      }
+      float mq = __half2float(__hmax(__low2half(m2), __high2half(m2)));
+      mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 1));
+      mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 2));
+      const float inv = mq > 0.f ? 32639.0f / mq : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __half2* h2 = reinterpret_cast<const __half2*>(&w[j]);
+        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = __half22float2(h2[k]);
+          const int ev = __float2int_rn(f.x * inv), od = __float2int_rn(f.y * inv);
+          const int eh = (ev + 128) >> 8, oh = (od + 128) >> 8;
+          hi[0] |= (uint32_t(eh) & 255u) << (8 * k);
+          hi[1] |= (uint32_t(oh) & 255u) << (8 * k);
+          lo[0] |= (uint32_t(ev) & 255u) << (8 * k);
+          lo[1] |= (uint32_t(od) & 255u) << (8 * k);
+        }
+        qf[nn][0][2 * j] = hi[0];
+        qf[nn][0][2 * j + 1] = hi[1];
+        qf[nn][1][2 * j] = lo[0];
+        qf[nn][1][2 * j + 1] = lo[1];
+      }
+      const float u = mq * (p.scale_log2 / (16.0f * 32639.0f));
+      unit[nn][0] = __shfl_sync(0xffffffffu, u, 8 * t4);
+      unit[nn][1] = __shfl_sync(0xffffffffu, u, 8 * t4 + 4);
     }
     float o[NT][8][4];
     float m[NT][2], l[NT][2];
@@ -337,67 +378,80 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       copy_wait<kDepth - 2>();
       __syncwarp();  // every lane's copies of this turn, and every lane is done with the last one
       {
-        const int id = next_id;
-        next_id = page_id(i + kDepth);
-        fetch(i + kDepth - 1, id, slot == 0 ? kDepth - 1 : slot - 1);
+        const Ids ids = next_ids;
+        next_ids = page_ids(i + kDepth);
+        fetch(i + kDepth - 1, ids, slot == 0 ? kDepth - 1 : slot - 1);
       }
       const uint8_t* sp = ring + slot * kStepBytes;
       slot = slot == kDepth - 1 ? 0 : slot + 1;
-      if (!((loaded >> (kDepth - 1)) & 1u)) continue;
-      const uint4 k0 = *reinterpret_cast<const uint4*>(sp + k_off);
-      const uint4 k1 = *reinterpret_cast<const uint4*>(sp + k_off + 8 * kKvRowBytes);
-      float ks0 = __half2float(*reinterpret_cast<const __half*>(sp + kStepKs + 2 * row0)) * p.scale_log2;
-      float ks1 = __half2float(*reinterpret_cast<const __half*>(sp + kStepKs + 2 * row0 + 16)) * p.scale_log2;
-      float vs0 = __half2float(*reinterpret_cast<const __half*>(sp + kStepVs + 2 * row0));
-      float vs1 = __half2float(*reinterpret_cast<const __half*>(sp + kStepVs + 2 * row0 + 16));
-      float sc[NT][4];
+      const uint32_t have = (loaded >> (2 * (kDepth - 1))) & 3u;
+      if (have == 0u) continue;
+      // scores of the 32 tokens: rows g, g + 8 of both halves
+      float sc[2][NT][4], ks[2][2], vs[2][2];
 #pragma unroll
-      for (int nn = 0; nn < NT; ++nn) {
-        sc[nn][0] = sc[nn][2] = c0[nn][0];
-        sc[nn][1] = sc[nn][3] = c0[nn][1];
-      }
-      const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
+      for (int h = 0; h < 2; ++h) {
+        const uint4 k0 = *reinterpret_cast<const uint4*>(sp + k_off + h * 1024);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(sp + k_off + h * 1024 + 8 * kKvRowBytes);
+        const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
+        int ah[NT][4], al[NT][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t a[4] = {codes72(kw0[j] << 4), codes72(kw1[j] << 4), codes72(kw0[j]), codes72(kw1[j])};
-        const uint32_t b[4] = {codes72(kw0[j] >> 4), codes72(kw1[j] >> 4), codes72(kw0[j] >> 8), codes72(kw1[j] >> 8)};
+        for (int nn = 0; nn < NT; ++nn)
 #pragma unroll
-        for (int nn = 0; nn < NT; ++nn) {
-          mma_f16(sc[nn], a, qf[nn][4 * j], qf[nn][4 * j + 1]);
-          mma_f16(sc[nn], b, qf[nn][4 * j + 2], qf[nn][4 * j + 3]);
+          for (int k = 0; k < 4; ++k) ah[nn][k] = al[nn][k] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t e0, d0, e1, d1;  // 16 q of the even and odd dims of rows g and g + 8
+          unpack8_hi(kw0[j], e0, d0);
+          unpack8_hi(kw1[j], e1, d1);
+#pragma unroll
+          for (int nn = 0; nn < NT; ++nn) {
+            mma_s8(ah[nn], e0, e1, d0, d1, qf[nn][0][2 * j], qf[nn][0][2 * j + 1]);
+            mma_s8(al[nn], e0, e1, d0, d1, qf[nn][1][2 * j], qf[nn][1][2 * j + 1]);
+          }
+        }
+#pragma unroll
+        for (int nn = 0; nn < NT; ++nn)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sc[h][nn][k] = float(ah[nn][k] * 256 + al[nn][k]) * unit[nn][k & 1];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          ks[h][k] = __half2float(*reinterpret_cast<const __half*>(sp + kStepKs + 2 * (row0 + 16 * h + 8 * k)));
+          vs[h][k] = __half2float(*reinterpret_cast<const __half*>(sp + kStepVs + 2 * (row0 + 16 * h + 8 * k)));
         }
       }
       const int at = tok0 + i * (kWarps * kStep);
-      if (at < s.lo || at + kStep > s.hi) {
+      if (at < s.lo || at + kStep > s.hi || have != 3u) {
         // what is masked scores -inf and weighs 0, whatever its scales hold
-        const bool ok0 = at + row0 >= s.lo && at + row0 < s.hi;
-        const bool ok1 = at + row0 + 8 >= s.lo && at + row0 + 8 < s.hi;
-        ks0 = ok0 ? ks0 : 1.0f;
-        ks1 = ok1 ? ks1 : 1.0f;
-        vs0 = ok0 ? vs0 : 0.0f;
-        vs1 = ok1 ? vs1 : 0.0f;
 #pragma unroll
-        for (int nn = 0; nn < NT; ++nn) {
-          sc[nn][0] = ok0 ? sc[nn][0] : -INFINITY;
-          sc[nn][1] = ok0 ? sc[nn][1] : -INFINITY;
-          sc[nn][2] = ok1 ? sc[nn][2] : -INFINITY;
-          sc[nn][3] = ok1 ? sc[nn][3] : -INFINITY;
-        }
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int t = at + row0 + 16 * h + 8 * k;
+            const bool ok = t >= s.lo && t < s.hi && ((have >> h) & 1u);
+            ks[h][k] = ok ? ks[h][k] : 1.0f;
+            vs[h][k] = ok ? vs[h][k] : 0.0f;
+#pragma unroll
+            for (int nn = 0; nn < NT; ++nn) {
+              sc[h][nn][2 * k] = ok ? sc[h][nn][2 * k] : -INFINITY;
+              sc[h][nn][2 * k + 1] = ok ? sc[h][nn][2 * k + 1] : -INFINITY;
+            }
+          }
       }
       // log2 of the weights before the v scale, and whether one passes its reference by too much
-      float x[NT][4];
-      bool move = fmaxf(vs0, vs1) > vcap;
+      const float vtop = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
+      float x[2][NT][4], top = -INFINITY;
 #pragma unroll
-      for (int nn = 0; nn < NT; ++nn) {
-        x[nn][0] = __fmaf_rn(sc[nn][0], ks0, -m[nn][0]);
-        x[nn][1] = __fmaf_rn(sc[nn][1], ks0, -m[nn][1]);
-        x[nn][2] = __fmaf_rn(sc[nn][2], ks1, -m[nn][0]);
-        x[nn][3] = __fmaf_rn(sc[nn][3], ks1, -m[nn][1]);
-        move |= fmaxf(fmaxf(x[nn][0], x[nn][1]), fmaxf(x[nn][2], x[nn][3])) > kSlack;
-      }
-      if (__any_sync(0xffffffffu, move)) {
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nn = 0; nn < NT; ++nn)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[h][nn][k] = __fmaf_rn(sc[h][nn][k], ks[h][k >> 1], -m[nn][k & 1]);
+            top = fmaxf(top, x[h][nn][k]);
+          }
+      if (__any_sync(0xffffffffu, top > kSlack || vtop > vcap)) {
         // new references: the largest score of each head, the largest v scale
-        float vm = fmaxf(fmaxf(vs0, vs1), vcap);
+        float vm = fmaxf(vtop, vcap);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, d));
         const float vf = vm > 0.f ? vcap / vm : 0.f;
@@ -407,13 +461,19 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
         for (int nn = 0; nn < NT; ++nn) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float mx = fmaxf(m[nn][k], fmaxf(sc[nn][k] * ks0, sc[nn][k + 2] * ks1));
+            float mx = m[nn][k];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mx = fmaxf(mx, fmaxf(sc[h][nn][k] * ks[h][0], sc[h][nn][k + 2] * ks[h][1]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
             const float f = exp2_approx(m[nn][k] - mx);
             m[nn][k] = mx;
-            x[nn][k] = __fmaf_rn(sc[nn][k], ks0, -mx);
-            x[nn][k + 2] = __fmaf_rn(sc[nn][k + 2], ks1, -mx);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              x[h][nn][k] = __fmaf_rn(sc[h][nn][k], ks[h][0], -mx);
+              x[h][nn][k + 2] = __fmaf_rn(sc[h][nn][k + 2], ks[h][1], -mx);
+            }
             l[nn][k] *= f;
 #pragma unroll
             for (int i8 = 0; i8 < 8; ++i8) {
@@ -423,37 +483,48 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
           }
         }
       }
-      uint32_t w0[NT], w1[NT];
-      const float v0 = vs0 * vinv, v1 = vs1 * vinv;
 #pragma unroll
-      for (int nn = 0; nn < NT; ++nn) {
-        const float p0 = exp2_approx(x[nn][0]), p1 = exp2_approx(x[nn][1]);
-        const float p2 = exp2_approx(x[nn][2]), p3 = exp2_approx(x[nn][3]);
-        l[nn][0] += p0 + p2;
-        l[nn][1] += p1 + p3;
-        const __half2 a = __floats2half2_rn(p0 * v0, p1 * v0), b = __floats2half2_rn(p2 * v1, p3 * v1);
-        w0[nn] = transpose8x8(*reinterpret_cast<const uint32_t*>(&a));
-        w1[nn] = transpose8x8(*reinterpret_cast<const uint32_t*>(&b));
-      }
-      // values: lane (g, t4) holds dims [16 g, 16 g + 16) of its four tokens
-      const uint2 x0 = *reinterpret_cast<const uint2*>(sp + va_off);
-      const uint2 x1 = *reinterpret_cast<const uint2*>(sp + vb_off);
-      const uint2 x2 = *reinterpret_cast<const uint2*>(sp + va_off + 8 * kKvRowBytes);
-      const uint2 x3 = *reinterpret_cast<const uint2*>(sp + vb_off + 8 * kKvRowBytes);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {  // four dims: half word j of the 16 dims
-        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-        const uint32_t y0 = __byte_perm(j < 2 ? x0.x : x0.y, j < 2 ? x1.x : x1.y, sel);
-        const uint32_t y1 = __byte_perm(j < 2 ? x2.x : x2.y, j < 2 ? x3.x : x3.y, sel);
-        const uint32_t a[4] = {hsub2(codes1032(y0), 0x64086408u), hsub2(codes72(y0), 0x54805480u),
-                               hsub2(codes1032(y1), 0x64086408u), hsub2(codes72(y1), 0x54805480u)};
-        const uint32_t z0 = y0 >> 8, z1 = y1 >> 8;
-        const uint32_t b[4] = {hsub2(codes1032(z0), 0x64086408u), hsub2(codes72(z0), 0x54805480u),
-                               hsub2(codes1032(z1), 0x64086408u), hsub2(codes72(z1), 0x54805480u)};
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w0[NT], w1[NT];
+        float c8[NT][4];  // -8 sum(w): rows g in the units of codes_lo, rows g + 8 of codes_hi
+        const float v0 = vs[h][0] * vinv, v1 = vs[h][1] * vinv;
 #pragma unroll
         for (int nn = 0; nn < NT; ++nn) {
-          mma_f16(o[nn][2 * j], a, w0[nn], w1[nn]);      // dims 4 j (rows g), 4 j + 1 (rows g + 8)
-          mma_f16(o[nn][2 * j + 1], b, w0[nn], w1[nn]);  // dims 4 j + 2, 4 j + 3
+          const float p0 = exp2_approx(x[h][nn][0]), p1 = exp2_approx(x[h][nn][1]);
+          const float p2 = exp2_approx(x[h][nn][2]), p3 = exp2_approx(x[h][nn][3]);
+          l[nn][0] += p0 + p2;
+          l[nn][1] += p1 + p3;
+          const __half2 a = __floats2half2_rn(p0 * v0, p1 * v0), b = __floats2half2_rn(p2 * v1, p3 * v1);
+          w0[nn] = transpose8x8(*reinterpret_cast<const uint32_t*>(&a));
+          w1[nn] = transpose8x8(*reinterpret_cast<const uint32_t*>(&b));
+          const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+          // -2^-21 = -8 2^-24 and -2^-17 = -8 2^-20 as fp16
+          mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w0[nn], w1[nn], zero);
+        }
+        // values: lane (g, t4) holds dims [16 g, 16 g + 16) of its four tokens
+        const uint2 x0 = *reinterpret_cast<const uint2*>(sp + va_off + h * 1024);
+        const uint2 x1 = *reinterpret_cast<const uint2*>(sp + vb_off + h * 1024);
+        const uint2 x2 = *reinterpret_cast<const uint2*>(sp + va_off + h * 1024 + 8 * kKvRowBytes);
+        const uint2 x3 = *reinterpret_cast<const uint2*>(sp + vb_off + h * 1024 + 8 * kKvRowBytes);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // four dims: half word j of the 16 dims
+          const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+          const uint32_t y0 = __byte_perm(j < 2 ? x0.x : x0.y, j < 2 ? x1.x : x1.y, sel);
+          const uint32_t y1 = __byte_perm(j < 2 ? x2.x : x2.y, j < 2 ? x3.x : x3.y, sel);
+          const uint32_t z0 = y0 >> 8, z1 = y1 >> 8;
+          // dims 4 j (rows g, in units of 2^-24), 4 j + 1 (rows g + 8, 2^-20); 4 j + 2, 4 j + 3
+          const uint32_t a0 = codes_lo(y0), a1 = codes_hi(y0), a2 = codes_lo(y1), a3 = codes_hi(y1);
+          const uint32_t b0 = codes_lo(z0), b1 = codes_hi(z0), b2 = codes_lo(z1), b3 = codes_hi(z1);
+#pragma unroll
+          for (int nn = 0; nn < NT; ++nn) {
+            float d[4];
+            mma_f16(d, a0, a1, a2, a3, w0[nn], w1[nn], c8[nn]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[nn][2 * j][k] += d[k];
+            mma_f16(d, b0, b1, b2, b3, w0[nn], w1[nn], c8[nn]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[nn][2 * j + 1][k] += d[k];
+          }
         }
       }
     }
@@ -487,12 +558,13 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm.m[w][nn * 8 + 2 * t4 + k]);
         const float f = exp2_approx(m[nn][k] - mx) * (vcap * (1.0f / kWeightScale));
+        const float flo = f * 0x1p24f, fhi = f * 0x1p20f;  // rows g hold 2^-24, rows g + 8 2^-20 of the sums
         float* dst = sums + (warp * 8 + 2 * t4 + k) * kHeadPad;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int d = 4 * (i >> 1) + 2 * (i & 1);
-          dst[sum_offset(g, d)] = o[nn][i][k] * f;
-          dst[sum_offset(g, d + 1)] = o[nn][i][k + 2] * f;
+          dst[sum_offset(g, d)] = o[nn][i][k] * flo;
+          dst[sum_offset(g, d + 1)] = o[nn][i][k + 2] * fhi;
         }
       }
       __syncthreads();
@@ -575,9 +647,9 @@ static_assert(kAttnSmem >= size_t(kWarps) * 8 * kHeadPad * sizeof(float), "the s
 int attn_nt(int G) { return G > 8 ? 2 : 1; }
 int attn_grid(int nt) { return sm_count() * (nt == 1 ? 2 : 1); }
 
-template <int NT>
+template <int NT, bool P16>
 fq_status launch_attn(const AttnParams& p, cudaStream_t stream) {
-  auto kern = kv_attn_kernel<NT>;
+  auto kern = kv_attn_kernel<NT, P16>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kAttnSmem)) != cudaSuccess)
     return fail(FQ_ERR_CUDA, "cannot reserve %zu bytes of shared memory", kAttnSmem);
   launch_pdl(kern, dim3(attn_grid(NT)), dim3(kAttnThreads), kAttnSmem, stream, p);
@@ -633,8 +705,10 @@ fq_status fq_kv_attn(const uint16_t* Q, long long ldq, int R, int Hq, const int3
   p.Y = reinterpret_cast<__half*>(Y);
   p.count = static_cast<unsigned*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + fq::sync_block_bytes());
-  return nt == 1 ? fq::launch_attn<1>(p, static_cast<cudaStream_t>(stream))
-                 : fq::launch_attn<2>(p, static_cast<cudaStream_t>(stream));
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const bool p16 = cache->page_size == 16;
+  if (nt == 1) return p16 ? fq::launch_attn<1, true>(p, cs) : fq::launch_attn<1, false>(p, cs);
+  return p16 ? fq::launch_attn<2, true>(p, cs) : fq::launch_attn<2, false>(p, cs);
 }
 
 }  // extern "C"

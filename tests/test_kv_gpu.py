@@ -4,20 +4,23 @@ Block tables, slots, codes, scales and what is read back are whole numbers or
 single roundings: compared bit for bit.
 
 Attention.  Per output, with p the exact weights and v the cached values:
-* the score's products are summed in float32 by eight matrix instructions of
-  17 terms, none above C = 72 sum|q| (the accumulator starts there), each term
-  off by at most 2^-24 C: |ds| <= 8 * 17 * 2^-24 C ks scale, ks the largest K
-  scale; the softmax then moves each weight by a factor within
-  exp(+-2 |ds|), the output by at most (exp(2 |ds|) - 1) sum p|v|;
+* the queries enter as 16-bit fixed point, half a step of qmax / 65278 off each,
+  and the integer sums are exact: |ds| <= scale (qmax / 65278) sum|k| <= scale (qmax / 65278) 128 * 8 ks,
+  ks the largest K scale, and four float32 roundings of the score; the softmax
+  then moves each weight by a factor within exp(+-2 |ds|), the output by at
+  most (exp(2 |ds|) - 1) sum p|v|;
 * a weight is rounded to fp16 (2^-11 relative), its two exponentials and
   products to float32 (16 * 2^-24 taken): (2^-11 + 2^-20) sum p|v|, and 2^-33 of the
   largest for each of n weights that fall below fp16's normal range: n 2^-33 max|v|;
-* the sums over n tokens add n 2^-24 sum p|v| at most;
+* the codes are summed as code + 8 and 8 sum(w) is taken off, 16 tokens at a
+  time: 17 terms below 16 w vs each, cut at 2^-23 of the largest, i.e. at most
+  17 * 16 * 2^-23 vs in all (the weights sum to 1), vs the largest V scale; the
+  float32 sums over n tokens add n 2^-24 sum p|v| at most;
 * the output's own rounding: 2^-11 |y|, and 2^-25 below fp16's normal range.
 On top of these worst cases the roundings to fp16 are independent, so the
 root mean square of the error stays under 2^-11 of the root mean square of
 y^2 + sum p^2 v^2 (each is at most 2^-11 / sqrt(3) of its term), plus the
-score's error with its 136 terms taken as independent.
+score's error with its 128 terms taken as independent.
 """
 import numpy as np
 import pytest
@@ -232,19 +235,20 @@ def attn_case(seed, lens, hq, h, page, spread=1.0, extra_pages=2, qstd=1.0):
 def check_attn(y, q, lens, table, pool, scale, window=0):
     ref, sa, sq, kmax = KO.attention(q, lens, table, pool, scale, window)
     y = y.cpu().numpy().astype(np.float64).reshape(ref.shape)
-    qa = np.abs(q.astype(np.float64)).sum(-1)                      # sum |q| of each query
-    # the largest K scale: codes reach 8, the oracle gives max|k| / 4 >= 2 * that when a code is 8 or -8
-    ds = 8 * 17 * 2.0 ** -24 * 72 * qa * kmax[:, None] * abs(scale)
+    qm, qa = np.abs(q.astype(np.float64)).max(-1), np.abs(q.astype(np.float64)).sum(-1)
+    # the oracle's max|k| / 4 is at least 2 ks when a code is 8 or -8, and ks from codes of 4 on
+    ks = kmax[:, None] * abs(scale)
+    ds = qm / 65278 * 128 * 8 * ks + 4 * 2.0 ** -24 * 8 * qa * ks
     n = min(max(int(max(lens)), 1), table.shape[1] * (pool.shape[2] // 132))
     vs = KO.views(pool)[3].astype(np.float64)
     vmax = 8 * np.abs(vs[np.isfinite(vs)]).max()
     tol = (np.expm1(2 * ds)[..., None] + 2.0 ** -11 + 2.0 ** -20 + n * 2.0 ** -24) * sa
-    tol += n * 2.0 ** -33 * vmax + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25
+    tol += (n * 2.0 ** -33 + 17 * 16 * 2.0 ** -23 / 8) * vmax + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25
     err = np.abs(y - ref)
     assert np.isfinite(y).all()
     assert (err <= tol).all(), f"worst {np.max(err / tol):.3f} of the bound"
-    dr = ds / np.sqrt(136.0)
-    rms = np.sqrt((ref ** 2 + sq ** 2).mean()) * 2.0 ** -11 + np.sqrt(((2 * dr[..., None] * sq * 1.5) ** 2).mean())
+    dr = qm / 65278 / np.sqrt(3) * np.sqrt(128) * 8 * ks
+    rms = np.sqrt((ref ** 2 + sq ** 2).mean()) * 2.0 ** -11 + np.sqrt(((2 * dr[..., None] * sq) ** 2).mean())
     assert np.sqrt((err ** 2).mean()) <= rms + 2.0 ** -25, (np.sqrt((err ** 2).mean()), rms)
 
 
