@@ -10,18 +10,18 @@
 // 256 nibbles into operands alone takes 10, so the layout below moves no operand
 // through shuffles or a second pass of shared memory.
 //
-// Division.  The tiles (64 tokens of one request and key-value head) of all
+// Division.  The turns (32 tokens of one request and key-value head) of all
 // requests form one sequence, request-major; every CTA takes an equal contiguous
-// part of it, found on the GPU from the lengths, so ragged batches load every SM
-// alike and a captured launch follows the lengths of its replay.  A part is a run of
-// segments (one request and head each).  A segment that covers its whole
-// request is finished by its CTA; otherwise the CTA leaves (sum, m, l) in the
-// workspace, and the CTA that arrives last adds the parts in their fixed order
-// (the sums come out the same whichever CTA that is).
-//
-// In a CTA eight warps take 16 tokens each in turn, each with its own m, l and sum,
-// joined per segment through shared memory.  A warp brings its own tokens
-// with 16-byte asynchronous copies several turns ahead and waits for nobody else's.
+// part of it and every warp an equal contiguous part of that, found on the GPU from the lengths, so
+// ragged batches load every SM alike and a captured launch follows the lengths
+// of its replay.  A warp's part is a run of segments (one request and head each) that it
+// streams on its own, with 16-byte asynchronous copies one turn ahead.  A segment that
+// covers its whole request leaves as output at once; a first one that continues an earlier warp's
+// goes to shared memory, a last one that is cut off stays in registers, and when all
+// warps are done the pieces are added in order.  What still lacks pieces of other CTAs
+// goes to the workspace as (sum, m, l), and the CTA that arrives last adds these in
+// their fixed order (the sums come out the same whichever CTA that is).  With one
+// join of the warps per CTA instead of one per segment, ragged batches lost a third of their time.
 //
 // Products: mma.m16n8k16 (fp16, float32 sums).  The tensor-memory path needs
 // 128 rows of queries, and a request has G = Hq / H <= 16 of them per head, so its
@@ -54,18 +54,19 @@ size_t sync_block_bytes();
 
 namespace {
 
-constexpr int kTile = 64;           // tokens per tile of the division
-constexpr int kStep = 32;           // tokens per warp and turn, taken as two halves of 16
+constexpr int kStep = 32;           // tokens per turn, taken as two halves of 16
 constexpr int kStepV = kStep * kKvRowBytes, kStepKs = 2 * kStepV, kStepVs = kStepKs + 2 * kStep;
 constexpr int kStepBytes = kStepVs + 2 * kStep;  // K codes, V codes, K scales, V scales
-constexpr int kDepth = 3;           // turns in flight per warp
+constexpr int kDepth = 2;           // turns of a warp in shared memory: one taken, one under way
+constexpr int kItemCost = 1;        // what a request and head costs besides its turns, in turns
+constexpr int kMinUnits = 40;       // least units of a CTA's part, where the work is small
 constexpr int kWarps = 8;
 constexpr int kAttnThreads = kWarps * 32;
-constexpr int kHeadPad = 164;       // floats of one head's sums in shared memory (see sum_offset)
 constexpr int kMaxAttnR = 16384;
 constexpr float kSlack = 7.0f;      // log2 of how far a score may pass the reference
 constexpr float kLowest = -1e30f;   // the reference before the first score
 constexpr float kWeightScale = 256.0f;
+constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it leaves a rounded integer in the low bits
 
 struct AttnParams {
   const __half* Q;
@@ -83,14 +84,18 @@ struct AttnParams {
 };
 
 struct AttnSmem {
-  int r0;                           // the request this CTA starts in, and the tiles before that request
-  long long before;
+  long long pre[kAttnThreads + 1];  // units of one head before each thread's run of requests
   long long wsum[kWarps];
-  float m[kWarps][16], l[kWarps][16];
-  int join;
+  // pieces of requests and heads: 0 a warp's first segment, if it continues an earlier warp's, 1 its last
+  // one, if it is cut off.  item: the first unit of the request and head, -1: no piece
+  long long item[kWarps][2];
+  int ends;                         // bit w: piece 0 of warp w reaches the end of its request
+  int row[kWarps][2], heads[kWarps][2], turns[kWarps][2];  // its first row of Y, heads, turns of the whole
+  float m[kWarps][2][16], l[kWarps][2][16];
+  int join[2], left[2];             // parts this CTA has left and is the last to: 0 continued, 1 started here
 };
 
-// Tiles [t0, t1) and tokens [lo, hi) of request r.
+// Turns [t0, t1) and tokens [lo, hi) of request r.
 struct Span {
   int lo, hi, t0, t1;
 };
@@ -99,9 +104,15 @@ __device__ __forceinline__ Span span_of(const AttnParams& p, int r) {
   Span s;
   s.hi = int(min(static_cast<long long>(max(p.len[r], 0)), cap));
   s.lo = p.window > 0 ? max(0, s.hi - p.window) : 0;
-  s.t0 = s.lo / kTile;
-  s.t1 = s.hi > s.lo ? (s.hi - 1) / kTile + 1 : s.t0;
+  s.t0 = s.lo / kStep;
+  s.t1 = s.hi > s.lo ? (s.hi - 1) / kStep + 1 : s.t0;
   return s;
+}
+
+// a / b of non-negative numbers, in 32 bits where they fit.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return uint32_t(a) / uint32_t(b);
+  return a / b;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -130,6 +141,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
+// The same byte of four words, by a byte selection of two words at a time.
+__device__ __forceinline__ uint32_t bytes4(const uint32_t (&v)[4], uint32_t sel) {
+  return __byte_perm(__byte_perm(v[0], v[1], sel), __byte_perm(v[2], v[3], sel), 0x5410);
+}
+
 // (a & b) ^ c in one logic operation.
 __device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
@@ -149,9 +165,10 @@ __device__ __forceinline__ int token_of_row(int i) {
   return (b ^ (t & 1)) | ((t & 1) << 1) | ((t >> 1) << 2) | (i & 8);
 }
 
-// Where dim 16 g + d of a head's sums lies in shared memory: lanes with
-// consecutive g write, and lanes with consecutive (d / 4, g) read, distinct banks.
-__device__ __forceinline__ int sum_offset(int g, int d) { return d * 8 + (d >> 2) * 8 + g; }
+// Where value k (of 4) of product i (of 8) of a lane lies in a kept piece: lanes write consecutive
+// words, and the lanes of a warp that read one head's values (see the adding of pieces) find 32 banks.
+constexpr int kPieceFloats = 32 * 32 + 4;
+__device__ __forceinline__ int piece_offset(int i, int k, int lane) { return (4 * i + k) * 32 + lane + (i >> 1); }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -162,31 +179,99 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The CTA whose part holds tile x of the sequence: parts are [total c / C, total (c + 1) / C).
-__device__ __forceinline__ int cta_of_tile(long long x, long long total, int C) {
-  return int(((x + 1) * C - 1) / total);
+// The CTA whose part holds unit x of the sequence: parts are [total c / C, total (c + 1) / C).
+__device__ __forceinline__ int cta_of_unit(long long x, long long total, int C) {
+  return int(divide((x + 1) * C - 1, total));
+}
+
+// The parts of one request and head, left by CTAs c_first .. c_first + parts - 1, added in that
+// order and written as `heads` rows of Y.  A warp takes one head, or, with four heads or
+// fewer, one head's every second (fourth, eighth) part; the loads of eight parts
+// are under way at a time.
+template <int HB>
+__device__ __noinline__ void join_parts(const float* all, int c_first, int parts, int heads, float* sums, __half* Y) {
+  constexpr size_t kSlot = static_cast<size_t>(HB) * (kHeadDim + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub_n = heads <= 1 ? 8 : heads <= 2 ? 4 : heads <= 4 ? 2 : 1;
+  auto slot = [&](int c) { return all + (2 * static_cast<size_t>(c_first + c) + (c == 0)) * kSlot; };
+  for (int hh = warp / sub_n; hh < heads; hh += kWarps / sub_n) {
+    const int sub = warp % sub_n;
+    float mx = kLowest;
+    for (int c = lane; c < parts; c += 32) mx = fmaxf(mx, __ldcg(slot(c) + HB * kHeadDim + hh));
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float ls = 0.f;
+    for (int c0 = sub; c0 < parts; c0 += 8 * sub_n) {
+      float4 v[8];
+      float mc[8], lc[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = c0 + k * sub_n;
+        const float* src = slot(min(c, parts - 1));
+        mc[k] = c < parts ? __ldcg(src + HB * kHeadDim + hh) : kLowest;
+        lc[k] = c < parts ? __ldcg(src + HB * kHeadDim + HB + hh) : 0.f;
+        v[k] = c < parts ? __ldcg(reinterpret_cast<const float4*>(src + hh * kHeadDim) + lane)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float f = exp2_approx(mc[k] - mx);
+        ls += lc[k] * f;
+        acc.x += v[k].x * f;
+        acc.y += v[k].y * f;
+        acc.z += v[k].z * f;
+        acc.w += v[k].w * f;
+      }
+    }
+    if (sub_n > 1) {  // at most one head per warp: every warp comes here once or not at all
+      float* mine = sums + warp * (kHeadDim + 4);
+      *reinterpret_cast<float4*>(mine + 4 * lane) = acc;
+      if (lane == 0) mine[kHeadDim] = ls;
+      named_barrier(1 + hh, 32 * sub_n);
+      if (sub != 0) continue;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      ls = 0.f;
+      for (int k = 0; k < sub_n; ++k) {
+        const float* other = sums + (warp + k) * (kHeadDim + 4);
+        const float4 v = *reinterpret_cast<const float4*>(other + 4 * lane);
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+        ls += other[kHeadDim];
+      }
+    }
+    const float inv = ls > 0.f ? 1.0f / ls : 0.f;
+    const __half2 a = __floats2half2_rn(acc.x * inv, acc.y * inv);
+    const __half2 b = __floats2half2_rn(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(Y + hh * kHeadDim + 4 * lane) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
 }
 
 // NT: tiles of 8 query heads; P16: pages of 16 tokens, so that a turn spans two.
 template <int NT, bool P16>
 __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(const AttnParams p) {
   constexpr int HB = 8 * NT;
-  // the warps' turns in flight; between segments the eight warps' sums, [warps][8][kHeadPad]
+  // the warps' turns, then each warp's continued segment, [32 NT values][32 lanes]
   extern __shared__ __align__(128) uint8_t dyn[];
-  float* sums = reinterpret_cast<float*>(dyn);
+  float* sums = reinterpret_cast<float*>(dyn + kWarps * kDepth * kStepBytes);
   __shared__ AttnSmem sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, HC = p.kv.H * p.chunks;
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- this CTA's part: tiles of each thread's run of requests, summed
+  // ---- the sequence: each thread's run of requests, summed (the requests that have tokens counted in
+  // the upper bits)
   const int run = (p.R + kAttnThreads - 1) / kAttnThreads;
   const int ra = min(p.R, tid * run), rb = min(p.R, ra + run);
+  constexpr int kCountBit = 44;
   long long mine = 0;
   for (int r = ra; r < rb; ++r) {
     const Span s = span_of(p, r);
-    mine += s.t1 - s.t0;
+    if (s.t1 > s.t0) mine += (s.t1 - s.t0) + kItemCost + (1ll << kCountBit);
   }
   long long incl = mine;
 #pragma unroll
@@ -195,45 +280,42 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
     if (lane >= o) incl += u;
   }
   if (lane == 31) sm.wsum[warp] = incl;
+  if (lane < 2) sm.item[warp][lane] = -1;
+  if (tid == 0) sm.ends = sm.join[0] = sm.join[1] = 0;
   __syncthreads();
-  long long base = 0, all = 0;
+  long long all = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) base += sm.wsum[w];
+    if (w < warp) incl += sm.wsum[w];
     all += sm.wsum[w];
   }
-  const long long total = all * HC;
-  // few tiles: fewer CTAs, so that a part is worth its join
-  const int C = int(min(static_cast<long long>(gridDim.x), (total + 1) / 2));
-  // requests without tokens
-  for (int r = cta; r < p.R; r += gridDim.x) {
+  constexpr long long kUnits = (1ll << kCountBit) - 1;
+  sm.pre[tid] = (incl - mine) & kUnits;
+  const long long total = (all & kUnits) * HC;
+  // little work: one CTA per request and head, or parts that are worth their join
+  const int C = int(min(static_cast<long long>(gridDim.x),
+                        max((all >> kCountBit) * HC, divide(total + kMinUnits - 1, kMinUnits))));
+  for (int r = cta; r < p.R; r += gridDim.x) {  // requests without tokens
     const Span s = span_of(p, r);
     if (s.t1 == s.t0)
       for (int i = tid; i < p.Hq * kHeadDim / 8; i += kAttnThreads)
         reinterpret_cast<uint4*>(p.Y + static_cast<size_t>(r) * p.Hq * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
   }
   if (cta >= C) return;
-  const long long first = total * cta / C, last = total * (cta + 1) / C;
-  {
-    const long long e0 = (base + incl - mine) * HC, e1 = (base + incl) * HC;
-    if (e0 <= first && first < e1) {
-      long long acc = e0;
-      for (int r = ra; r < rb; ++r) {
-        const Span s = span_of(p, r);
-        const long long n = static_cast<long long>(s.t1 - s.t0) * HC;
-        if (first < acc + n) {
-          sm.r0 = r;
-          sm.before = acc;
-          break;
-        }
-        acc += n;
-      }
-    }
-  }
   __syncthreads();
+  // this CTA's part, this warp's part of it, and the request that one starts in
+  const long long first_c = divide(total * cta, C), last_c = divide(total * (cta + 1), C);
+  const long long first = first_c + (last_c - first_c) * warp / kWarps;
+  const long long last = first_c + (last_c - first_c) * (warp + 1) / kWarps;
+  int wr;
+  long long before;  // units before request wr
+  {
+    const int b8 = 8 * (__popc(__ballot_sync(0xffffffffu, sm.pre[8 * lane] * HC <= first)) - 1);
+    const int t = b8 + __popc(__ballot_sync(0xffffffffu, lane < 8 && sm.pre[b8 + (lane & 7)] * HC <= first)) - 1;
+    wr = t * run;
+    before = sm.pre[t] * HC;
+  }
 
-  int r = sm.r0;
-  long long pos = first, before = sm.before;  // next tile; tiles before request r
   const int ps = p.kv.page_shift;
   const int g = lane >> 2, t4 = lane & 3;
   // what this lane copies of a turn: every 32nd 16-byte piece of the K and of the V codes, and lanes
@@ -250,86 +332,170 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   const int k_off = row0 * kKvRowBytes + t4 * 16;
   const int va_off = kStepV + token_of_row(2 * t4) * kKvRowBytes + 8 * g;
   const int vb_off = kStepV + token_of_row(2 * t4 + 1) * kKvRowBytes + 8 * g;
-  while (pos < last) {
-    const Span s = span_of(p, r);
-    const int nt = s.t1 - s.t0;
-    const long long len_r = static_cast<long long>(nt) * HC;
-    if (pos >= before + len_r) {
-      before += len_r;
-      ++r;
-      continue;
-    }
-    const int hc = int((pos - before) / nt), ta = int((pos - before) % nt);
-    const int tb = int(min(static_cast<long long>(nt), ta + (last - pos)));
-    const int head = hc / p.chunks, q0 = head * p.G + (hc % p.chunks) * HB;  // first query head
-    const int heads = min(HB, p.G - (hc % p.chunks) * HB);
-
-    // ---- this warp's turns: 32 tokens at tok0 + 256 i
-    const int tok0 = (s.t0 + ta) * kTile + warp * kStep;
-    const int tok_end = min(s.hi, (s.t0 + tb) * kTile);
-    const int turns = tok0 < tok_end ? (tok_end - 1 - tok0) / (kWarps * kStep) + 1 : 0;
-    const int32_t* row = p.table + static_cast<size_t>(r) * p.max_pages;
-    struct Ids {
-      int id[kHalves];
-    };
-    auto page_ids = [&](int i) {
-      Ids v;
-#pragma unroll
-      for (int h = 0; h < kHalves; ++h) {
-        const int t = tok0 + i * (kWarps * kStep) + 16 * h;
-        const bool in = i < turns && t + (P16 ? 16 : kStep) > s.lo && t < tok_end;
-        v.id[h] = in ? __ldg(row + (t >> ps)) : -1;
+  // A segment: turns [ta, tb) of the nt turns of a request and head.
+  struct Seg {
+    int r, hc, tok0, turns, nt, ta, lo, hi;
+    long long item0;  // its request and head's first unit
+  };
+  long long pos = first;
+  auto next_segment = [&](Seg& q) {
+    while (pos < last) {
+      const Span s = span_of(p, wr);
+      const int nt = s.t1 - s.t0, units = nt ? nt + kItemCost : 0;
+      const long long len_r = static_cast<long long>(units) * HC;
+      if (pos >= before + len_r) {
+        before += len_r;
+        ++wr;
+        continue;
       }
-      return v;
-    };
-    uint32_t loaded = 0;  // bits 2 j, 2 j + 1: the halves of the turn fetched j turns ago have their tokens
-    auto fetch = [&](int i, const Ids& ids, int slot) {
-      loaded <<= 2;
+      const int hc = int(divide(pos - before, units));
+      const long long item0 = before + static_cast<long long>(hc) * units;
+      const int ta = max(0, int(pos - item0) - kItemCost);
+      const int tb = int(min(static_cast<long long>(units), last - item0)) - kItemCost;
+      pos = min(item0 + units, last);
+      if (tb <= ta) continue;
+      q.r = wr;
+      q.hc = hc;
+      q.item0 = item0;
+      q.nt = nt;
+      q.ta = ta;
+      q.turns = tb - ta;
+      q.lo = s.lo;
+      q.hi = s.hi;
+      q.tok0 = (s.t0 + ta) * kStep;
+      return true;
+    }
+    return false;
+  };
+  struct Ids {
+    int id[kHalves];
+  };
+  auto page_ids = [&](const Seg& q, int i) {
+    Ids v;
 #pragma unroll
-      for (int h = 0; h < kHalves; ++h) {
-        if (ids.id[h] >= 0 && ids.id[h] < p.kv.num_pages) {
-          const int off = P16 ? 0 : (tok0 + i * (kWarps * kStep)) & ((1 << ps) - 1);
-          const uint8_t* src = p.kv.block(ids.id[h], head);
-          const uint32_t dst = my_ring + uint32_t(slot * kStepBytes);
-          const uint8_t* k = src + off * kKvRowBytes + lane * 16;
-          const uint8_t* v = k + (kKvRowBytes << ps);
-          const uint32_t d = dst + h * 1024 + lane * 16;
+    for (int h = 0; h < kHalves; ++h) {
+      const int t = q.tok0 + i * kStep + 16 * h;
+      const bool in = i < q.turns && (!P16 || t + 16 > q.lo) && t < q.hi;
+      v.id[h] = in ? __ldg(p.table + static_cast<size_t>(q.r) * p.max_pages + (t >> ps)) : -1;
+    }
+    return v;
+  };
+  // Copies of turn i into ring slot `to`; returns which halves have their tokens (bits 0, 1).
+  auto fetch = [&](const Seg& q, int i, const Ids& ids, int to) {
+    uint32_t got = 0;
 #pragma unroll
-          for (int c = 0; c < kPieces; ++c) {
-            copy16(d + 512 * c, k + 512 * c);
-            copy16(d + kStepV + 512 * c, v + 512 * c);
-          }
-          if (lane < 2 * kScalePieces) copy16(dst + sc_dst + h * 32, src + sc_src + 2 * off);
-          loaded |= P16 ? 1u << h : 3u;
+    for (int h = 0; h < kHalves; ++h) {
+      if (ids.id[h] >= 0 && ids.id[h] < p.kv.num_pages) {
+        const int off = P16 ? 0 : (q.tok0 + i * kStep) & ((1 << ps) - 1);
+        const uint8_t* src = p.kv.block(ids.id[h], q.hc / p.chunks);
+        const uint32_t dst = my_ring + uint32_t(to * kStepBytes);
+        const uint8_t* k = src + off * kKvRowBytes + lane * 16;
+        const uint8_t* v = k + (kKvRowBytes << ps);
+        const uint32_t d = dst + h * 1024 + lane * 16;
+#pragma unroll
+        for (int c = 0; c < kPieces; ++c) {
+          copy16(d + 512 * c, k + 512 * c);
+          copy16(d + kStepV + 512 * c, v + 512 * c);
         }
+        if (lane < 2 * kScalePieces) copy16(dst + sc_dst + h * 32, src + sc_src + 2 * off);
+        got |= P16 ? 1u << h : 3u;
       }
-      copy_commit();
-    };
-    Ids next_ids;
-    {
-      Ids ids[kDepth - 1];
-#pragma unroll
-      for (int i = 0; i < kDepth - 1; ++i) ids[i] = page_ids(i);
-      next_ids = page_ids(kDepth - 1);
-#pragma unroll
-      for (int i = 0; i < kDepth - 1; ++i) fetch(i, ids[i], i);
     }
+    copy_commit();
+    return got;
+  };
+  // Query heads of a segment: heads [q0, q0 + heads)
+  auto first_head = [&](const Seg& q) { return (q.hc / p.chunks) * p.G + (q.hc % p.chunks) * HB; };
+  auto head_count = [&](const Seg& q) { return min(HB, p.G - (q.hc % p.chunks) * HB); };
+  uint4 raw[NT][4];  // lane (g, t4): head g, dims [32 t4, 32 t4 + 32)
+  auto load_queries = [&](const Seg& q) {
+    const __half* src = p.Q + static_cast<long long>(q.r) * p.ldq + (first_head(q) + g) * kHeadDim + 32 * t4;
+    const int heads = head_count(q);
+#pragma unroll
+    for (int nn = 0; nn < NT; ++nn)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        raw[nn][j] = nn * 8 + g < heads ? *reinterpret_cast<const uint4*>(src + nn * 8 * kHeadDim + 8 * j)
+                                        : make_uint4(0, 0, 0, 0);
+  };
 
-    // queries of this segment in 16-bit fixed point, two signed bytes: q = unit (256 hi + lo).  Lane
-    // (g, t4) holds head g, dims [32 t4, 32 t4 + 32): the even dims of 8 in one word, the odd ones in the next
+  Seg seg;
+  int slot = 0;         // ring slot of the turn to be taken
+  float o[NT][8][4];
+  float m[NT][2], l[NT][2];
+  float vcap = 0.f, vinv = 0.f;  // largest v scale so far, and 2^8 over it
+  bool held = false;             // the last segment is cut off and stays in registers
+  static_assert(NT * kPieceFloats * 4 <= kDepth * kStepBytes, "a piece fits a warp's turns");
+  auto in_units = [&]() {  // rows g hold 2^-24, rows g + 8 2^-20 of the sums, both over 2^8 / vcap
+    const float f = vcap * (1.0f / kWeightScale);
+#pragma unroll
+    for (int nn = 0; nn < NT; ++nn)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          o[nn][i][k] *= f * 0x1p24f;
+          o[nn][i][k + 2] *= f * 0x1p20f;
+        }
+  };
+  // piece 0 of a warp lies behind the turns, piece 1 takes the warp's own turns' bytes
+  auto piece = [&](int w, int which) {
+    return which ? reinterpret_cast<float*>(dyn + w * kDepth * kStepBytes) : sums + w * NT * kPieceFloats;
+  };
+  auto keep = [&](const Seg& q, int which) {
+    float* dst = piece(warp, which);
+#pragma unroll
+    for (int nn = 0; nn < NT; ++nn) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dst[nn * kPieceFloats + piece_offset(i, k, lane)] = o[nn][i][k];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (g == 0) {
+          sm.m[warp][which][nn * 8 + 2 * t4 + k] = m[nn][k];
+          sm.l[warp][which][nn * 8 + 2 * t4 + k] = l[nn][k];
+        }
+    }
+    if (lane == 0) {
+      sm.item[warp][which] = q.item0;
+      sm.row[warp][which] = q.r * p.Hq + first_head(q);
+      sm.heads[warp][which] = head_count(q);
+      sm.turns[warp][which] = q.nt;
+    }
+  };
+  auto write_heads = [&](int r, int q0, int heads) {
+#pragma unroll
+    for (int nn = 0; nn < NT; ++nn)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int hh = nn * 8 + 2 * t4 + k;
+        if (hh >= heads) continue;
+        const float inv = l[nn][k] > 0.f ? 1.0f / l[nn][k] : 0.f;
+        uint32_t v[8];  // dims 16 g + 2 j, 16 g + 2 j + 1
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const __half2 x = __floats2half2_rn(o[nn][j][k] * inv, o[nn][j][k + 2] * inv);
+          v[j] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(p.Y + (static_cast<size_t>(r) * p.Hq + q0 + hh) * kHeadDim + 16 * g);
+        dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+      }
+  };
+  while (next_segment(seg)) {
+    load_queries(seg);
+    Ids next_ids = page_ids(seg, 0);
+    // queries of this segment in 16-bit fixed point, two signed bytes: q = unit (256 hi + lo); the even
+    // dims of 8 in one word, the odd ones in the next
     uint32_t qf[NT][2][8];
     float unit[NT][2];  // of heads 2 t4, 2 t4 + 1, times the score's scale and 1/16 (a nibble is taken 16-fold)
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn) {
-      uint4 w[4];
       __half2 m2 = __float2half2_rn(0.f);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        w[j] = make_uint4(0, 0, 0, 0);
-        if (nn * 8 + g < heads)
-          w[j] = *reinterpret_cast<const uint4*>(p.Q + static_cast<long long>(r) * p.ldq +
-                                                 (q0 + nn * 8 + g) * kHeadDim + 32 * t4 + 8 * j);
-        const __half2* h2 = reinterpret_cast<const __half2*>(&w[j]);
+        const __half2* h2 = reinterpret_cast<const __half2*>(&raw[nn][j]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) m2 = __hmax2(m2, __habs2(h2[k]));
       }
@@ -339,30 +505,25 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       const float inv = mq > 0.f ? 32639.0f / mq : 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const __half2* h2 = reinterpret_cast<const __half2*>(&w[j]);
-        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+        const __half2* h2 = reinterpret_cast<const __half2*>(&raw[nn][j]);
+        uint32_t ev[4], od[4];  // round(q inv) + 128 in the low 16 bits
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = __half22float2(h2[k]);
-          const int ev = __float2int_rn(f.x * inv), od = __float2int_rn(f.y * inv);
-          const int eh = (ev + 128) >> 8, oh = (od + 128) >> 8;
-          hi[0] |= (uint32_t(eh) & 255u) << (8 * k);
-          hi[1] |= (uint32_t(oh) & 255u) << (8 * k);
-          lo[0] |= (uint32_t(ev) & 255u) << (8 * k);
-          lo[1] |= (uint32_t(od) & 255u) << (8 * k);
+          ev[k] = __float_as_uint(__fmaf_rn(f.x, inv, kRound + 128.0f));
+          od[k] = __float_as_uint(__fmaf_rn(f.y, inv, kRound + 128.0f));
         }
-        qf[nn][0][2 * j] = hi[0];
-        qf[nn][0][2 * j + 1] = hi[1];
-        qf[nn][1][2 * j] = lo[0];
-        qf[nn][1][2 * j + 1] = lo[1];
+        // byte 1 is hi; byte 0 is lo + 128
+        qf[nn][0][2 * j] = bytes4(ev, 0x5151u);
+        qf[nn][0][2 * j + 1] = bytes4(od, 0x5151u);
+        qf[nn][1][2 * j] = bytes4(ev, 0x4040u) ^ 0x80808080u;
+        qf[nn][1][2 * j + 1] = bytes4(od, 0x4040u) ^ 0x80808080u;
       }
       const float u = mq * (p.scale_log2 / (16.0f * 32639.0f));
       unit[nn][0] = __shfl_sync(0xffffffffu, u, 8 * t4);
       unit[nn][1] = __shfl_sync(0xffffffffu, u, 8 * t4 + 4);
     }
-    float o[NT][8][4];
-    float m[NT][2], l[NT][2];
-    float vcap = 0.f, vinv = 0.f;  // largest v scale so far, and 2^8 over it
+    vcap = vinv = 0.f;
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn) {
 #pragma unroll
@@ -373,19 +534,19 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       l[nn][0] = l[nn][1] = 0.f;
     }
 
-    int slot = 0;
-    for (int i = 0; i < turns; ++i) {
-      copy_wait<kDepth - 2>();
+    uint32_t coming = 0;  // halves of the turn under way
+    for (int i = -1; i < seg.turns; ++i) {
+      copy_wait<0>();
       __syncwarp();  // every lane's copies of this turn, and every lane is done with the last one
+      const uint32_t have = coming;
       {
         const Ids ids = next_ids;
-        next_ids = page_ids(i + kDepth);
-        fetch(i + kDepth - 1, ids, slot == 0 ? kDepth - 1 : slot - 1);
+        next_ids = page_ids(seg, i + 2);
+        coming = fetch(seg, i + 1, ids, slot ^ 1);
       }
       const uint8_t* sp = ring + slot * kStepBytes;
-      slot = slot == kDepth - 1 ? 0 : slot + 1;
-      const uint32_t have = (loaded >> (2 * (kDepth - 1))) & 3u;
-      if (have == 0u) continue;
+      slot ^= 1;
+      if (have == 0u) continue;  // nothing there, or the first copies have just been sent
       // scores of the 32 tokens: rows g, g + 8 of both halves
       float sc[2][NT][4], ks[2][2], vs[2][2];
 #pragma unroll
@@ -419,15 +580,15 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
           vs[h][k] = __half2float(*reinterpret_cast<const __half*>(sp + kStepVs + 2 * (row0 + 16 * h + 8 * k)));
         }
       }
-      const int at = tok0 + i * (kWarps * kStep);
-      if (at < s.lo || at + kStep > s.hi || have != 3u) {
+      const int at = seg.tok0 + i * kStep;
+      if (at < seg.lo || at + kStep > seg.hi || have != 3u) {
         // what is masked scores -inf and weighs 0, whatever its scales hold
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int t = at + row0 + 16 * h + 8 * k;
-            const bool ok = t >= s.lo && t < s.hi && ((have >> h) & 1u);
+            const bool ok = t >= seg.lo && t < seg.hi && ((have >> h) & 1u);
             ks[h][k] = ok ? ks[h][k] : 1.0f;
             vs[h][k] = ok ? vs[h][k] : 0.0f;
 #pragma unroll
@@ -528,119 +689,113 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
         }
       }
     }
-    copy_wait<0>();
-
-    // ---- the eight warps' parts of the segment
+    __syncwarp();
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float v = l[nn][k];
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-        if (g == 0) {
-          sm.m[warp][nn * 8 + 2 * t4 + k] = m[nn][k];
-          sm.l[warp][nn * 8 + 2 * t4 + k] = v;
-        }
-      }
-    __syncthreads();  // also: every warp is done with its turns, whose bytes the sums take
-    const long long item0 = before + static_cast<long long>(hc) * nt;  // the request and head's tiles in the sequence
-    const bool whole = ta == 0 && tb == nt;
-    const int c_first = cta_of_tile(item0, total, C);
-    const int parts = cta_of_tile(item0 + nt - 1, total, C) - c_first + 1;
-    float* part = p.part + static_cast<size_t>(2 * cta + (ta == 0 ? 1 : 0)) * HB * (kHeadDim + 2);
-#pragma unroll
-    for (int nn = 0; nn < NT; ++nn) {
-      // 1. every warp's sums at the common reference
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float mx = kLowest;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm.m[w][nn * 8 + 2 * t4 + k]);
-        const float f = exp2_approx(m[nn][k] - mx) * (vcap * (1.0f / kWeightScale));
-        const float flo = f * 0x1p24f, fhi = f * 0x1p20f;  // rows g hold 2^-24, rows g + 8 2^-20 of the sums
-        float* dst = sums + (warp * 8 + 2 * t4 + k) * kHeadPad;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int d = 4 * (i >> 1) + 2 * (i & 1);
-          dst[sum_offset(g, d)] = o[nn][i][k] * flo;
-          dst[sum_offset(g, d + 1)] = o[nn][i][k + 2] * fhi;
-        }
-      }
-      __syncthreads();
-      // 2. added over the warps: this thread takes head `warp`, dims 16 (lane % 8) + 4 (lane / 8) + 0..3
-      const int hh = nn * 8 + warp;
-      const int gg = lane & 7, d4 = lane >> 3;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      float mx = kLowest, ls = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float* src = sums + (w * 8 + warp) * kHeadPad;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] += src[sum_offset(gg, 4 * d4 + k)];
-        mx = fmaxf(mx, sm.m[w][hh]);
-      }
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) ls += sm.l[w][hh] * exp2_approx(sm.m[w][hh] - mx);
-      if (hh < heads) {
-        const int dim = 16 * gg + 4 * d4;
-        if (whole) {
-          const float inv = ls > 0.f ? 1.0f / ls : 0.f;
-          const __half2 a = __floats2half2_rn(acc[0] * inv, acc[1] * inv);
-          const __half2 b = __floats2half2_rn(acc[2] * inv, acc[3] * inv);
-          *reinterpret_cast<uint2*>(p.Y + (static_cast<size_t>(r) * p.Hq + q0 + hh) * kHeadDim + dim) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-        } else {
-          *reinterpret_cast<float4*>(part + hh * kHeadDim + dim) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-          if (lane == 0) {
-            part[HB * kHeadDim + hh] = mx;
-            part[HB * kHeadDim + HB + hh] = ls;
-          }
-        }
-      }
-      if (nn + 1 < NT) __syncthreads();
+        for (int d = 4; d < 32; d <<= 1) l[nn][k] += __shfl_xor_sync(0xffffffffu, l[nn][k], d);
+    const bool to_end = seg.ta + seg.turns == seg.nt;
+    in_units();
+    if (seg.ta == 0 && to_end) {
+      write_heads(seg.r, first_head(seg), head_count(seg));
+    } else if (seg.ta > 0) {
+      keep(seg, 0);
+      if (lane == 0 && to_end) atomicOr(&sm.ends, 1 << warp);
+    } else {
+      held = true;  // cut off: this warp's last segment, kept when its turns' bytes are free
     }
-    if (!whole) {
-      // 3. the CTA that arrives last joins the parts, in the order of the CTAs
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) sm.join = atomicInc(&p.count[c_first], unsigned(parts - 1)) == unsigned(parts - 1);
-      __syncthreads();
-      if (sm.join) {
-        __threadfence();
-        const size_t stride = static_cast<size_t>(HB) * (kHeadDim + 2);
-        for (int hh = warp; hh < heads; hh += kWarps) {
-          float mx = kLowest;
-          for (int c = 0; c < parts; ++c)
-            mx = fmaxf(mx, __ldcg(p.part + (2 * (c_first + c) + (c == 0)) * stride + HB * kHeadDim + hh));
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          float ls = 0.f;
-          for (int c = 0; c < parts; ++c) {
-            const float* src = p.part + (2 * (c_first + c) + (c == 0)) * stride;
-            const float f = exp2_approx(__ldcg(src + HB * kHeadDim + hh) - mx);
-            ls += __ldcg(src + HB * kHeadDim + HB + hh) * f;
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + hh * kHeadDim) + lane);
-            acc.x += v.x * f;
-            acc.y += v.y * f;
-            acc.z += v.z * f;
-            acc.w += v.w * f;
-          }
-          const float inv = ls > 0.f ? 1.0f / ls : 0.f;
-          const __half2 a = __floats2half2_rn(acc.x * inv, acc.y * inv);
-          const __half2 b = __floats2half2_rn(acc.z * inv, acc.w * inv);
-          *reinterpret_cast<uint2*>(p.Y + (static_cast<size_t>(r) * p.Hq + q0 + hh) * kHeadDim + 4 * lane) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-        }
-      }
-    }
-    pos += tb - ta;
-    // the next segment's copies and writes to sm follow every warp's reads above
-    __syncthreads();
   }
-}
+  copy_wait<0>();
+  __syncwarp();
+  if (held) keep(seg, 1);
+  __syncthreads();
 
-constexpr size_t kAttnSmem = size_t(kWarps) * kDepth * kStepBytes;
-static_assert(kAttnSmem >= size_t(kWarps) * 8 * kHeadPad * sizeof(float), "the sums take the turns' bytes");
+  // ---- pieces of one request and head, added in the order of the warps.  A group is led by a piece 1, or
+  // by the first piece 0 when that continues an earlier CTA's; a warp takes one head of it.  Lane
+  // 2 w + which knows of piece (w, which).
+  const long long my_item = lane < 2 * kWarps ? sm.item[lane >> 1][lane & 1] : -1;
+  const bool from_before = (lane & 1) == 0 && my_item >= 0 && my_item + kItemCost < first_c;
+  const uint32_t before_mask = __ballot_sync(0xffffffffu, from_before);
+  // all pieces 0 from before are of one request and head: the first leads
+  uint32_t leads = __ballot_sync(0xffffffffu, (lane & 1) && my_item >= 0) | (before_mask & -before_mask);
+  const int my_ends = sm.ends;
+#pragma unroll 1
+  for (; leads; leads &= leads - 1) {
+    const int lead = __ffs(leads) - 1, lw = lead >> 1, which = lead & 1;
+    const long long item0 = __shfl_sync(0xffffffffu, my_item, lead);
+    const bool member = my_item == item0 && ((lane & 1) ? lane == lead : lane >= lead);
+    const uint32_t members = __ballot_sync(0xffffffffu, member);
+    const bool complete = which && __any_sync(0xffffffffu, member && !(lane & 1) && ((my_ends >> (lane >> 1)) & 1));
+    const int heads = sm.heads[lw][which], row = sm.row[lw][which];
+    float* part = p.part + static_cast<size_t>(2 * cta + which) * HB * (kHeadDim + 2);
+#pragma unroll 1
+    for (int hh = warp; hh < heads; hh += kWarps) {
+      const float mo = member ? sm.m[lane >> 1][lane & 1][hh] : kLowest;
+      float mx = mo;
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      mx = __shfl_sync(0xffffffffu, mx, 0);
+      const float f = member ? exp2_approx(mo - mx) : 0.f;
+      float ls = member ? sm.l[lane >> 1][lane & 1][hh] * f : 0.f;
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+      ls = __shfl_sync(0xffffffffu, ls, 0);
+      const int gg = lane & 7, q = lane >> 3;  // dims 16 gg + 4 q + 0..3
+      const int at = (hh >> 3) * kPieceFloats + piece_offset(2 * q, hh & 1, 4 * gg + ((hh & 7) >> 1));
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = -1; w < kWarps; ++w) {  // the lead's piece 1, then the pieces 0
+        const int src_lane = w < 0 ? lead : 2 * w;
+        const float fw = __shfl_sync(0xffffffffu, f, src_lane);
+        if (!((members >> src_lane) & 1u) || (w < 0 && !which)) continue;
+        const float* src = (w < 0 ? piece(lw, 1) : piece(w, 0)) + at;
+        acc[0] += src[0] * fw;
+        acc[1] += src[64] * fw;  // rows g + 8 of the same instruction
+        acc[2] += src[128] * fw;
+        acc[3] += src[192] * fw;
+      }
+      const int dim = 16 * gg + 4 * q;
+      if (complete) {
+        const float inv = ls > 0.f ? 1.0f / ls : 0.f;
+        const __half2 a = __floats2half2_rn(acc[0] * inv, acc[1] * inv);
+        const __half2 b = __floats2half2_rn(acc[2] * inv, acc[3] * inv);
+        *reinterpret_cast<uint2*>(p.Y + (static_cast<size_t>(row) + hh) * kHeadDim + dim) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      } else {
+        *reinterpret_cast<float4*>(part + hh * kHeadDim + dim) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        if (lane == 0) {
+          part[HB * kHeadDim + hh] = mx;
+          part[HB * kHeadDim + HB + hh] = ls;
+        }
+      }
+    }
+    if (!complete && tid == 0) sm.left[which] = lw, sm.join[which] = 1;
+  }
+  __syncthreads();
+  if (tid < 2 && sm.join[tid]) {
+    // counted, once every thread's share of the part is written
+    const int lw = sm.left[tid];
+    const long long t0 = sm.item[lw][tid] + kItemCost;
+    const int c_first = cta_of_unit(t0, total, C);
+    const int parts = cta_of_unit(t0 + sm.turns[lw][tid] - 1, total, C) - c_first + 1;
+    __threadfence();
+    sm.join[tid] = atomicInc(&p.count[c_first], unsigned(parts - 1)) == unsigned(parts - 1);
+    sm.turns[lw][tid] = parts;
+    sm.item[lw][tid] = c_first;
+  }
+  __syncthreads();
+  for (int which = 0; which < 2; ++which)
+    if (sm.join[which]) {
+      // the CTA that arrived last joins the parts, in the order of the CTAs
+      const int lw = sm.left[which];
+      __threadfence();
+      join_parts<HB>(p.part, int(sm.item[lw][which]), sm.turns[lw][which], sm.heads[lw][which], sums,
+                     p.Y + static_cast<size_t>(sm.row[lw][which]) * kHeadDim);
+      __syncthreads();
+    }
+}
 
 // CTAs of a launch: two per SM with one tile of 8 queries, one with two (their
 // registers hold 16 queries' sums).
@@ -650,9 +805,10 @@ int attn_grid(int nt) { return sm_count() * (nt == 1 ? 2 : 1); }
 template <int NT, bool P16>
 fq_status launch_attn(const AttnParams& p, cudaStream_t stream) {
   auto kern = kv_attn_kernel<NT, P16>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kAttnSmem)) != cudaSuccess)
-    return fail(FQ_ERR_CUDA, "cannot reserve %zu bytes of shared memory", kAttnSmem);
-  launch_pdl(kern, dim3(attn_grid(NT)), dim3(kAttnThreads), kAttnSmem, stream, p);
+  constexpr size_t smem = size_t(kWarps) * (kDepth * kStepBytes + NT * kPieceFloats * sizeof(float));
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+    return fail(FQ_ERR_CUDA, "cannot reserve %zu bytes of shared memory", smem);
+  launch_pdl(kern, dim3(attn_grid(NT)), dim3(kAttnThreads), smem, stream, p);
   return check_launch("kv_attn_kernel");
 }
 
