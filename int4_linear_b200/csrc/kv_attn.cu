@@ -135,6 +135,15 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void add4(float (&a)[4], const float (&b)[4]) {
+  const float2 x = fadd2(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
+  const float2 y = fadd2(make_float2(a[2], a[3]), make_float2(b[2], b[3]));
+  a[0] = x.x;
+  a[1] = x.y;
+  a[2] = y.x;
+  a[3] = y.y;
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -536,8 +545,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
 
     uint32_t coming = 0;  // halves of the turn under way
     for (int i = -1; i < seg.turns; ++i) {
-      copy_wait<0>();
-      __syncwarp();  // every lane's copies of this turn, and every lane is done with the last one
+      __syncwarp();  // every lane is done with the last turn, whose bytes the next one takes
       const uint32_t have = coming;
       {
         const Ids ids = next_ids;
@@ -547,6 +555,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       const uint8_t* sp = ring + slot * kStepBytes;
       slot ^= 1;
       if (have == 0u) continue;  // nothing there, or the first copies have just been sent
+      copy_wait<1>();
+      __syncwarp();  // every lane's copies of this turn
       // scores of the 32 tokens: rows g, g + 8 of both halves
       float sc[2][NT][4], ks[2][2], vs[2][2];
 #pragma unroll
@@ -680,11 +690,9 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
           for (int nn = 0; nn < NT; ++nn) {
             float d[4];
             mma_f16(d, a0, a1, a2, a3, w0[nn], w1[nn], c8[nn]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[nn][2 * j][k] += d[k];
+            add4(o[nn][2 * j], d);
             mma_f16(d, b0, b1, b2, b3, w0[nn], w1[nn], c8[nn]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[nn][2 * j + 1][k] += d[k];
+            add4(o[nn][2 * j + 1], d);
           }
         }
       }
