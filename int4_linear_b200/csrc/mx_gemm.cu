@@ -3,14 +3,19 @@
 //
 //   y[m][n] = fp16(g_x g_w sum_b s_x[m][b] s_w[n][b] sum_{k in b} x[m][k] w[n][k])
 //
-// The weights are the 128-row operand (tensor-memory lanes), the tokens the N
+// The weights are the row operand (tensor-memory lanes), the tokens the N
 // operand (BN = 16..256 columns), so that few tokens still fill the lanes. One CTA per SM:
 // warp 0 brings stages of 256 values along K (128 bytes per row: one swizzle
 // row) and their scales, which lie in memory as the 512-byte tiles that
-// tcgen05.cp spreads over tensor memory; one thread of warp 1 issues the scale copies and
-// the four MMAs of a stage; warps 4-7 drain finished tiles. A copy of scales is
-// ordered before the MMAs issued after it, and every stage has its own scale
-// columns, so the stage's barriers guard both.
+// tcgen05.cp spreads over tensor memory; one thread of warp 2 issues these copies (6 or 12 per
+// stage at 256 tokens, each holding its thread for 45 cycles, which in the MMA thread's
+// way cost a third of the rate), one of warp 1 the four MMAs of a stage; warps 4-7 drain finished
+// tiles. Every stage has its own scale columns, so the stage's barriers guard both.
+//
+// More than 128 tokens run on CTA pairs (PAIR): 256 weight rows per tile, each CTA
+// holding its 128 rows, half of the tokens' rows and the scales of all of them; the even CTA's
+// thread issues for both. A stage's copies of both CTAs complete on the even CTA's barrier, and its
+// commits reach both.
 //
 // Work: whole tiles dealt to the CTAs in turn, or, where the tiles do not fill
 // the SMs evenly and K is what there is to divide, equal contiguous parts of
@@ -38,7 +43,6 @@ constexpr int kStoreRows = 16;                  // tokens per output block
 constexpr int kStoreBytes = kStoreRows * 32 * 2;  // one warp's 16 x 32 outputs
 
 struct MxGemmParams {
-  const uint8_t *Sx, *Sw;
   const float *gx, *gw;
   int M, N, K;
   int mt, tiles, ks;       // token tiles, tiles, stages per tile
@@ -48,11 +52,12 @@ struct MxGemmParams {
   unsigned* err;
 };
 
-template <int FMT, int BN>
+template <int FMT, int BN, bool PAIR>
 struct MxCfg {
   static constexpr int SB = FMT == FQ_NVFP4 ? 4 : 2;      // scale tiles along K per stage
   static constexpr int NBT = (BN + 127) / 128;            // scale tiles along the tokens
-  static constexpr int A_BYTES = kTileN * kRowB, B_BYTES = BN * kRowB;
+  static constexpr int BROWS = PAIR ? BN / 2 : BN;        // tokens' rows in this CTA
+  static constexpr int A_BYTES = kTileN * kRowB, B_BYTES = BROWS * kRowB;
   static constexpr int SA_BYTES = SB * kMxTileBytes, SX_BYTES = SB * NBT * kMxTileBytes;
   static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES + SX_BYTES;
   static constexpr int AB = BN <= 128 ? 2 : 1;            // accumulators
@@ -68,45 +73,84 @@ struct MxCfg {
   static constexpr int OFF_SA = S * (A_BYTES + B_BYTES);
   static constexpr int OFF_OUT = OFF_SA + S * (SA_BYTES + SX_BYTES);
   static constexpr int OFF_BAR = OFF_OUT + OUT;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;
-  static_assert((A_BYTES + B_BYTES) % 1024 == 0 && A_BYTES % 1024 == 0, "swizzle atoms");
+  static constexpr int SMEM = OFF_BAR + 512 + 1024;
+  static_assert((A_BYTES + B_BYTES) % 1024 == 0 && A_BYTES % 1024 == 0 && SA_BYTES % 512 == 0, "operand layout");
   static_assert(SF0 + S * (SFA + SFX) <= 512, "tensor memory");
-  static_assert(SMEM <= 227 * 1024 && (2 * S + 5) * 8 + 8 <= 256, "shared memory");
+  static_assert(SMEM <= 227 * 1024 && (3 * S + 5) * 8 + 8 <= 512, "shared memory");
 };
 
 // 32 rows of 16 bytes (8-row groups 128 bytes apart, no swizzle) -> 4 columns of 32
-// lanes, repeated in each quarter of the lanes.
+// lanes, repeated in each quarter of the lanes; PAIR: in both CTAs.
+template <bool PAIR>
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
   const uint64_t d = uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(128u >> 4) << 32) | (uint64_t(1) << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+  if (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
-// Instruction descriptor of kind::mxf4 / mxf4nvf4: A = B = E2M1 K-major, M = 128, N = n,
+// Instruction descriptor of kind::mxf4 / mxf4nvf4: A = B = E2M1 K-major, M = m, N = n,
 // scale type E8M0 or E4M3, scale byte (0 or 2) of both operands' 32-bit columns.
 template <int FMT>
-__host__ __device__ constexpr uint32_t idesc_mx(int n, uint32_t sf) {
+__host__ __device__ constexpr uint32_t idesc_mx(int m, int n, uint32_t sf) {
   return (sf << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | ((FMT == FQ_MXFP4 ? 1u : 0u) << 23) |
-         (uint32_t(128 >> 4) << 24) | (sf << 29);
+         (uint32_t(m >> 4) << 24) | (sf << 29);
 }
 
-template <int FMT>
+template <int FMT, bool PAIR>
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
                                        uint32_t accumulate) {
-  if (FMT == FQ_MXFP4)
+#define FQ_MX_MMA(GROUP, KIND)                                                                                   \
+  asm volatile(                                                                                                  \
+      "{\n\t.reg .pred p;\n\t"                                                                                  \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                                                \
+      "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),          \
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)                                              \
+      : "memory")
+  if (FMT == FQ_MXFP4) {
+    if (PAIR)
+      FQ_MX_MMA("2", "mxf4.block_scale.scale_vec::2X");
+    else
+      FQ_MX_MMA("1", "mxf4.block_scale.scale_vec::2X");
+  } else {
+    if (PAIR)
+      FQ_MX_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+    else
+      FQ_MX_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
+  }
+#undef FQ_MX_MMA
+}
+
+// Tile load into this CTA's shared memory; PAIR: completing on the even CTA's barrier (`bar` is then a
+// shared::cluster address).
+template <bool PAIR>
+__device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, uint64_t pol) {
+  if (PAIR)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+        "[%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(pol)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-            d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, "
+        "%4}], [%2], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(pol)
         : "memory");
+}
+
+// shared::cluster address of `p`'s counterpart in CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 
 // This CTA's segments: (tile, stages [k0, k1)), the same sequence for every role.
@@ -141,60 +185,73 @@ struct MxWalk {
   }
 };
 
-template <int FMT, int BN>
+template <int FMT, int BN, bool PAIR>
 __global__ void __launch_bounds__(kMxGemmThreads, 1)
     mx_gemm_kernel(const MxGemmParams p, const __grid_constant__ CUtensorMap tmW,
-                   const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY) {
-  using C = MxCfg<FMT, BN>;
+                   const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmSw,
+                   const __grid_constant__ CUtensorMap tmSx, const __grid_constant__ CUtensorMap tmY) {
+  using C = MxCfg<FMT, BN, PAIR>;
   constexpr int S = C::S;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + S;
-  uint64_t* acc_full = empty + S;      // [2]
+  uint64_t* sf_full = empty + S;       // scales in tensor memory
+  uint64_t* acc_full = sf_full + S;    // [2]
   uint64_t* acc_empty = acc_full + 2;  // [2]
   uint64_t* done = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   int* join = reinterpret_cast<int*>(done + 1) + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_rank() : 0;
+  const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&sf_full[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 4);
+      mbar_init(&acc_empty[b], PAIR ? 8 : 4);
     }
     mbar_init(done, 1);
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(tmem_slot, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if (PAIR)
+    cluster_sync();
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_launch_dependents();
   pdl_wait();
 
-  const int kbt = p.K / kStageK * C::SB + (p.K % kStageK ? C::SB / 2 : 0);  // scale tiles along K
-  MxWalk walk(p, blockIdx.x, gridDim.x);
+  MxWalk walk(p, unit, units);
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       prefetch_tensormap(&tmW);
       prefetch_tensormap(&tmX);
-      const uint64_t pol = policy_evict_last();  // the tokens are read by every CTA
-      const int rt = (p.M + kMxTileRows - 1) / kMxTileRows;
+      prefetch_tensormap(&tmSw);
+      prefetch_tensormap(&tmSx);
+      const uint64_t pol_w = BN <= 64 ? policy_evict_first() : policy_evict_normal();  // few tokens: read once
+      const uint64_t pol_x = policy_evict_last();  // the tokens are read by every CTA
       int it = 0;
       bool ok = true;
       while (ok && walk.next()) {
-        const int nt = walk.tile / p.mt, mt = walk.tile % p.mt;
-        const int nb = min(C::NBT, rt - mt * BN / kMxTileRows);
+        const int nt = walk.tile / p.mt * (PAIR ? 2 : 1) + int(rank), mt = walk.tile % p.mt;  // 128 rows, BN tokens
         for (int k = walk.k0; k < walk.k1; ++k, ++it) {
           const int s = it % S;
           if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1)) {
@@ -202,34 +259,42 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t sfb = min(C::SB, kbt - k * C::SB) * kMxTileBytes;  // the last stage may be half a stage
-          mbar_arrive_expect_tx(&full[s], C::A_BYTES + C::B_BYTES + sfb * (1 + nb));
+          const uint32_t bar = PAIR ? cluster_addr(&full[s], 0) : smem_u32(&full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], C::STAGE * (PAIR ? 2 : 1));
           uint8_t* ab = smem + s * (C::A_BYTES + C::B_BYTES);
           uint8_t* sf = smem + C::OFF_SA + s * (C::SA_BYTES + C::SX_BYTES);
-          tma_load_2d(ab, &tmW, &full[s], k * kRowB, nt * kTileN);
-          tma_load_2d_hint(ab + C::A_BYTES, &tmX, &full[s], k * kRowB, mt * BN, pol);
-          bulk_load(sf, p.Sw + (size_t(nt) * kbt + size_t(k) * C::SB) * kMxTileBytes, sfb, &full[s]);
-          for (int b = 0; b < nb; ++b)
-            bulk_load(sf + C::SA_BYTES * (1 + b),
-                      p.Sx + (size_t(mt * BN / kMxTileRows + b) * kbt + size_t(k) * C::SB) * kMxTileBytes, sfb,
-                      &full[s]);
+          load_tile<PAIR>(ab, &tmW, bar, k * kRowB, nt * kTileN, pol_w);
+          load_tile<PAIR>(ab + C::A_BYTES, &tmX, bar, k * kRowB, mt * BN + int(rank) * C::BROWS, pol_x);
+          // scale tiles, 64 words of 8 bytes each; what lies past the last one reads as 0
+          load_tile<PAIR>(sf, &tmSw, bar, k * C::SB * 64, nt, pol_w);
+#pragma unroll
+          for (int j = 0; j < C::NBT; ++j)
+            load_tile<PAIR>(sf + C::SA_BYTES * (1 + j), &tmSx, bar, k * C::SB * 64, mt * BN / kMxTileRows + j, pol_x);
         }
       }
       // every copy has landed before the CTA may leave
-      for (int i = max(0, it - S); i < it; ++i)
-        if (!mbar_wait(&full[i % S], (i / S) & 1)) {
-          record_error(p.err, kErrTimeoutDrain);
-          break;
-        }
+      if (rank == 0)
+        for (int i = max(0, it - S); i < it; ++i)
+          if (!mbar_wait(&full[i % S], (i / S) & 1)) {
+            record_error(p.err, kErrTimeoutDrain);
+            break;
+          }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ scale copies and MMAs
-    if (lane == 0) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0 && rank == 0) {
+      auto commit = [&](uint64_t* bar) {
+        if (PAIR)
+          mma_commit_pair(bar, 3);
+        else
+          mma_commit(bar);
+      };
       int it = 0, seg = 0;
       bool ok = true;
       while (ok && walk.next()) {
         const int buf = seg % C::AB;
-        if (!mbar_wait(&acc_empty[buf], ((seg / C::AB) & 1) ^ 1)) {
+        if (!(PAIR ? mbar_wait_cluster(&acc_empty[buf], ((seg / C::AB) & 1) ^ 1)
+                   : mbar_wait(&acc_empty[buf], ((seg / C::AB) & 1) ^ 1))) {
           record_error(p.err, kErrTimeoutMma);
           break;
         }
@@ -237,42 +302,72 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
         const uint32_t d = tmem + uint32_t(buf * C::ACC);
         for (int k = walk.k0; k < walk.k1; ++k, ++it) {
           const int s = it % S;
-          if (!mbar_wait(&full[s], (it / S) & 1)) {
+          // the scales came after the operands: one wait for both, the first for the operands' visibility
+          if (!(PAIR ? mbar_wait_cluster(&full[s], (it / S) & 1) : mbar_wait(&full[s], (it / S) & 1)) ||
+              !mbar_wait(&sf_full[s], (it / S) & 1)) {
             record_error(p.err, kErrTimeoutMma);
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t ab = smem_u32(smem + s * (C::A_BYTES + C::B_BYTES));
-          const uint32_t sf = smem_u32(smem + C::OFF_SA + s * (C::SA_BYTES + C::SX_BYTES));
           const uint32_t ta = tmem + uint32_t(C::SF0 + s * (C::SFA + C::SFX)), tx = ta + uint32_t(C::SFA);
           const bool half = (k + 1) * kStageK > p.K;  // 128 values in the last stage
-          const int sb = half ? C::SB / 2 : C::SB;
-#pragma unroll
-          for (int b = 0; b < C::SB; ++b) {
-            if (b >= sb) break;
-            copy_scales(ta + 4 * b, sf + b * kMxTileBytes);
-#pragma unroll
-            for (int j = 0; j < C::NBT; ++j)
-              copy_scales(tx + 4 * (b * C::NBT + j), sf + C::SA_BYTES * (1 + j) + b * kMxTileBytes);
-          }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             if (half && q >= 2) break;
             const int b = FMT == FQ_NVFP4 ? q : q / 2;
-            constexpr uint32_t i0 = idesc_mx<FMT>(BN, 0), i2 = idesc_mx<FMT>(BN, 2);
-            mma_mx<FMT>(d, sdesc_k128_sw128(ab + 32 * q), sdesc_k128_sw128(ab + C::A_BYTES + 32 * q),
-                        FMT == FQ_MXFP4 && (q & 1) ? i2 : i0, ta + 4 * b, tx + 4 * b * C::NBT,
-                        uint32_t(k > walk.k0 || q > 0));
+            constexpr uint32_t i0 = idesc_mx<FMT>(PAIR ? 256 : 128, BN, 0), i2 = idesc_mx<FMT>(PAIR ? 256 : 128, BN, 2);
+            mma_mx<FMT, PAIR>(d, sdesc_k128_sw128(ab + 32 * q), sdesc_k128_sw128(ab + C::A_BYTES + 32 * q),
+                              FMT == FQ_MXFP4 && (q & 1) ? i2 : i0, ta + 4 * b, tx + 4 * b * C::NBT,
+                              uint32_t(k > walk.k0 || q > 0));
           }
-          mma_commit(&empty[s]);
+          commit(&empty[s]);
         }
-        mma_commit(&acc_full[buf]);
+        commit(&acc_full[buf]);
         ++seg;
       }
       // nothing issued may still run when tensor memory is freed
-      mma_commit(done);
+      commit(done);
       if (!mbar_wait(done, 0)) record_error(p.err, kErrTimeoutDrain);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ scales to tensor memory
+    if (lane == 0 && rank == 0) {
+      int it = 0;
+      bool ok = true;
+      while (ok && walk.next()) {
+        for (int k = walk.k0; k < walk.k1; ++k, ++it) {
+          const int s = it % S;
+          if (!(PAIR ? mbar_wait_cluster(&full[s], (it / S) & 1) : mbar_wait(&full[s], (it / S) & 1))) {
+            record_error(p.err, kErrTimeoutUnpack);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sf = smem_u32(smem + C::OFF_SA + s * (C::SA_BYTES + C::SX_BYTES));
+          const uint32_t ta = tmem + uint32_t(C::SF0 + s * (C::SFA + C::SFX)), tx = ta + uint32_t(C::SFA);
+          const int sb = (k + 1) * kStageK > p.K ? C::SB / 2 : C::SB;
+#pragma unroll
+          for (int b = 0; b < C::SB; ++b) {
+            if (b >= sb) break;
+            copy_scales<PAIR>(ta + 4 * b, sf + b * kMxTileBytes);
+#pragma unroll
+            for (int j = 0; j < C::NBT; ++j)
+              copy_scales<PAIR>(tx + 4 * (b * C::NBT + j), sf + C::SA_BYTES * (1 + j) + b * kMxTileBytes);
+          }
+          if (PAIR)
+            mma_commit_pair(&sf_full[s], 1);
+          else
+            mma_commit(&sf_full[s]);
+        }
+      }
+      // every copy sent has been made before tensor memory is freed
+      for (int i = max(0, it - S); i < it; ++i)
+        if (!mbar_wait(&sf_full[i % S], (i / S) & 1)) {
+          record_error(p.err, kErrTimeoutDrain);
+          break;
+        }
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ finished tiles
@@ -310,9 +405,19 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
     };
     constexpr int CH = BN < 32 ? 16 : 32;  // columns per tensor-memory load
     while (walk.next()) {
-      const int nt = walk.tile / p.mt, mt = walk.tile % p.mt;
+      const int nt = walk.tile / p.mt * (PAIR ? 2 : 1) + int(rank), mt = walk.tile % p.mt;
       const int buf = seg % C::AB;
       const uint32_t d = tmem + uint32_t(buf * C::ACC) + lanes;
+      auto release = [&]() {  // the accumulator goes back
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_cluster(&acc_empty[buf], 0);
+          else
+            mbar_arrive(&acc_empty[buf]);
+        }
+      };
       if (!bad && !warp_wait(&acc_full[buf], (seg / C::AB) & 1)) {
         if (lane == 0) record_error(p.err, kErrTimeoutEpilogue);
         bad = true;
@@ -321,22 +426,24 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
       ++seg;
       if (walk.k0 == 0 && walk.k1 == p.ks) {
         uint32_t h[BN / 2];
+        uint32_t v[2][32];
+        auto load = [&](int c) {
+          if (CH == 32)
+            tmem_ld_32x32(d + c, v[(c / CH) & 1]);
+          else
+            tmem_ld_32x16(d + c, v[(c / CH) & 1]);
+        };
+        load(0);
 #pragma unroll
         for (int c = 0; c < BN; c += CH) {
-          uint32_t v[32];
-          if (CH == 32)
-            tmem_ld_32x32(d + c, v);
-          else
-            tmem_ld_32x16(d + c, v);
           tmem_wait_ld();
+          if (c + CH < BN) load(c + CH);  // under way while this one is packed
+          const uint32_t* w = v[(c / CH) & 1];
 #pragma unroll
           for (int j = 0; j < CH / 2; ++j)
-            h[c / 2 + j] = pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            h[c / 2 + j] = pack(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
         }
-        // the accumulator goes back before the outputs are on their way
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        release();  // before the outputs are on their way
         if (!bad) {
 #pragma unroll
           for (int c = 0; c < BN; c += kStoreRows) {
@@ -350,7 +457,7 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
       }
       // a part of a tile: float32 sums to this CTA's slot, [column][128]
       const long long total = static_cast<long long>(p.tiles) * p.ks, t0 = static_cast<long long>(walk.tile) * p.ks;
-      const int G = gridDim.x;
+      const int G = units;
       const int c_first = int(((t0 + 1) * G - 1) / total);
       const int parts = int(((t0 + p.ks) * G - 1) / total) - c_first + 1;
       const size_t slot_floats = size_t(BN) * kTileN;
@@ -368,9 +475,7 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
         for (int j = 0; j < CH; ++j)
           if (c + j < cols) dst[size_t(c + j) * kTileN] = __uint_as_float(v[j]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      release();
       __threadfence();
       named_barrier(1, 128);
       if (threadIdx.x == 128) *join = atomicInc(&p.count[c_first], unsigned(parts - 1)) == unsigned(parts - 1);
@@ -398,59 +503,72 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
     }
     if (lane == 0) bulk_wait_group<0>();
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  // a pair: neither CTA leaves while the other may still signal it or read its operands
+  if (PAIR)
+    cluster_sync();
+  else
+    __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if (PAIR)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
   }
 }
 
 // Tokens per tile, tiles and whether K is divided, from the sizes alone.
 struct MxPlan {
   int bn, mt, tiles, ks, split, grid;
+  bool pair;
 };
 
 MxPlan mx_plan(int M, int N, int K) {
   MxPlan q;
   const int sms = sm_count();
   q.ks = (K + kStageK - 1) / kStageK;
-  const int nt = (N + kTileN - 1) / kTileN;
-  if (M <= 128) {
+  q.pair = M > 128;
+  const int workers = q.pair ? sms / 2 : sms;
+  const int nt = (N + (q.pair ? 255 : 127)) / (q.pair ? 256 : 128);
+  if (!q.pair) {
     q.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   } else {
     const long long t128 = static_cast<long long>(nt) * ((M + 127) / 128), t256 = static_cast<long long>(nt) * ((M + 255) / 256);
-    const long long w128 = (t128 + sms - 1) / sms, w256 = (t256 + sms - 1) / sms;
+    const long long w128 = (t128 + workers - 1) / workers, w256 = (t256 + workers - 1) / workers;
     q.bn = w128 * 11 < w256 * 20 ? 128 : 256;
   }
   q.mt = (M + q.bn - 1) / q.bn;
   q.tiles = nt * q.mt;
-  q.split = q.bn <= 64 || (q.tiles < sms && q.ks > 1);
+  q.split = !q.pair && (q.bn <= 64 || (q.tiles < sms && q.ks > 1));
   const long long units = static_cast<long long>(q.tiles) * q.ks;
-  q.grid = int(std::min<long long>(sms, q.split ? units : q.tiles));
+  q.grid = int(std::min<long long>(workers, q.split ? units : q.tiles)) * (q.pair ? 2 : 1);
   return q;
 }
 
-template <int FMT, int BN>
-fq_status launch_mx(const MxGemmParams& p, const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& y, int grid,
-                    cudaStream_t stream) {
-  using C = MxCfg<FMT, BN>;
-  auto kern = mx_gemm_kernel<FMT, BN>;
+template <int FMT, int BN, bool PAIR>
+fq_status launch_mx(const MxGemmParams& p, const CUtensorMap (&m)[5], int grid, cudaStream_t stream) {
+  using C = MxCfg<FMT, BN, PAIR>;
+  auto kern = mx_gemm_kernel<FMT, BN, PAIR>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return fail(FQ_ERR_CUDA, "cannot reserve %d bytes of shared memory", C::SMEM);
-  launch_pdl(kern, dim3(grid), dim3(kMxGemmThreads), C::SMEM, stream, p, w, x, y);
+  if (PAIR)
+    launch_pdl_cluster(kern, dim3(grid), dim3(kMxGemmThreads), C::SMEM, stream, 2, p, m[0], m[1], m[2], m[3], m[4]);
+  else
+    launch_pdl(kern, dim3(grid), dim3(kMxGemmThreads), C::SMEM, stream, p, m[0], m[1], m[2], m[3], m[4]);
   return check_launch("mx_gemm_kernel");
 }
 
 template <int FMT>
-fq_status launch_mx_bn(int bn, const MxGemmParams& p, const CUtensorMap& w, const CUtensorMap& x,
-                       const CUtensorMap& y, int grid, cudaStream_t stream) {
-  switch (bn) {
-    case 16: return launch_mx<FMT, 16>(p, w, x, y, grid, stream);
-    case 32: return launch_mx<FMT, 32>(p, w, x, y, grid, stream);
-    case 64: return launch_mx<FMT, 64>(p, w, x, y, grid, stream);
-    case 128: return launch_mx<FMT, 128>(p, w, x, y, grid, stream);
-    default: return launch_mx<FMT, 256>(p, w, x, y, grid, stream);
+fq_status launch_mx_bn(const MxPlan& q, const MxGemmParams& p, const CUtensorMap (&m)[5], cudaStream_t stream) {
+  if (q.pair)
+    return q.bn == 128 ? launch_mx<FMT, 128, true>(p, m, q.grid, stream) : launch_mx<FMT, 256, true>(p, m, q.grid, stream);
+  switch (q.bn) {
+    case 16: return launch_mx<FMT, 16, false>(p, m, q.grid, stream);
+    case 32: return launch_mx<FMT, 32, false>(p, m, q.grid, stream);
+    case 64: return launch_mx<FMT, 64, false>(p, m, q.grid, stream);
+    default: return launch_mx<FMT, 128, false>(p, m, q.grid, stream);
   }
 }
 
@@ -500,18 +618,23 @@ fq_status fq_mx_gemm(const uint8_t* Xq, const uint8_t* Sx, const float* g_x, con
   FQ_CHECK_ARG(static_cast<long long>((N + 127) / 128) * q.mt < (1ll << 31), "M = %d and N = %d: too many tiles", M, N);
   unsigned* err = fq::device_error_word();
   if (!err) return fq::fail(FQ_ERR_CUDA, "device error word unavailable");
-  CUtensorMap w, x, y;
-  fq_status st = fq::make_tmap_2d(&w, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, N, K / 2, fq::kRowB, fq::kTileN,
+  // weights, tokens, their scales (rows of 128-row tiles, 8-byte words), outputs
+  CUtensorMap m[5];
+  const int sb = fmt == FQ_NVFP4 ? 4 : 2;
+  const uint64_t sw = uint64_t(K / fq::mx_block(fmt) / fq::kMxTileBlocks) * (fq::kMxTileBytes / 8);
+  fq_status st = fq::make_tmap_2d(&m[0], Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, N, K / 2, fq::kRowB, fq::kTileN,
                                   CU_TENSOR_MAP_SWIZZLE_128B);
   if (st == FQ_OK)
-    st = fq::make_tmap_2d(&x, Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, M, K / 2, fq::kRowB, q.bn,
-                          CU_TENSOR_MAP_SWIZZLE_128B);
+    st = fq::make_tmap_2d(&m[1], Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, M, K / 2, fq::kRowB,
+                          q.pair ? q.bn / 2 : q.bn, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st == FQ_OK)
-    st = fq::make_tmap_2d(&y, Y, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, N, M, size_t(N) * 2, 32, fq::kStoreRows);
+    st = fq::make_tmap_2d(&m[2], Sw, CU_TENSOR_MAP_DATA_TYPE_INT64, sw, (N + 127) / 128, sw * 8, sb * 64, 1);
+  if (st == FQ_OK)
+    st = fq::make_tmap_2d(&m[3], Sx, CU_TENSOR_MAP_DATA_TYPE_INT64, sw, (M + 127) / 128, sw * 8, sb * 64, 1);
+  if (st == FQ_OK)
+    st = fq::make_tmap_2d(&m[4], Y, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, N, M, size_t(N) * 2, 32, fq::kStoreRows);
   if (st != FQ_OK) return st;
   fq::MxGemmParams p{};
-  p.Sx = Sx;
-  p.Sw = Sw;
   p.gx = g_x;
   p.gw = g_w;
   p.M = M;
@@ -525,8 +648,7 @@ fq_status fq_mx_gemm(const uint8_t* Xq, const uint8_t* Sx, const float* g_x, con
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + fq::sync_block_bytes());
   p.err = err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return fmt == FQ_MXFP4 ? fq::launch_mx_bn<FQ_MXFP4>(q.bn, p, w, x, y, q.grid, s)
-                         : fq::launch_mx_bn<FQ_NVFP4>(q.bn, p, w, x, y, q.grid, s);
+  return fmt == FQ_MXFP4 ? fq::launch_mx_bn<FQ_MXFP4>(q, p, m, s) : fq::launch_mx_bn<FQ_NVFP4>(q, p, m, s);
 }
 
 fq_status fq_mx_linear(const uint16_t* X, long long ldx, int M, int K, fq_mx_format fmt, const float* g_x,
