@@ -7,10 +7,10 @@
 // operand (BN = 16..256 columns), so that few tokens still fill the lanes. One CTA per SM:
 // warp 0 brings stages of 256 values along K (128 bytes per row: one swizzle
 // row) and their scales, which lie in memory as the 512-byte tiles that
-// tcgen05.cp spreads over tensor memory; one thread of warp 2 issues these copies (6 or 12 per
-// stage at 256 tokens, each holding its thread for 45 cycles, which in the MMA thread's
-// way cost a third of the rate), one of warp 1 the four MMAs of a stage; warps 4-7 drain finished
-// tiles. Every stage has its own scale columns, so the stage's barriers guard both.
+// tcgen05.cp spreads over tensor memory; a thread each of warps 2 and 3 issues these copies (6 or 12
+// per stage at 256 tokens, each holding its thread for 45 cycles: in the MMA thread's way they cost a
+// third of the rate, from one thread 13 % of NVFP4's), one of warp 1 the four MMAs of a stage; warps
+// 4-7 drain finished tiles. Every stage has its own scale columns, so the stage's barriers guard both.
 //
 // More than 128 tokens run on CTA pairs (PAIR): 256 weight rows per tile, each CTA
 // holding its 128 rows, half of the tokens' rows and the scales of all of them; the even CTA's
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&sf_full[s], 1);
+      mbar_init(&sf_full[s], 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
@@ -331,8 +331,8 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
       commit(done);
       if (!mbar_wait(done, 0)) record_error(p.err, kErrTimeoutDrain);
     }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ scales to tensor memory
+  } else if (warp == 2 || warp == 3) {
+    // ------------------------------------------------------------ scales to tensor memory, every other tile each
     if (lane == 0 && rank == 0) {
       int it = 0;
       bool ok = true;
@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
 #pragma unroll
           for (int b = 0; b < C::SB; ++b) {
             if (b >= sb) break;
+            if ((b & 1) != (warp & 1)) continue;  // warps 2 and 3
             copy_scales<PAIR>(ta + 4 * b, sf + b * kMxTileBytes);
 #pragma unroll
             for (int j = 0; j < C::NBT; ++j)
