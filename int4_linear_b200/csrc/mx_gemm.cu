@@ -81,13 +81,15 @@ struct MxCfg {
 
 // 32 rows of 16 bytes (8-row groups 128 bytes apart, no swizzle) -> 4 columns of 32
 // lanes, repeated in each quarter of the lanes; PAIR: in both CTAs.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(128u >> 4) << 32) | (uint64_t(1) << 46);
+}
 template <bool PAIR>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
-  const uint64_t d = uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(128u >> 4) << 32) | (uint64_t(1) << 46);
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
   if (PAIR)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
   else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // Instruction descriptor of kind::mxf4 / mxf4nvf4: A = B = E2M1 K-major, M = m, N = n,
@@ -152,6 +154,52 @@ __device__ __forceinline__ uint64_t policy_evict_normal() {
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
+
+// Wait for a barrier's phase.  The thread sleeps in the instruction (up to the hint, 1 ms) instead of asking
+// again and again: polling threads get in the way of the ones that issue copies and MMAs (64 quick
+// tries per wait cost 20 % of the rate).  false after kWaitLimitNs.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+  constexpr uint32_t kHintNs = 1000000;
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    if (CLUSTER)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(kHintNs)
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(kHintNs)
+          : "memory");
+    if (ok) return true;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0)
+      t0 = now;
+    else if (now - t0 > kWaitLimitNs)
+      return false;
+  }
+}
+
+// A stage of the ring and its phase.
+struct MxStage {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int S) {
+    if (++s == S) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+};
 
 // This CTA's segments: (tile, stages [k0, k1)), the same sequence for every role.
 struct MxWalk {
@@ -248,37 +296,42 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
       prefetch_tensormap(&tmSx);
       const uint64_t pol_w = BN <= 64 ? policy_evict_first() : policy_evict_normal();  // few tokens: read once
       const uint64_t pol_x = policy_evict_last();  // the tokens are read by every CTA
-      int it = 0;
+      const uint32_t bar0 = PAIR ? cluster_addr(full, 0) : smem_u32(full);
+      MxStage st;
+      int sent = 0;
       bool ok = true;
       while (ok && walk.next()) {
         const int nt = walk.tile / p.mt * (PAIR ? 2 : 1) + int(rank), mt = walk.tile % p.mt;  // 128 rows, BN tokens
-        for (int k = walk.k0; k < walk.k1; ++k, ++it) {
-          const int s = it % S;
-          if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1)) {
+        const int yw = nt * kTileN, yx = mt * BN + int(rank) * C::BROWS, ysx = mt * BN / kMxTileRows;
+        for (int k = walk.k0; k < walk.k1; ++k, st.next(S)) {
+          if (!wait_phase<false>(&empty[st.s], st.phase ^ 1)) {
             record_error(p.err, kErrTimeoutProducer);
             ok = false;
             break;
           }
-          const uint32_t bar = PAIR ? cluster_addr(&full[s], 0) : smem_u32(&full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], C::STAGE * (PAIR ? 2 : 1));
-          uint8_t* ab = smem + s * (C::A_BYTES + C::B_BYTES);
-          uint8_t* sf = smem + C::OFF_SA + s * (C::SA_BYTES + C::SX_BYTES);
-          load_tile<PAIR>(ab, &tmW, bar, k * kRowB, nt * kTileN, pol_w);
-          load_tile<PAIR>(ab + C::A_BYTES, &tmX, bar, k * kRowB, mt * BN + int(rank) * C::BROWS, pol_x);
+          const uint32_t bar = bar0 + 8u * st.s;
+          if (rank == 0) mbar_arrive_expect_tx(&full[st.s], C::STAGE * (PAIR ? 2 : 1));
+          uint8_t* ab = smem + st.s * (C::A_BYTES + C::B_BYTES);
+          uint8_t* sf = smem + C::OFF_SA + st.s * (C::SA_BYTES + C::SX_BYTES);
+          load_tile<PAIR>(ab, &tmW, bar, k * kRowB, yw, pol_w);
+          load_tile<PAIR>(ab + C::A_BYTES, &tmX, bar, k * kRowB, yx, pol_x);
           // scale tiles, 64 words of 8 bytes each; what lies past the last one reads as 0
           load_tile<PAIR>(sf, &tmSw, bar, k * C::SB * 64, nt, pol_w);
 #pragma unroll
           for (int j = 0; j < C::NBT; ++j)
-            load_tile<PAIR>(sf + C::SA_BYTES * (1 + j), &tmSx, bar, k * C::SB * 64, mt * BN / kMxTileRows + j, pol_x);
+            load_tile<PAIR>(sf + C::SA_BYTES * (1 + j), &tmSx, bar, k * C::SB * 64, ysx + j, pol_x);
+          sent = min(sent + 1, S);
         }
       }
-      // every copy has landed before the CTA may leave
+      // every copy has landed before the CTA may leave: the last `sent` stages, oldest first
       if (rank == 0)
-        for (int i = max(0, it - S); i < it; ++i)
-          if (!mbar_wait(&full[i % S], (i / S) & 1)) {
+        for (int i = 0; i < sent; ++i) {
+          const int back = sent - i, s = st.s - back < 0 ? st.s - back + S : st.s - back;
+          if (!mbar_wait(&full[s], st.s - back < 0 ? st.phase ^ 1 : st.phase)) {
             record_error(p.err, kErrTimeoutDrain);
             break;
           }
+        }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
@@ -289,40 +342,40 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
         else
           mma_commit(bar);
       };
-      int it = 0, seg = 0;
+      constexpr uint32_t kStep16 = (C::A_BYTES + C::B_BYTES) >> 4;  // a stage in the descriptors' 16-byte units
+      const uint64_t a_desc = sdesc_k128_sw128(smem_u32(smem)), b_desc = sdesc_k128_sw128(smem_u32(smem) + C::A_BYTES);
+      constexpr uint32_t i0 = idesc_mx<FMT>(PAIR ? 256 : 128, BN, 0), i2 = idesc_mx<FMT>(PAIR ? 256 : 128, BN, 2);
+      const bool tail = p.K % kStageK != 0;  // 128 values in the last stage
+      MxStage st;
+      int seg = 0;
       bool ok = true;
       while (ok && walk.next()) {
         const int buf = seg % C::AB;
-        if (!(PAIR ? mbar_wait_cluster(&acc_empty[buf], ((seg / C::AB) & 1) ^ 1)
-                   : mbar_wait(&acc_empty[buf], ((seg / C::AB) & 1) ^ 1))) {
+        if (!wait_phase<PAIR>(&acc_empty[buf], ((seg / C::AB) & 1) ^ 1)) {
           record_error(p.err, kErrTimeoutMma);
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(buf * C::ACC);
-        for (int k = walk.k0; k < walk.k1; ++k, ++it) {
-          const int s = it % S;
-          // the scales came after the operands: one wait for both, the first for the operands' visibility
-          if (!(PAIR ? mbar_wait_cluster(&full[s], (it / S) & 1) : mbar_wait(&full[s], (it / S) & 1)) ||
-              !mbar_wait(&sf_full[s], (it / S) & 1)) {
+        for (int k = walk.k0; k < walk.k1; ++k, st.next(S)) {
+          // the operands, then the scales, which came after them
+          if (!wait_phase<PAIR>(&full[st.s], st.phase) || !wait_phase<false>(&sf_full[st.s], st.phase)) {
             record_error(p.err, kErrTimeoutMma);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t ab = smem_u32(smem + s * (C::A_BYTES + C::B_BYTES));
-          const uint32_t ta = tmem + uint32_t(C::SF0 + s * (C::SFA + C::SFX)), tx = ta + uint32_t(C::SFA);
-          const bool half = (k + 1) * kStageK > p.K;  // 128 values in the last stage
+          const uint64_t ad = a_desc + uint32_t(st.s) * kStep16, bd = b_desc + uint32_t(st.s) * kStep16;
+          const uint32_t ta = tmem + uint32_t(C::SF0 + st.s * (C::SFA + C::SFX)), tx = ta + uint32_t(C::SFA);
+          const bool half = tail && k + 1 == p.ks;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            if (half && q >= 2) break;
+            if (q >= 2 && half) break;
             const int b = FMT == FQ_NVFP4 ? q : q / 2;
-            constexpr uint32_t i0 = idesc_mx<FMT>(PAIR ? 256 : 128, BN, 0), i2 = idesc_mx<FMT>(PAIR ? 256 : 128, BN, 2);
-            mma_mx<FMT, PAIR>(d, sdesc_k128_sw128(ab + 32 * q), sdesc_k128_sw128(ab + C::A_BYTES + 32 * q),
-                              FMT == FQ_MXFP4 && (q & 1) ? i2 : i0, ta + 4 * b, tx + 4 * b * C::NBT,
-                              uint32_t(k > walk.k0 || q > 0));
+            mma_mx<FMT, PAIR>(d, ad + 2 * q, bd + 2 * q, FMT == FQ_MXFP4 && (q & 1) ? i2 : i0, ta + 4 * b,
+                              tx + 4 * b * C::NBT, q > 0 ? 1u : uint32_t(k > walk.k0));
           }
-          commit(&empty[s]);
+          commit(&empty[st.s]);
         }
         commit(&acc_full[buf]);
         ++seg;
@@ -334,41 +387,48 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
   } else if (warp == 2 || warp == 3) {
     // ------------------------------------------------------------ scales to tensor memory, every other tile each
     if (lane == 0 && rank == 0) {
-      int it = 0;
+      const uint64_t sf_desc = sdesc_scales(smem_u32(smem + C::OFF_SA));
+      constexpr uint32_t kStep16 = (C::SA_BYTES + C::SX_BYTES) >> 4, kTile16 = kMxTileBytes >> 4;
+      const bool tail = p.K % kStageK != 0;
+      MxStage st;
+      int sent = 0;
       bool ok = true;
       while (ok && walk.next()) {
-        for (int k = walk.k0; k < walk.k1; ++k, ++it) {
-          const int s = it % S;
-          if (!(PAIR ? mbar_wait_cluster(&full[s], (it / S) & 1) : mbar_wait(&full[s], (it / S) & 1))) {
+        for (int k = walk.k0; k < walk.k1; ++k, st.next(S)) {
+          if (!wait_phase<PAIR>(&full[st.s], st.phase)) {
             record_error(p.err, kErrTimeoutUnpack);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sf = smem_u32(smem + C::OFF_SA + s * (C::SA_BYTES + C::SX_BYTES));
-          const uint32_t ta = tmem + uint32_t(C::SF0 + s * (C::SFA + C::SFX)), tx = ta + uint32_t(C::SFA);
-          const int sb = (k + 1) * kStageK > p.K ? C::SB / 2 : C::SB;
+          const uint64_t sd = sf_desc + uint32_t(st.s) * kStep16;
+          const uint32_t ta = tmem + uint32_t(C::SF0 + st.s * (C::SFA + C::SFX)), tx = ta + uint32_t(C::SFA);
+          const bool half = tail && k + 1 == p.ks;
 #pragma unroll
-          for (int b = 0; b < C::SB; ++b) {
-            if (b >= sb) break;
-            if ((b & 1) != (warp & 1)) continue;  // warps 2 and 3
-            copy_scales<PAIR>(ta + 4 * b, sf + b * kMxTileBytes);
+          for (int b0 = 0; b0 < C::SB; b0 += 2) {
+            if (b0 >= C::SB / 2 && half && C::SB > 2) break;
+            if (half && C::SB == 2 && warp == 3) break;
+            const int b = b0 + (warp & 1);  // warps 2 and 3
+            copy_scales<PAIR>(ta + 4 * b, sd + b * kTile16);
 #pragma unroll
             for (int j = 0; j < C::NBT; ++j)
-              copy_scales<PAIR>(tx + 4 * (b * C::NBT + j), sf + C::SA_BYTES * (1 + j) + b * kMxTileBytes);
+              copy_scales<PAIR>(tx + 4 * (b * C::NBT + j), sd + (C::SB * (1 + j) + b) * kTile16);
           }
           if (PAIR)
-            mma_commit_pair(&sf_full[s], 1);
+            mma_commit_pair(&sf_full[st.s], 1);
           else
-            mma_commit(&sf_full[s]);
+            mma_commit(&sf_full[st.s]);
+          sent = min(sent + 1, S);
         }
       }
       // every copy sent has been made before tensor memory is freed
-      for (int i = max(0, it - S); i < it; ++i)
-        if (!mbar_wait(&sf_full[i % S], (i / S) & 1)) {
+      for (int i = 0; i < sent; ++i) {
+        const int back = sent - i, s = st.s - back < 0 ? st.s - back + S : st.s - back;
+        if (!mbar_wait(&sf_full[s], st.s - back < 0 ? st.phase ^ 1 : st.phase)) {
           record_error(p.err, kErrTimeoutDrain);
           break;
         }
+      }
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ finished tiles
@@ -419,7 +479,7 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
             mbar_arrive(&acc_empty[buf]);
         }
       };
-      if (!bad && !warp_wait(&acc_full[buf], (seg / C::AB) & 1)) {
+      if (!bad && !__all_sync(0xffffffffu, lane != 0 || wait_phase<false>(&acc_full[buf], (seg / C::AB) & 1))) {
         if (lane == 0) record_error(p.err, kErrTimeoutEpilogue);
         bad = true;
       }
