@@ -155,6 +155,28 @@ __device__ __forceinline__ uint64_t policy_evict_normal() {
   return p;
 }
 
+// 16 lanes x 32 (x4) or 16 (x2) columns as 8-column blocks b: r[4 b + 2 h + e] is lane t / 4 + 8 h, column
+// 8 b + 2 (t % 4) + e of thread t, the fragment that stmatrix stores.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+// Four 8 x 8 blocks of fp16 stored transposed; lane l gives the address of row l % 8 of block l / 8.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
 // Wait for a barrier's phase.  The thread sleeps in the instruction (up to the hint, 1 ms) instead of asking
 // again and again: polling threads get in the way of the ones that issue copies and MMAs (64 quick
 // tries per wait cost 20 % of the rate).  false after kWaitLimitNs.
@@ -438,33 +460,48 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
     const float g = (p.gx ? *p.gx : 1.0f) * (p.gw ? *p.gw : 1.0f);
     int seg = 0, stored = 0;
     bool bad = false;
-    // 16 tokens (columns col0..) of this warp's 32 rows: to shared memory as rows of tokens, out by one copy
-    auto emit = [&](int nt, int mt, int col0, const uint32_t(&h)[kStoreRows / 2]) {
+    // 16 tokens (columns col0..) of this warp's 32 rows: a block of 16 token rows of 64 bytes in shared
+    // memory (64-byte swizzle, which keeps the 8 rows of a stored block in different banks), out by one
+    // copy.  h[4 hf + 2 b + r]: rows 16 hf + 8 r + lane / 4, tokens 8 b + 2 (lane % 4), + 1
+    const int mrow = lane & 7, mblk = lane >> 3;
+    auto emit = [&](int nt, int mt, int col0, const uint32_t* h) {
       const int x = nt * kTileN + 32 * w, y = mt * BN + col0;
       if (x >= p.N || y >= p.M) return;
-      uint8_t* blk = out + (stored & 1) * kStoreBytes;
+      const uint32_t blk = smem_u32(out) + (stored & 1) * kStoreBytes;
       if (lane == 0) bulk_wait_group_read<1>();
       __syncwarp();
-      __half* row = reinterpret_cast<__half*>(blk) + lane;
 #pragma unroll
-      for (int j = 0; j < kStoreRows / 2; ++j) {
-        const __half2 v = *reinterpret_cast<const __half2*>(&h[j]);
-        row[(2 * j) * 32] = __low2half(v);
-        row[(2 * j + 1) * 32] = __high2half(v);
+      for (int b = 0; b < 2; ++b) {
+        const int row = 8 * b + mrow;
+        stmatrix_x4_trans(blk + row * 64 + ((mblk ^ ((row >> 1) & 3)) << 4), h[2 * b], h[2 * b + 1], h[4 + 2 * b],
+                          h[4 + 2 * b + 1]);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tma_store_2d(&tmY, blk, x, y);
+        tma_store_2d(&tmY, out + (stored & 1) * kStoreBytes, x, y);
         bulk_commit_group();
       }
       ++stored;
     };
-    auto pack = [&](float a, float b) {
-      const __half2 v = __floats2half2_rn(a * g, b * g);
-      return *reinterpret_cast<const uint32_t*>(&v);
+    auto pack = [&](uint32_t a, uint32_t b) {  // MXFP4 has no tensor scales
+      const float2 v = make_float2(__uint_as_float(a), __uint_as_float(b));
+      const float2 s = FMT == FQ_NVFP4 ? fmul2(v, make_float2(g, g)) : v;
+      const __half2 r = __floats2half2_rn(s.x, s.y);
+      return *reinterpret_cast<const uint32_t*>(&r);
     };
+    // CH columns of this warp's lanes: v[16 hf + 4 b + ...] (CH = 32) or v[8 hf + 4 b + ...] (CH = 16)
     constexpr int CH = BN < 32 ? 16 : 32;  // columns per tensor-memory load
+    constexpr int FR = CH / 2;             // fragment words per half of the lanes
+    auto load_columns = [&](uint32_t addr, uint32_t* v) {
+      if (CH == 32) {
+        tmem_ld_16x256b_x4(addr, v);
+        tmem_ld_16x256b_x4(addr + (16u << 16), v + FR);
+      } else {
+        tmem_ld_16x256b_x2(addr, v);
+        tmem_ld_16x256b_x2(addr + (16u << 16), v + FR);
+      }
+    };
     while (walk.next()) {
       const int nt = walk.tile / p.mt * (PAIR ? 2 : 1) + int(rank), mt = walk.tile % p.mt;
       const int buf = seg % C::AB;
@@ -486,77 +523,70 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
       tc_fence_after();
       ++seg;
       if (walk.k0 == 0 && walk.k1 == p.ks) {
-        uint32_t h[BN / 2];
-        uint32_t v[2][32];
-        auto load = [&](int c) {
-          if (CH == 32)
-            tmem_ld_32x32(d + c, v[(c / CH) & 1]);
-          else
-            tmem_ld_32x16(d + c, v[(c / CH) & 1]);
-        };
-        load(0);
+        uint32_t h[BN / 2];  // 8 words per 16 tokens
+        uint32_t v[2][2 * FR];
+        load_columns(d, v[0]);
 #pragma unroll
         for (int c = 0; c < BN; c += CH) {
           tmem_wait_ld();
-          if (c + CH < BN) load(c + CH);  // under way while this one is packed
-          const uint32_t* w = v[(c / CH) & 1];
+          if (c + CH < BN) load_columns(d + c + CH, v[(c / CH + 1) & 1]);  // under way while this one is packed
+          const uint32_t* f = v[(c / CH) & 1];
 #pragma unroll
-          for (int j = 0; j < CH / 2; ++j)
-            h[c / 2 + j] = pack(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+          for (int q = 0; q < CH / 16; ++q)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int at = FR * (j >> 2) + 8 * q + 4 * ((j >> 1) & 1) + 2 * (j & 1);
+              h[c / 2 + 8 * q + j] = pack(f[at], f[at + 1]);
+            }
         }
         release();  // before the outputs are on their way
         if (!bad) {
 #pragma unroll
-          for (int c = 0; c < BN; c += kStoreRows) {
-            uint32_t hh[kStoreRows / 2];
-#pragma unroll
-            for (int j = 0; j < kStoreRows / 2; ++j) hh[j] = h[c / 2 + j];
-            emit(nt, mt, c, hh);
-          }
+          for (int c = 0; c < BN; c += kStoreRows) emit(nt, mt, c, h + c / 2);
         }
         continue;
       }
-      // a part of a tile: float32 sums to this CTA's slot, [column][128]
+      // a part of a tile: float32 sums to this CTA's slot, as the lanes hold them: [warp][16 tokens][16][32]
       const long long total = static_cast<long long>(p.tiles) * p.ks, t0 = static_cast<long long>(walk.tile) * p.ks;
       const int G = units;
       const int c_first = int(((t0 + 1) * G - 1) / total);
       const int parts = int(((t0 + p.ks) * G - 1) / total) - c_first + 1;
       const size_t slot_floats = size_t(BN) * kTileN;
       const int cols = min(BN, p.M - mt * BN);
-      float* dst = p.part + (2 * size_t(blockIdx.x) + (walk.k0 == 0 ? 1 : 0)) * slot_floats + 32 * w + lane;
+      const size_t mine = size_t(w) * BN * 32 + lane;
+      float* dst = p.part + (2 * size_t(blockIdx.x) + (walk.k0 == 0 ? 1 : 0)) * slot_floats + mine;
 #pragma unroll
       for (int c = 0; c < BN; c += CH) {
-        uint32_t v[32];
-        if (CH == 32)
-          tmem_ld_32x32(d + c, v);
-        else
-          tmem_ld_32x16(d + c, v);
+        uint32_t v[2 * FR];
+        load_columns(d + c, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
-          if (c + j < cols) dst[size_t(c + j) * kTileN] = __uint_as_float(v[j]);
+        for (int q = 0; q < CH / 16; ++q)
+          if (c + 16 * q < cols) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              dst[((c + 16 * q) + j) * 32] = __uint_as_float(v[FR * (j >> 3) + 8 * q + (j & 7)]);
+          }
       }
       release();
       __threadfence();
       named_barrier(1, 128);
       if (threadIdx.x == 128) *join = atomicInc(&p.count[c_first], unsigned(parts - 1)) == unsigned(parts - 1);
       named_barrier(1, 128);
-      const bool mine = *join && !bad;
-      if (mine) {
+      if (*join && !bad) {
         __threadfence();
         for (int c = 0; c < cols; c += kStoreRows) {
-          float acc[kStoreRows];
+          float acc[16];
 #pragma unroll
-          for (int j = 0; j < kStoreRows; ++j) acc[j] = 0.f;
+          for (int j = 0; j < 16; ++j) acc[j] = 0.f;
           for (int i = 0; i < parts; ++i) {
-            const float* src = p.part + (2 * size_t(c_first + i) + (i == 0)) * slot_floats + 32 * w + lane;
+            const float* src = p.part + (2 * size_t(c_first + i) + (i == 0)) * slot_floats + mine + c * 32;
 #pragma unroll
-            for (int j = 0; j < kStoreRows; ++j)
-              if (c + j < cols) acc[j] += __ldcg(src + size_t(c + j) * kTileN);
+            for (int j = 0; j < 16; ++j) acc[j] += __ldcg(src + j * 32);
           }
-          uint32_t hh[kStoreRows / 2];
+          uint32_t hh[8];
 #pragma unroll
-          for (int j = 0; j < kStoreRows / 2; ++j) hh[j] = pack(acc[2 * j], acc[2 * j + 1]);
+          for (int j = 0; j < 8; ++j) hh[j] = pack(__float_as_uint(acc[2 * j]), __float_as_uint(acc[2 * j + 1]));
           emit(nt, mt, c, hh);
         }
       }
@@ -693,7 +723,8 @@ fq_status fq_mx_gemm(const uint8_t* Xq, const uint8_t* Sx, const float* g_x, con
   if (st == FQ_OK)
     st = fq::make_tmap_2d(&m[3], Sx, CU_TENSOR_MAP_DATA_TYPE_INT64, sw, (M + 127) / 128, sw * 8, sb * 64, 1);
   if (st == FQ_OK)
-    st = fq::make_tmap_2d(&m[4], Y, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, N, M, size_t(N) * 2, 32, fq::kStoreRows);
+    st = fq::make_tmap_2d(&m[4], Y, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, N, M, size_t(N) * 2, 32, fq::kStoreRows,
+                          CU_TENSOR_MAP_SWIZZLE_64B);
   if (st != FQ_OK) return st;
   fq::MxGemmParams p{};
   p.gx = g_x;
