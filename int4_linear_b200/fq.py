@@ -72,41 +72,36 @@ class _KVCache(ctypes.Structure):
                 ("H", ctypes.c_int)]
 
 
+_HEAD_SCALE = 128 ** -0.5
 KV_TOKEN_BYTES = 132  # per token and head: K and V codes (64 bytes each), two fp16 scales
 
 
-@dataclass
 class KVCache:
     """A paged INT4 key/value cache: pool uint8 [num_pages, H, page_size * 132]
     (the bytes of a page and head: see fq_kv_cache in fq.h).  Make an empty one
     with kv_cache()."""
-    pool: torch.Tensor
+
+    def __init__(self, pool: torch.Tensor):
+        _check(pool, torch.uint8, "pool")
+        if pool.dim() != 3 or pool.shape[2] % KV_TOKEN_BYTES:
+            raise ValueError("pool must be [num_pages, H, page_size * 132]")
+        self._pool = pool
+        self.num_pages, self.heads = pool.shape[:2]
+        self.page_size = pool.shape[2] // KV_TOKEN_BYTES
+        self._c = _KVCache(pool.data_ptr(), self.num_pages, self.page_size, self.heads)
+        self._ref = ctypes.byref(self._c)
 
     @property
-    def num_pages(self) -> int:
-        return self.pool.shape[0]
-
-    @property
-    def heads(self) -> int:
-        return self.pool.shape[1]
-
-    @property
-    def page_size(self) -> int:
-        return self.pool.shape[2] // KV_TOKEN_BYTES
+    def pool(self) -> torch.Tensor:
+        return self._pool
 
     def views(self):
         """(K codes [P, H, page, 64], V codes, K scales fp16 [P, H, page], V scales): views of the pool."""
         n = self.page_size
-        parts = self.pool.split([64 * n, 64 * n, 2 * n, 2 * n], dim=-1)
+        parts = self._pool.split([64 * n, 64 * n, 2 * n, 2 * n], dim=-1)
         kq, vq = (x.unflatten(-1, (n, 64)) for x in parts[:2])
         ks, vs = (x.view(torch.float16) for x in parts[2:])
         return kq, vq, ks, vs
-
-    def as_c(self) -> _KVCache:
-        _check(self.pool, torch.uint8, "pool")
-        if self.pool.dim() != 3 or self.pool.shape[2] % KV_TOKEN_BYTES:
-            raise ValueError("pool must be [num_pages, H, page_size * 132]")
-        return _KVCache(self.pool.data_ptr(), self.num_pages, self.page_size, self.heads)
 
 
 def kv_cache(num_pages: int, heads: int, page_size: int, device="cuda") -> KVCache:
@@ -187,6 +182,8 @@ def _raise(status: int):
 def _check(t, dtype, name):
     if t is None:
         return
+    if type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -248,7 +245,7 @@ def _on(stream, *tensors):
 
 
 def _check_shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -260,12 +257,14 @@ def _check_rows(t, name, width):
     if t.dtype != torch.float16:
         raise ValueError(f"{name} must be torch.float16, got {t.dtype}")
     shape, strides = t.shape, t.stride()
-    n = 1
-    dense = True
-    for d in range(len(shape) - 1, 0, -1):
-        dense = dense and (strides[d] == n or shape[d] == 1)
-        n *= shape[d]
-    if len(shape) < 2 or shape[0] < 1 or n != width:
+    if len(shape) == 2:
+        n, dense = shape[1], strides[1] == 1 or shape[1] == 1
+    elif len(shape) == 3:
+        n = shape[1] * shape[2]
+        dense = (strides[2] == 1 or shape[2] == 1) and (strides[1] == shape[2] or shape[1] == 1)
+    else:
+        n = dense = None
+    if n != width or shape[0] < 1:
         raise ValueError(f"{name} must have rows of {width} values, got shape {tuple(shape)}")
     if not dense:
         raise ValueError(f"the rows of {name} must be contiguous")
@@ -441,79 +440,89 @@ def fq_kv_plan(lens, new_tokens, block_table, free_pages, pages_used, page_size:
     """Block tables and slots of one step from the request lengths: lens, new_tokens int32 [R],
     block_table int32 [R, max_pages] (updated in place), free_pages int32 [F], pages_used int32 [1].
     Returns (lens_out [R], token_start [R + 1], slots [max_tokens], pages_used_out [1])."""
-    for t, name in ((lens, "lens"), (new_tokens, "new_tokens"), (block_table, "block_table"),
-                    (free_pages, "free_pages"), (pages_used, "pages_used"), (lens_out, "lens_out"),
-                    (token_start, "token_start"), (slots, "slots"), (pages_used_out, "pages_used_out")):
-        _check(t, torch.int32, name)
-    r = lens.shape[0]
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [R, max_pages]")
+    i32 = torch.int32
+    _check(lens, i32, "lens")
+    _check(new_tokens, i32, "new_tokens")
+    _check(block_table, i32, "block_table")
+    _check(free_pages, i32, "free_pages")
+    _check(pages_used, i32, "pages_used")
+    r = lens.numel()
+    table_shape = block_table.shape
+    if lens.dim() != 1 or len(table_shape) != 2 or table_shape[0] != r:
+        raise ValueError(f"lens must be [R] and block_table [R, max_pages], got {tuple(lens.shape)} and "
+                         f"{tuple(table_shape)}")
     _check_shape(new_tokens, (r,), "new_tokens")
-    _check_shape(block_table, (r, block_table.shape[1]), "block_table")
     _check_shape(pages_used, (1,), "pages_used")
     with _on(stream, lens, new_tokens, block_table, free_pages, pages_used, lens_out, token_start, slots,
              pages_used_out) as s:
-        dev = lens.device
         if lens_out is None and token_start is None and slots is None and pages_used_out is None:
             # one allocation for the four
-            lens_out, token_start, slots, pages_used_out = torch.empty(
-                2 * r + 2 + max_tokens, dtype=torch.int32, device=dev).split([r, r + 1, max_tokens, 1])
-        lens_out = torch.empty(r, dtype=torch.int32, device=dev) if lens_out is None else lens_out
-        token_start = torch.empty(r + 1, dtype=torch.int32, device=dev) if token_start is None else token_start
-        slots = torch.empty(max_tokens, dtype=torch.int32, device=dev) if slots is None else slots
-        pages_used_out = torch.empty(1, dtype=torch.int32, device=dev) if pages_used_out is None else pages_used_out
-        _check_shape(lens_out, (r,), "lens_out")
-        _check_shape(token_start, (r + 1,), "token_start")
-        _check_shape(slots, (max_tokens,), "slots")
-        _check_shape(pages_used_out, (1,), "pages_used_out")
+            lens_out, token_start, slots, pages_used_out = torch.unsafe_split_with_sizes(
+                lens.new_empty(2 * r + 2 + max_tokens), [r, r + 1, max_tokens, 1])
+        else:
+            sizes = (r, r + 1, max_tokens, 1)
+            given = (lens_out, token_start, slots, pages_used_out)
+            for t, n, name in zip(given, sizes, ("lens_out", "token_start", "slots", "pages_used_out")):
+                if t is not None:
+                    _check(t, i32, name)
+                    _check_shape(t, (n,), name)
+            lens_out, token_start, slots, pages_used_out = (
+                lens.new_empty(n) if t is None else t for t, n in zip(given, sizes))
         _raise(lib().fq_kv_plan(lens.data_ptr(), new_tokens.data_ptr(), r, page_size, block_table.data_ptr(),
-                                block_table.shape[1], free_pages.data_ptr() or None, free_pages.numel(),
+                                table_shape[1], free_pages.data_ptr() or None, free_pages.numel(),
                                 pages_used.data_ptr(), lens_out.data_ptr(), token_start.data_ptr(),
                                 slots.data_ptr() or None, max_tokens, pages_used_out.data_ptr(), s))
     return lens_out, token_start, slots, pages_used_out
 
 
+def _check_slots(slots, t):
+    _check(slots, torch.int32, "slots")
+    _check_shape(slots, (t,), "slots")
+
+
 def fq_kv_write(K, V, slots, cache: KVCache, alpha_k: float = 1.0, alpha_v: float = 1.0, stream=None):
     """New keys and values (fp16 [T, H, 128] or [T, H * 128], rows any distance apart) into the
     cache's slots (int32 [T], -1: skipped) as INT4."""
-    c = cache.as_c()
-    t, ldk = _check_rows(K, "K", c.H * 128)
-    tv, ldv = _check_rows(V, "V", c.H * 128)
-    _check(slots, torch.int32, "slots")
-    _check_shape(slots, (t,), "slots")
+    width = cache.heads * 128
+    t, ldk = _check_rows(K, "K", width)
+    tv, ldv = _check_rows(V, "V", width)
     if tv != t:
         raise ValueError(f"K has {t} rows, V {tv}")
+    _check_slots(slots, t)
     with _on(stream, K, V, slots, cache.pool) as s:
         _raise(lib().fq_kv_write(K.data_ptr(), ldk, V.data_ptr(), ldv, t, slots.data_ptr(), alpha_k, alpha_v,
-                                 ctypes.byref(c), s))
+                                 cache._ref, s))
 
 
 def fq_kv_store(Kq, Ks, Vq, Vs, slots, cache: KVCache, stream=None):
     """Codes and scales that fq_quant_kv returned (uint8 [T, H * 64], fp16 [T, H]) into the cache's slots."""
-    c = cache.as_c()
+    h = cache.heads
     t = slots.shape[0]
-    for x, dt, w, name in ((Kq, torch.uint8, c.H * 64, "Kq"), (Ks, torch.float16, c.H, "Ks"),
-                           (Vq, torch.uint8, c.H * 64, "Vq"), (Vs, torch.float16, c.H, "Vs")):
+    for x, dt, w, name in ((Kq, torch.uint8, h * 64, "Kq"), (Ks, torch.float16, h, "Ks"),
+                           (Vq, torch.uint8, h * 64, "Vq"), (Vs, torch.float16, h, "Vs")):
         _check(x, dt, name)
         _check_shape(x, (t, w), name)
-    _check(slots, torch.int32, "slots")
+    _check_slots(slots, t)
     with _on(stream, Kq, Ks, Vq, Vs, slots, cache.pool) as s:
         _raise(lib().fq_kv_store(Kq.data_ptr(), Ks.data_ptr(), Vq.data_ptr(), Vs.data_ptr(), t, slots.data_ptr(),
-                                 ctypes.byref(c), s))
+                                 cache._ref, s))
 
 
 def fq_kv_read(cache: KVCache, slots, K=None, V=None, stream=None):
     """The cached tokens of `slots` (int32 [T]) as fp16 (K, V), each [T, H, 128]; zeros where a slot is no place."""
-    c = cache.as_c()
-    _check(slots, torch.int32, "slots")
-    shape = (slots.shape[0], c.H, 128)
+    t = slots.numel()
+    _check_slots(slots, t)
+    shape = (t, cache.heads, 128)
     with _on(stream, slots, cache.pool, K, V) as s:
-        K = torch.empty(shape, dtype=torch.float16, device=slots.device) if K is None else K
-        V = torch.empty(shape, dtype=torch.float16, device=slots.device) if V is None else V
         for x, name in ((K, "K"), (V, "V")):
-            _check(x, torch.float16, name)
-            _check_shape(x, shape, name)
-        _raise(lib().fq_kv_read(ctypes.byref(c), slots.data_ptr(), shape[0], K.data_ptr(), V.data_ptr(), s))
+            if x is not None:
+                _check(x, torch.float16, name)
+                _check_shape(x, shape, name)
+        if K is None:
+            K = slots.new_empty(shape, dtype=torch.float16)
+        if V is None:
+            V = slots.new_empty(shape, dtype=torch.float16)
+        _raise(lib().fq_kv_read(cache._ref, slots.data_ptr(), t, K.data_ptr(), V.data_ptr(), s))
     return K, V
 
 
@@ -532,29 +541,32 @@ def fq_kv_attn(Q, lens, block_table, cache: KVCache, scale: float | None = None,
     """Attention of one new token per request over the paged cache: Q fp16 [R, Hq, 128] or
     [R, Hq * 128] (rows any distance apart), lens int32 [R], block_table int32 [R, max_pages];
     scale defaults to 128^-0.5, window > 0 keeps the last `window` tokens.  Returns Y fp16 [R, Hq * 128]."""
-    c = cache.as_c()
     _check(lens, torch.int32, "lens")
     _check(block_table, torch.int32, "block_table")
-    r = lens.shape[0]
-    if block_table.dim() != 2 or Q.dim() < 2:
-        raise ValueError("block_table must be [R, max_pages] and Q [R, Hq, 128] or [R, Hq * 128]")
-    _check_shape(block_table, (r, block_table.shape[1]), "block_table")
-    width = Q.shape[-1] * (Q.shape[1] if Q.dim() == 3 else 1)
+    r = lens.numel()
+    table_shape, q_shape = block_table.shape, Q.shape
+    if lens.dim() != 1 or len(table_shape) != 2 or table_shape[0] != r:
+        raise ValueError(f"lens must be [R] and block_table [R, max_pages], got {tuple(lens.shape)} and "
+                         f"{tuple(table_shape)}")
+    width = q_shape[-1] * (q_shape[1] if len(q_shape) == 3 else 1) if len(q_shape) > 1 else 0
     rows, ldq = _check_rows(Q, "Q", width)
     if rows != r or width < 128 or width % 128:
-        raise ValueError(f"Q must have {r} rows of Hq * 128 values, got shape {tuple(Q.shape)}")
+        raise ValueError(f"Q must have {r} rows of Hq * 128 values, got shape {tuple(q_shape)}")
     hq = width // 128
     with _on(stream, Q, lens, block_table, cache.pool, Y, workspace) as s:
-        Y = torch.empty(r, hq * 128, dtype=torch.float16, device=Q.device) if Y is None else Y
-        _check(Y, torch.float16, "Y")
-        if Y.numel() != r * hq * 128:
-            raise ValueError(f"Y must hold {r} x {hq * 128} values, got shape {tuple(Y.shape)}")
+        if Y is None:
+            Y = Q.new_empty((r, width))
+        else:
+            _check(Y, torch.float16, "Y")
+            if Y.numel() != r * width:
+                raise ValueError(f"Y must hold {r} x {width} values, got shape {tuple(Y.shape)}")
         if workspace is None:
-            workspace = fq_kv_attn_workspace(r, hq, c.H, Q.device)
-        _check(workspace, torch.uint8, "workspace")
-        _raise(lib().fq_kv_attn(Q.data_ptr(), ldq, r, hq, lens.data_ptr(), block_table.data_ptr(),
-                                block_table.shape[1], ctypes.byref(c), 128 ** -0.5 if scale is None else scale,
-                                window, Y.data_ptr(), workspace.data_ptr(), workspace.numel(), s))
+            workspace = fq_kv_attn_workspace(r, hq, cache.heads, Q.device)
+        else:
+            _check(workspace, torch.uint8, "workspace")
+        _raise(lib().fq_kv_attn(Q.data_ptr(), ldq, r, hq, lens.data_ptr(), block_table.data_ptr(), table_shape[1],
+                                cache._ref, _HEAD_SCALE if scale is None else scale, window, Y.data_ptr(),
+                                workspace.data_ptr(), workspace.numel(), s))
     return Y
 
 
@@ -564,42 +576,55 @@ def fq_mx_scale_bytes(rows: int, k: int, fmt: int) -> int:
 
 
 def _check_mx(Q, S, fmt, name):
+    """(rows, K) of microscaled codes Q [rows, K/2] with their tiled scales S."""
     _check(Q, torch.uint8, name + "q")
     _check(S, torch.uint8, "S" + name.lower())
-    if Q.dim() != 2:
+    shape = Q.shape
+    if len(shape) != 2:
         raise ValueError(f"{name}q must be [rows, K/2]")
-    need = fq_mx_scale_bytes(Q.shape[0], 2 * Q.shape[1], fmt)
+    rows, k = shape[0], 2 * shape[1]
+    need = (rows + 127) // 128 * 128 * (k // (16 if fmt == NVFP4 else 32))
     if S.numel() != need:
         raise ValueError(f"S{name.lower()} must hold {need} bytes, got {S.numel()}")
+    return rows, k
+
+
+def _check_x(X, name):
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        raise ValueError(f"{name} must be a CUDA tensor [rows, K]")
+    k = X.shape[1]
+    r, ldx = _check_rows(X, name, k)
+    return r, k, ldx
 
 
 def fq_mx_quant(X, fmt: int, g=None, Q=None, S=None, stream=None):
     """fp16 [R, K] (rows any distance apart) to microscaled 4-bit codes: (Q uint8 [R, K/2], S uint8, the
     tiled scales).  fmt MXFP4 or NVFP4 (g: its float32 [1] tensor scale on the device, None: 1)."""
-    if not isinstance(X, torch.Tensor) or X.dim() != 2:
-        raise ValueError("X must be a CUDA tensor [R, K]")
-    r, ldx = _check_rows(X, "X", X.shape[1])
-    k = X.shape[1]
-    _check(g, torch.float32, "g")
+    r, k, ldx = _check_x(X, "X")
+    _check_g(g, "g")
     with _on(stream, X, g, Q, S) as s:
-        Q = torch.empty(r, k // 2, dtype=torch.uint8, device=X.device) if Q is None else Q
-        S = torch.empty(fq_mx_scale_bytes(r, k, fmt), dtype=torch.uint8, device=X.device) if S is None else S
-        if fq_mx_scale_bytes(r, k, fmt):
-            _check_shape(Q, (r, k // 2), "Q")
+        if Q is None:
+            Q = X.new_empty((r, k // 2), dtype=torch.uint8)
+        if S is None:
+            S = X.new_empty(fq_mx_scale_bytes(r, k, fmt), dtype=torch.uint8)
+        elif k % 128 == 0:
             _check_mx(Q, S, fmt, "X")
-        _raise(lib().fq_mx_quant(X.data_ptr(), ldx, r, k, fmt, _p(g), Q.data_ptr(), S.data_ptr(), s))
+        _check(Q, torch.uint8, "Q")
+        _check_shape(Q, (r, k // 2), "Q")
+        _raise(lib().fq_mx_quant(X.data_ptr(), ldx, r, k, fmt, _p(g), Q.data_ptr(), S.data_ptr() or None, s))
     return Q, S
 
 
 def fq_mx_dequant(Q, S, fmt: int, g=None, X=None, stream=None):
     """Microscaled codes back to fp16 [R, K]."""
-    _check_mx(Q, S, fmt, "X")
-    _check(g, torch.float32, "g")
-    r, k = Q.shape[0], 2 * Q.shape[1]
+    r, k = _check_mx(Q, S, fmt, "X")
+    _check_g(g, "g")
     with _on(stream, Q, S, g, X) as s:
-        X = torch.empty(r, k, dtype=torch.float16, device=Q.device) if X is None else X
-        _check(X, torch.float16, "X")
-        _check_shape(X, (r, k), "X")
+        if X is None:
+            X = Q.new_empty((r, k), dtype=torch.float16)
+        else:
+            _check(X, torch.float16, "X")
+            _check_shape(X, (r, k), "X")
         _raise(lib().fq_mx_dequant(Q.data_ptr(), S.data_ptr(), r, k, fmt, _p(g), X.data_ptr(), s))
     return X
 
@@ -618,19 +643,32 @@ def fq_mx_linear_workspace(m: int, n: int, k: int, fmt: int, device="cuda"):
         return torch.zeros(fq_mx_linear_workspace_size(m, n, k, fmt), dtype=torch.uint8, device=device)
 
 
+def _check_g(g, name):
+    if g is not None:
+        _check(g, torch.float32, name)
+        if g.numel() != 1:
+            raise ValueError(f"{name} must hold one value, got shape {tuple(g.shape)}")
+
+
+def _mx_out(like, Y, m, n):
+    if Y is None:
+        return like.new_empty((m, n), dtype=torch.float16)
+    _check(Y, torch.float16, "Y")
+    _check_shape(Y, (m, n), "Y")
+    return Y
+
+
 def fq_mx_gemm(Xq, Sx, Wq, Sw, fmt: int, g_x=None, g_w=None, Y=None, workspace=None, stream=None):
     """Y fp16 [M, N] = the block-scaled product of microscaled activations and weights
     (codes and scales as fq_mx_quant returns them), times g_x g_w."""
-    _check_mx(Xq, Sx, fmt, "X")
-    _check_mx(Wq, Sw, fmt, "W")
-    _check(g_x, torch.float32, "g_x")
-    _check(g_w, torch.float32, "g_w")
-    m, k, n = Xq.shape[0], 2 * Xq.shape[1], Wq.shape[0]
-    _check_shape(Wq, (n, k // 2), "Wq")
+    m, k = _check_mx(Xq, Sx, fmt, "X")
+    n, kw = _check_mx(Wq, Sw, fmt, "W")
+    if kw != k:
+        raise ValueError(f"Xq has K = {k}, Wq {kw}")
+    _check_g(g_x, "g_x")
+    _check_g(g_w, "g_w")
     with _on(stream, Xq, Sx, Wq, Sw, g_x, g_w, Y, workspace) as s:
-        Y = torch.empty(m, n, dtype=torch.float16, device=Xq.device) if Y is None else Y
-        _check(Y, torch.float16, "Y")
-        _check_shape(Y, (m, n), "Y")
+        Y = _mx_out(Xq, Y, m, n)
         ws, wsb = _workspace(fq_mx_gemm_workspace_size(m, n, k, fmt), Xq.device, workspace)
         _raise(lib().fq_mx_gemm(Xq.data_ptr(), Sx.data_ptr(), _p(g_x), Wq.data_ptr(), Sw.data_ptr(), _p(g_w), m, n, k,
                                 fmt, Y.data_ptr(), _p(ws), wsb, s))
@@ -640,21 +678,20 @@ def fq_mx_gemm(Xq, Sx, Wq, Sw, fmt: int, g_x=None, g_w=None, Y=None, workspace=N
 def fq_mx_linear(X, fmt: int, Wq, Sw, g_x=None, g_w=None, Y=None, workspace=None, stream=None):
     """Y fp16 [M, N]: X fp16 [M, K] (rows any distance apart) quantized to microscaled 4-bit,
     times the microscaled weights Wq [N, K/2], Sw, on one stream."""
-    if not isinstance(X, torch.Tensor) or X.dim() != 2:
-        raise ValueError("X must be a CUDA tensor [M, K]")
-    m, ldx = _check_rows(X, "X", X.shape[1])
-    k, n = X.shape[1], Wq.shape[0]
-    _check_mx(Wq, Sw, fmt, "W")
-    _check_shape(Wq, (n, k // 2), "Wq")
-    _check(g_x, torch.float32, "g_x")
-    _check(g_w, torch.float32, "g_w")
+    m, k, ldx = _check_x(X, "X")
+    n, kw = _check_mx(Wq, Sw, fmt, "W")
+    if kw != k:
+        raise ValueError(f"X has K = {k}, Wq {kw}")
+    _check_g(g_x, "g_x")
+    _check_g(g_w, "g_w")
     with _on(stream, X, Wq, Sw, g_x, g_w, Y, workspace) as s:
-        Y = torch.empty(m, n, dtype=torch.float16, device=X.device) if Y is None else Y
-        _check(Y, torch.float16, "Y")
-        _check_shape(Y, (m, n), "Y")
-        ws, wsb = _workspace(fq_mx_linear_workspace_size(m, n, k, fmt), X.device, workspace)
+        Y = _mx_out(X, Y, m, n)
+        if workspace is None:
+            workspace = fq_mx_linear_workspace(m, n, k, fmt, X.device)
+        else:
+            _check(workspace, torch.uint8, "workspace")
         _raise(lib().fq_mx_linear(X.data_ptr(), ldx, m, k, fmt, _p(g_x), Wq.data_ptr(), Sw.data_ptr(), _p(g_w), n,
-                                  Y.data_ptr(), _p(ws), wsb, s))
+                                  Y.data_ptr(), workspace.data_ptr(), workspace.numel(), s))
     return Y
 
 
