@@ -818,7 +818,8 @@ template <int NT, bool P16>
 fq_status launch_attn(const AttnParams& p, cudaStream_t stream) {
   auto kern = kv_attn_kernel<NT, P16>;
   constexpr size_t smem = size_t(kWarps) * (kDepth * kStepBytes + NT * kPieceFloats * sizeof(float));
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+  static std::atomic<uint64_t> allowed{0};
+  if (!allow_smem(kern, smem, allowed))
     return fail(FQ_ERR_CUDA, "cannot reserve %zu bytes of shared memory", smem);
   launch_pdl(kern, dim3(attn_grid(NT)), dim3(kAttnThreads), smem, stream, p);
   return check_launch("kv_attn_kernel");

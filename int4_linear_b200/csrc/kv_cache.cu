@@ -132,8 +132,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
     for (int o = 16; o; o >>= 1) grant_end = max(grant_end, __shfl_xor_sync(0xffffffffu, grant_end, o));
     if ((tid & 31) == 0) part[tid >> 5] = grant_end;
     __syncthreads();
-#pragma unroll 1
-    for (int w = 0; w < kPlanThreads / 32; ++w) taken = max(taken, part[w]);
+    grant_end = part[tid & 31];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) grant_end = max(grant_end, __shfl_xor_sync(0xffffffffu, grant_end, o));
+    taken = max(taken, grant_end);
     __syncthreads();
   }
   if (ncta > 1)
@@ -158,21 +160,48 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
     const int held = (s_len[r] + page - 1) >> p.page_shift;
     p.table[size_t(r) * p.max_pages + held + (j - s_first[r])] = p.free_pages[used + j];
   }
-  // per row of the batch; a page that this step takes is read from the free
-  // list, so that no CTA waits for another's table entries
-  for (int i = rank * kPlanThreads + tid; i < p.max_tokens; i += ncta * kPlanThreads) {
-    int slot = -1;
-    if (i < tokens) {
-      const int r = last_not_above(s_start, p.R, i);
-      const int l = s_len[r];
-      if (l >= 0) {
+  // per row of the batch, four at a time so that their searches and loads overlap; a page that this
+  // step takes is read from the free list, so that no CTA waits for another's table entries
+  const int stride = ncta * kPlanThreads;
+  for (int i0 = rank * kPlanThreads + tid; i0 < p.max_tokens; i0 += 4 * stride) {
+    int lo[4], hi[4], slot[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      lo[u] = 0;
+      hi[u] = p.R;
+    }
+    while (hi[0] - lo[0] > 1) {  // the same number of halvings for all, give or take one
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int mid = (lo[u] + hi[u]) >> 1;
+        if (s_start[mid] <= i0 + u * stride)
+          lo[u] = mid;
+        else
+          hi[u] = mid;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * stride;
+      while (hi[u] - lo[u] > 1) {
+        const int mid = (lo[u] + hi[u]) >> 1;
+        if (s_start[mid] <= i)
+          lo[u] = mid;
+        else
+          hi[u] = mid;
+      }
+      slot[u] = -1;
+      const int r = lo[u], l = s_len[r];
+      if (i < tokens && l >= 0) {
         const int pos = l + (i - s_start[r]);
         const int pi = pos >> p.page_shift, held = (l + page - 1) >> p.page_shift;
         const int id = pi < held ? p.table[size_t(r) * p.max_pages + pi] : p.free_pages[used + s_first[r] + pi - held];
-        slot = id * page + (pos & (page - 1));
+        slot[u] = id * page + (pos & (page - 1));
       }
     }
-    p.slots[i] = slot;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i0 + u * stride < p.max_tokens) p.slots[i0 + u * stride] = slot[u];
   }
 }
 
@@ -180,74 +209,101 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
 
 constexpr int kRowThreads = 256;
 
-// clamp(round-half-even(v / s), -8, 7) for fp16 values v and an fp16 scale s > 0
-// (both widened), inv ~ 1 / s.  v / s differs from a tie (k + 1/2) by at least
-// 2^-12 unless it is one, since v and s have 11 bits each, so the nearest integer of
-// v * inv is right except on a tie; there |v - q s| = s / 2 exactly, and q moves to
-// the even neighbour.
-__device__ __forceinline__ int code_f16(float v, float s, float inv) {
-  float q = rintf(__fmul_rn(v, inv));
-  const float e = __fmaf_rn(-q, s, v);
-  int c = int(q);
-  if (fabsf(e) + fabsf(e) == s && (c & 1)) c += e > 0.f ? 1 : -1;
-  return min(max(c, -8), 7);
+// Codes clamp(round-half-even(v / s), -8, 7) of eight fp16 values and an fp16 scale s > 0, packed.
+// v and s have 11 bits each, so v / s is a tie (k + 1/2) or at least 2^-12 from one.  Rounding v / s
+// (1 - 2^-21) and v / s (1 + 2^-21) to integers therefore gives the same number twice, or at a tie
+// the two neighbours, and half their sum, rounded to even, is the code; this takes five packed float32
+// operations per two values where the divisions took the kernel's time.  Values past the clamp
+// are cut first, to 7.25 s and -8.25 s, which round to 7 and -8.
+__device__ __forceinline__ uint32_t codes8(const __half2 (&v)[4], __half2 top, __half2 bottom, float2 inv_dn,
+                                           float2 inv_up) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer in the low bits
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(__hmax2(__hmin2(v[j], top), bottom));
+    const float2 m = make_float2(kMagic, kMagic);
+    const float2 a = ffma2(f, inv_dn, m), b = ffma2(f, inv_up, m);
+    const float2 sum = fadd2(a, fadd2(b, make_float2(-2.0f * kMagic, -2.0f * kMagic)));
+    const float2 q = ffma2(sum, make_float2(0.5f, 0.5f), m);
+    const uint32_t lo = __float_as_uint(q.x) & 15u, hi = __float_as_uint(q.y) & 15u;
+    w |= (lo | hi << 4) << (8 * j);
+  }
+  return w;
 }
 
-// One head vector per 8 lanes: 32 bytes in, 8 bytes of codes out per lane.
-// Bound by HBM (256 bytes read, 66 written per vector).
+// Token, head and kind (0 key, 1 value) of vector vec, a token's vectors being its H keys, then its H values.
+struct KvVec {
+  long long t;
+  int h, which;
+};
+__device__ __forceinline__ KvVec kv_vector(long long vec, int H) {
+  const uint32_t per = 2u * uint32_t(H);
+  KvVec v;
+  v.t = (vec >> 32) == 0 ? uint32_t(vec) / per : vec / per;
+  const int h = int(vec - v.t * per);
+  v.which = h >= H;
+  v.h = v.which ? h - H : h;
+  return v;
+}
+
+// One head vector per 8 lanes: 32 bytes in, 8 bytes of codes out per lane, two vectors per turn, read
+// before their slots are known so that the loads overlap.  Bound by HBM (256 bytes read, 66 written per vector).
 __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const __half* __restrict__ K, long long ldk,
                                                                const __half* __restrict__ V, long long ldv, int T,
                                                                const int32_t* __restrict__ slots, float alpha_k,
                                                                float alpha_v, KvView c) {
   pdl_launch_dependents();
   pdl_wait();
+  constexpr int kVecs = 2;
   const int sub = threadIdx.x & 7;
-  const long long nvec = 2ll * T * c.H;
   const int limit = c.num_pages << c.page_shift;
+  const long long total = 2ll * T * c.H;
   const long long step = static_cast<long long>(gridDim.x) * (kRowThreads / 8);
   // every lane of a warp takes the same number of turns (the shuffles below)
   const long long first = static_cast<long long>(blockIdx.x) * (kRowThreads / 8) + (threadIdx.x >> 3);
-  const long long turns = (nvec - (first - ((threadIdx.x >> 3) & 3)) + step - 1) / step;
-  for (long long it = 0; it < turns; ++it) {
-    const long long vec = first + it * step;
-    int slot = -1, h = 0, which = 0;
-    long long t = 0;
-    if (vec < nvec) {
-      h = int(vec % c.H);
-      const long long tw = vec / c.H;
-      which = int(tw & 1);
-      t = tw >> 1;
-      slot = slots[t];
-    }
-    const bool ok = slot >= 0 && slot < limit;
-    uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (ok) {
-      const uint4* src = reinterpret_cast<const uint4*>((which ? V + t * ldv : K + t * ldk) + h * kHeadDim) + 2 * sub;
-      raw[0] = src[0];
-      raw[1] = src[1];
-    }
-    const __half2* h2 = reinterpret_cast<const __half2*>(raw);
-    __half2 m2 = __habs2(h2[0]);
+  for (long long base = first - ((threadIdx.x >> 3) & 3); base < total; base += kVecs * step) {
+    const long long vec0 = base + ((threadIdx.x >> 3) & 3);
+    KvVec v[kVecs];
+    uint4 raw[kVecs][2];
+    int slot[kVecs];
 #pragma unroll
-    for (int j = 1; j < 8; ++j) m2 = __hmax2(m2, __habs2(h2[j]));
-    float m = __half2float(__hmax(__low2half(m2), __high2half(m2)));
-#pragma unroll
-    for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const __half sh = __float2half_rn(__fdiv_rn(__fmul_rn(m, which ? alpha_v : alpha_k), 7.0f));
-    const float s = __half2float(sh);
-    const float inv = s > 0.f ? __fdividef(1.0f, s) : 0.f;
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 f = __half22float2(h2[j]);
-      w[j >> 2] |= (uint32_t(code_f16(f.x, s, inv)) & 15u) << (8 * (j & 3));
-      w[j >> 2] |= (uint32_t(code_f16(f.y, s, inv)) & 15u) << (8 * (j & 3) + 4);
+    for (int u = 0; u < kVecs; ++u) {
+      raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+      slot[u] = -1;
+      if (vec0 + u * step < total) {
+        v[u] = kv_vector(vec0 + u * step, c.H);
+        const uint4* src =
+            reinterpret_cast<const uint4*>((v[u].which ? V + v[u].t * ldv : K + v[u].t * ldk) + v[u].h * kHeadDim) +
+            2 * sub;
+        raw[u][0] = src[0];
+        raw[u][1] = src[1];
+        slot[u] = slots[v[u].t];
+      }
     }
-    if (ok) {
-      uint8_t* base = c.block(slot >> c.page_shift, h);
-      const int off = slot & ((1 << c.page_shift) - 1);
-      *reinterpret_cast<uint2*>(base + c.codes(which) + off * kKvRowBytes + 8 * sub) = make_uint2(w[0], w[1]);
-      if (sub == 0) *reinterpret_cast<__half*>(base + c.scales(which) + 2 * off) = sh;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const __half2(&h2)[8] = reinterpret_cast<const __half2(&)[8]>(raw[u]);
+      __half2 m2 = __habs2(h2[0]);
+#pragma unroll
+      for (int j = 1; j < 8; ++j) m2 = __hmax2(m2, __habs2(h2[j]));
+      float m = __half2float(__hmax(__low2half(m2), __high2half(m2)));
+#pragma unroll
+      for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (slot[u] < 0 || slot[u] >= limit) continue;
+      const __half sh = __float2half_rn(__fdiv_rn(__fmul_rn(m, v[u].which ? alpha_v : alpha_k), 7.0f));
+      const float s = __half2float(sh);
+      const float inv = s > 0.f ? __fdividef(1.0f, s) : 0.f;  // s = 0: codes 0
+      const __half2 top = __float2half2_rn(7.25f * s), bottom = __float2half2_rn(-8.25f * s);
+      const float dn = inv * (1.0f - 0x1p-21f), up = inv * (1.0f + 0x1p-21f);
+      const uint32_t w0 = codes8(reinterpret_cast<const __half2(&)[4]>(h2[0]), top, bottom, make_float2(dn, dn),
+                                 make_float2(up, up));
+      const uint32_t w1 = codes8(reinterpret_cast<const __half2(&)[4]>(h2[4]), top, bottom, make_float2(dn, dn),
+                                 make_float2(up, up));
+      uint8_t* page = c.block(slot[u] >> c.page_shift, v[u].h);
+      const int off = slot[u] & ((1 << c.page_shift) - 1);
+      *reinterpret_cast<uint2*>(page + c.codes(v[u].which) + off * kKvRowBytes + 8 * sub) = make_uint2(w0, w1);
+      if (sub == 0) *reinterpret_cast<__half*>(page + c.scales(v[u].which) + 2 * off) = sh;
     }
   }
 }
@@ -261,14 +317,13 @@ __global__ void __launch_bounds__(kRowThreads) kv_store_kernel(const uint8_t* __
   pdl_launch_dependents();
   pdl_wait();
   const int sub = threadIdx.x & 3;
-  const long long nvec = 2ll * T * c.H;
   const int limit = c.num_pages << c.page_shift;
-  for (long long vec = static_cast<long long>(blockIdx.x) * (kRowThreads / 4) + (threadIdx.x >> 2); vec < nvec;
+  const long long total = 2ll * T * c.H;
+  for (long long vec = static_cast<long long>(blockIdx.x) * (kRowThreads / 4) + (threadIdx.x >> 2); vec < total;
        vec += static_cast<long long>(gridDim.x) * (kRowThreads / 4)) {
-    const int h = int(vec % c.H);
-    const long long tw = vec / c.H;
-    const int which = int(tw & 1);
-    const long long t = tw >> 1;
+    const KvVec v = kv_vector(vec, c.H);
+    const long long t = v.t;
+    const int h = v.h, which = v.which;
     const int slot = slots[t];
     if (slot < 0 || slot >= limit) continue;
     const long long row = t * c.H + h;
@@ -280,41 +335,59 @@ __global__ void __launch_bounds__(kRowThreads) kv_store_kernel(const uint8_t* __
   }
 }
 
-// One head vector per 8 lanes: 8 bytes of codes in, 32 bytes out per lane.
-// The product of a 4-bit code and an 11-bit scale is exact in float32, so
-// there is one rounding, to fp16.
+// One head vector per 8 lanes: 8 bytes of codes in, 32 bytes out per lane, four vectors per turn so that
+// their slots and codes are loaded together.  The product of a 4-bit code and an 11-bit scale is exact
+// in float32, so there is one rounding, to fp16.
 __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const int32_t* __restrict__ slots, int T,
                                                               __half* __restrict__ K, __half* __restrict__ V,
                                                               KvView c) {
   pdl_launch_dependents();
   pdl_wait();
+  constexpr int kVecs = 4;
   const int sub = threadIdx.x & 7;
-  const long long nvec = 2ll * T * c.H;
   const int limit = c.num_pages << c.page_shift;
-  for (long long vec = static_cast<long long>(blockIdx.x) * (kRowThreads / 8) + (threadIdx.x >> 3); vec < nvec;
-       vec += static_cast<long long>(gridDim.x) * (kRowThreads / 8)) {
-    const int h = int(vec % c.H);
-    const long long tw = vec / c.H;
-    const int which = int(tw & 1);
-    const long long t = tw >> 1;
-    const int slot = slots[t];
-    uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (slot >= 0 && slot < limit) {
-      const uint8_t* base = c.block(slot >> c.page_shift, h);
-      const int off = slot & ((1 << c.page_shift) - 1);
-      const uint2 w = *reinterpret_cast<const uint2*>(base + c.codes(which) + off * kKvRowBytes + 8 * sub);
-      const float s = __half2float(*reinterpret_cast<const __half*>(base + c.scales(which) + 2 * off));
+  const long long total = 2ll * T * c.H;
+  const long long step = static_cast<long long>(gridDim.x) * (kRowThreads / 8);
+  for (long long vec = static_cast<long long>(blockIdx.x) * (kRowThreads / 8) + (threadIdx.x >> 3); vec < total;
+       vec += kVecs * step) {
+    KvVec v[kVecs];
+    int slot[kVecs];
+    uint2 w[kVecs];
+    float s[kVecs];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      slot[u] = -1;
+      if (vec + u * step < total) {
+        v[u] = kv_vector(vec + u * step, c.H);
+        slot[u] = slots[v[u].t];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      w[u] = make_uint2(0, 0);
+      s[u] = 0.f;
+      if (slot[u] >= 0 && slot[u] < limit) {
+        const uint8_t* page = c.block(slot[u] >> c.page_shift, v[u].h);
+        const int off = slot[u] & ((1 << c.page_shift) - 1);
+        w[u] = *reinterpret_cast<const uint2*>(page + c.codes(v[u].which) + off * kKvRowBytes + 8 * sub);
+        s[u] = __half2float(*reinterpret_cast<const __half*>(page + c.scales(v[u].which) + 2 * off));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      if (vec + u * step >= total) break;
+      uint4 out[2];
       __half2* o2 = reinterpret_cast<__half2*>(out);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int b = int(((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 255u);
+        const int b = int(((j < 4 ? w[u].x : w[u].y) >> (8 * (j & 3))) & 255u);
         const int lo = (b << 28) >> 28, hi = (b << 24) >> 28;
-        o2[j] = __floats2half2_rn(float(lo) * s, float(hi) * s);
+        o2[j] = __floats2half2_rn(float(lo) * s[u], float(hi) * s[u]);
       }
+      uint4* dst = reinterpret_cast<uint4*>((v[u].which ? V : K) + (v[u].t * c.H + v[u].h) * kHeadDim) + 2 * sub;
+      dst[0] = out[0];
+      dst[1] = out[1];
     }
-    uint4* dst = reinterpret_cast<uint4*>((which ? V : K) + (t * c.H + h) * kHeadDim) + 2 * sub;
-    dst[0] = out[0];
-    dst[1] = out[1];
   }
 }
 

@@ -26,15 +26,37 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   return r;
 }
 
+// Codes of 16 values times inv.
+__device__ __forceinline__ void codes16(const __half2* h2, float inv, uint32_t (&q)[2]) {
+  q[0] = q[1] = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 f = fmul2(__half22float2(h2[j]), make_float2(inv, inv));
+    q[j >> 2] |= e2m1x2(f.x, f.y) << (8 * (j & 3));
+  }
+}
+
+// Codes of 16 values over d.
+__device__ __noinline__ void codes16_divided(const __half2* h2, float d, uint32_t (&q)[2]) {
+  q[0] = q[1] = 0;
+  for (int j = 0; j < 8; ++j) {
+    const float2 f = __half22float2(h2[j]);
+    const uint32_t b = e2m1x2(__fdiv_rn(f.x, d), __fdiv_rn(f.y, d)) << (8 * (j & 3));
+    if (j < 4)
+      q[0] |= b;
+    else
+      q[1] |= b;
+  }
+}
+
 __device__ __forceinline__ float e4m3_value(uint8_t b) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
 }
 
 // One thread per 16 values: 32 bytes in, 8 bytes of codes out, and the scales
 // of four blocks leave as one word from the first of the threads that hold
-// them (a scale tile keeps a row's four blocks together).  Bound by HBM for
-// E8M0 (2 bytes read and 0.53 written per value); the float32 divisions of
-// the E4M3 form keep its instruction rate near the memory's.
+// them (a scale tile keeps a row's four blocks together).  Bound by HBM in
+// both formats (2 bytes read and 0.53 or 0.56 written per value).
 template <int FMT, typename Index>
 __global__ void __launch_bounds__(kMxThreads) mx_quant_kernel(const __half* __restrict__ X, long long ldx, int R,
                                                               int K, const float* __restrict__ g, uint8_t* Q,
@@ -72,20 +94,17 @@ __global__ void __launch_bounds__(kMxThreads) mx_quant_kernel(const __half* __re
       if (!finite) sb = 0x7Fu;
     }
     uint32_t q[2] = {0, 0};
-    if (finite && (FMT == FQ_MXFP4 || d != 0.f)) {
-      const __half2* h2 = reinterpret_cast<const __half2*>(raw);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float2 f = __half22float2(h2[j]);
-        if (FMT == FQ_MXFP4) {
-          f.x *= inv;
-          f.y *= inv;
-        } else {
-          f.x = __fdiv_rn(f.x, d);
-          f.y = __fdiv_rn(f.y, d);
-        }
-        q[j >> 2] |= e2m1x2(f.x, f.y) << (8 * (j & 3));
-      }
+    const __half2* h2 = reinterpret_cast<const __half2*>(raw);
+    if (FMT == FQ_MXFP4) {
+      if (finite) codes16(h2, inv, q);
+    } else if (finite && d != 0.f) {
+      // the codes of the quotients a little below and a little above; where they differ (next to
+      // a tie), or the reciprocal may overflow, the division itself decides
+      inv = __fdividef(1.0f, d);
+      uint32_t up[2];
+      codes16(h2, inv * (1.0f - 0x1p-20f), q);
+      codes16(h2, inv * (1.0f + 0x1p-20f), up);
+      if (q[0] != up[0] || q[1] != up[1] || d < 0x1p-100f) codes16_divided(h2, d, q);
     }
     *reinterpret_cast<uint2*>(Q + static_cast<size_t>(r) * (K / 2) + c * 8) = make_uint2(q[0], q[1]);
     // the scales of four blocks: every thread (E4M3) or every other one (E8M0)

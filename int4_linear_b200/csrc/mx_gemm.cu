@@ -642,7 +642,8 @@ template <int FMT, int BN, bool PAIR>
 fq_status launch_mx(const MxGemmParams& p, const CUtensorMap (&m)[5], int grid, cudaStream_t stream) {
   using C = MxCfg<FMT, BN, PAIR>;
   auto kern = mx_gemm_kernel<FMT, BN, PAIR>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+  static std::atomic<uint64_t> allowed{0};
+  if (!allow_smem(kern, C::SMEM, allowed))
     return fail(FQ_ERR_CUDA, "cannot reserve %d bytes of shared memory", C::SMEM);
   if (PAIR)
     launch_pdl_cluster(kern, dim3(grid), dim3(kMxGemmThreads), C::SMEM, stream, 2, p, m[0], m[1], m[2], m[3], m[4]);
