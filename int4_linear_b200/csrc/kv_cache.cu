@@ -210,22 +210,19 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
 constexpr int kRowThreads = 256;
 
 // Codes clamp(round-half-even(v / s), -8, 7) of eight fp16 values and an fp16 scale s > 0, packed.
-// v and s have 11 bits each, so v / s is a tie (k + 1/2) or at least 2^-12 from one.  Rounding v / s
-// (1 - 2^-21) and v / s (1 + 2^-21) to integers therefore gives the same number twice, or at a tie
-// the two neighbours, and half their sum, rounded to even, is the code; this takes five packed float32
-// operations per two values where the divisions took the kernel's time.  Values past the clamp
-// are cut first, to 7.25 s and -8.25 s, which round to 7 and -8.
-__device__ __forceinline__ uint32_t codes8(const __half2 (&v)[4], __half2 top, __half2 bottom, float2 inv_dn,
-                                           float2 inv_up) {
-  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer in the low bits
+// v and s have 11 bits each, so v / s is a tie (k + 1/2) or at least 2^-12 from one.  v * inv, off by
+// less than 2^-18, is therefore first rounded to a multiple of 2^-13 (by adding 1.5 * 2^10), which makes a tie
+// exact and moves nothing else across one, then to an integer (by adding 1.5 * 2^23), ties to even:
+// two float32 operations where an IEEE division and its rounding take some fifteen.  Values past the clamp are
+// cut first, to 7.25 s and -8.25 s, which round to 7 and -8.
+__device__ __forceinline__ uint32_t codes8(const __half2 (&v)[4], __half2 top, __half2 bottom, float inv) {
+  constexpr float kFine = 1536.0f, kWhole = 12582912.0f;
   uint32_t w = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 f = __half22float2(__hmax2(__hmin2(v[j], top), bottom));
-    const float2 m = make_float2(kMagic, kMagic);
-    const float2 a = ffma2(f, inv_dn, m), b = ffma2(f, inv_up, m);
-    const float2 sum = fadd2(a, fadd2(b, make_float2(-2.0f * kMagic, -2.0f * kMagic)));
-    const float2 q = ffma2(sum, make_float2(0.5f, 0.5f), m);
+    const float2 a = ffma2(f, make_float2(inv, inv), make_float2(kFine, kFine));
+    const float2 q = fadd2(a, make_float2(kWhole - kFine, kWhole - kFine));
     const uint32_t lo = __float_as_uint(q.x) & 15u, hi = __float_as_uint(q.y) & 15u;
     w |= (lo | hi << 4) << (8 * j);
   }
@@ -247,8 +244,9 @@ __device__ __forceinline__ KvVec kv_vector(long long vec, int H) {
   return v;
 }
 
-// One head vector per 8 lanes: 32 bytes in, 8 bytes of codes out per lane, two vectors per turn, read
-// before their slots are known so that the loads overlap.  Bound by HBM (256 bytes read, 66 written per vector).
+// One head vector per 8 lanes, each with the 8 values at 8 sub and at 64 + 8 sub (whole sectors per load and
+// store), two vectors per turn, read before their slots are known so that the loads overlap.  Bound by HBM
+// (256 bytes read, 66 written per vector).
 __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const __half* __restrict__ K, long long ldk,
                                                                const __half* __restrict__ V, long long ldv, int T,
                                                                const int32_t* __restrict__ slots, float alpha_k,
@@ -274,10 +272,9 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const __half* __r
       if (vec0 + u * step < total) {
         v[u] = kv_vector(vec0 + u * step, c.H);
         const uint4* src =
-            reinterpret_cast<const uint4*>((v[u].which ? V + v[u].t * ldv : K + v[u].t * ldk) + v[u].h * kHeadDim) +
-            2 * sub;
+            reinterpret_cast<const uint4*>((v[u].which ? V + v[u].t * ldv : K + v[u].t * ldk) + v[u].h * kHeadDim) + sub;
         raw[u][0] = src[0];
-        raw[u][1] = src[1];
+        raw[u][1] = src[8];
         slot[u] = slots[v[u].t];
       }
     }
@@ -295,14 +292,13 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const __half* __r
       const float s = __half2float(sh);
       const float inv = s > 0.f ? __fdividef(1.0f, s) : 0.f;  // s = 0: codes 0
       const __half2 top = __float2half2_rn(7.25f * s), bottom = __float2half2_rn(-8.25f * s);
-      const float dn = inv * (1.0f - 0x1p-21f), up = inv * (1.0f + 0x1p-21f);
-      const uint32_t w0 = codes8(reinterpret_cast<const __half2(&)[4]>(h2[0]), top, bottom, make_float2(dn, dn),
-                                 make_float2(up, up));
-      const uint32_t w1 = codes8(reinterpret_cast<const __half2(&)[4]>(h2[4]), top, bottom, make_float2(dn, dn),
-                                 make_float2(up, up));
+      const uint32_t w0 = codes8(reinterpret_cast<const __half2(&)[4]>(h2[0]), top, bottom, inv);
+      const uint32_t w1 = codes8(reinterpret_cast<const __half2(&)[4]>(h2[4]), top, bottom, inv);
       uint8_t* page = c.block(slot[u] >> c.page_shift, v[u].h);
       const int off = slot[u] & ((1 << c.page_shift) - 1);
-      *reinterpret_cast<uint2*>(page + c.codes(v[u].which) + off * kKvRowBytes + 8 * sub) = make_uint2(w0, w1);
+      uint32_t* row = reinterpret_cast<uint32_t*>(page + c.codes(v[u].which) + off * kKvRowBytes) + sub;
+      row[0] = w0;
+      row[8] = w1;
       if (sub == 0) *reinterpret_cast<__half*>(page + c.scales(v[u].which) + 2 * off) = sh;
     }
   }
@@ -335,9 +331,8 @@ __global__ void __launch_bounds__(kRowThreads) kv_store_kernel(const uint8_t* __
   }
 }
 
-// One head vector per 8 lanes: 8 bytes of codes in, 32 bytes out per lane, four vectors per turn so that
-// their slots and codes are loaded together.  The product of a 4-bit code and an 11-bit scale is exact
-// in float32, so there is one rounding, to fp16.
+// One head vector per 8 lanes, each with the 8 values at 8 sub and at 64 + 8 sub (whole sectors per load and
+// store), four vectors per turn so that their slots and codes are loaded together.  One rounding: the fp16 product.
 __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const int32_t* __restrict__ slots, int T,
                                                               __half* __restrict__ K, __half* __restrict__ V,
                                                               KvView c) {
@@ -353,7 +348,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const int32_t* __r
     KvVec v[kVecs];
     int slot[kVecs];
     uint2 w[kVecs];
-    float s[kVecs];
+    __half s[kVecs];
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       slot[u] = -1;
@@ -365,12 +360,13 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const int32_t* __r
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       w[u] = make_uint2(0, 0);
-      s[u] = 0.f;
+      s[u] = __ushort_as_half(0);
       if (slot[u] >= 0 && slot[u] < limit) {
         const uint8_t* page = c.block(slot[u] >> c.page_shift, v[u].h);
         const int off = slot[u] & ((1 << c.page_shift) - 1);
-        w[u] = *reinterpret_cast<const uint2*>(page + c.codes(v[u].which) + off * kKvRowBytes + 8 * sub);
-        s[u] = __half2float(*reinterpret_cast<const __half*>(page + c.scales(v[u].which) + 2 * off));
+        const uint32_t* row = reinterpret_cast<const uint32_t*>(page + c.codes(v[u].which) + off * kKvRowBytes) + sub;
+        w[u] = make_uint2(row[0], row[8]);
+        s[u] = *reinterpret_cast<const __half*>(page + c.scales(v[u].which) + 2 * off);
       }
     }
 #pragma unroll
@@ -378,15 +374,20 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const int32_t* __r
       if (vec + u * step >= total) break;
       uint4 out[2];
       __half2* o2 = reinterpret_cast<__half2*>(out);
+      const __half2 s2 = __half2half2(s[u]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int b = int(((j < 4 ? w[u].x : w[u].y) >> (8 * (j & 3))) & 255u);
-        const int lo = (b << 28) >> 28, hi = (b << 24) >> 28;
-        o2[j] = __floats2half2_rn(float(lo) * s[u], float(hi) * s[u]);
+        // byte j's two nibbles q as the fp16 numbers 1032 + q, less 1032, times the scale
+        const uint32_t word = j < 4 ? w[u].x : w[u].y;
+        const uint32_t pair = __byte_perm(word, word >> 4, 0x0400u + 0x0101u * (j & 3));
+        uint32_t h;
+        asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(h) : "r"(pair), "r"(0x000F000Fu), "r"(0x64086408u));
+        const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x6408)));
+        o2[j] = __hmul2(q, s2);
       }
-      uint4* dst = reinterpret_cast<uint4*>((v[u].which ? V : K) + (v[u].t * c.H + v[u].h) * kHeadDim) + 2 * sub;
+      uint4* dst = reinterpret_cast<uint4*>((v[u].which ? V : K) + (v[u].t * c.H + v[u].h) * kHeadDim) + sub;
       dst[0] = out[0];
-      dst[1] = out[1];
+      dst[8] = out[1];
     }
   }
 }
