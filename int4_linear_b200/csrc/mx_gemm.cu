@@ -211,6 +211,23 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// wait_phase by a whole warp, which leaves it together.
+template <bool CLUSTER>
+__device__ __forceinline__ bool warp_wait_phase(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_phase<CLUSTER>(bar, parity));
+}
+
+// True on one lane of the warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // A stage of the ring and its phase.
 struct MxStage {
   int s = 0;
@@ -272,7 +289,10 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
   uint64_t* done = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   int* join = reinterpret_cast<int*>(done + 1) + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The issuing warps run their loops as whole warps, one elected lane sending the instructions: addresses and
+  // descriptors then stay in uniform registers, which the instructions take (from divergent code every operand
+  // is moved there first).
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_rank() : 0;
   const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
 
@@ -304,37 +324,39 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
   else
     __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_launch_dependents();
   pdl_wait();
 
   MxWalk walk(p, unit, units);
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    const bool leader = elect_one();
+    if (leader) {
       prefetch_tensormap(&tmW);
       prefetch_tensormap(&tmX);
       prefetch_tensormap(&tmSw);
       prefetch_tensormap(&tmSx);
-      const uint64_t pol_w = BN <= 64 ? policy_evict_first() : policy_evict_normal();  // few tokens: read once
-      const uint64_t pol_x = policy_evict_last();  // the tokens are read by every CTA
-      const uint32_t bar0 = PAIR ? cluster_addr(full, 0) : smem_u32(full);
-      MxStage st;
-      int sent = 0;
-      bool ok = true;
-      while (ok && walk.next()) {
-        const int nt = walk.tile / p.mt * (PAIR ? 2 : 1) + int(rank), mt = walk.tile % p.mt;  // 128 rows, BN tokens
-        const int yw = nt * kTileN, yx = mt * BN + int(rank) * C::BROWS, ysx = mt * BN / kMxTileRows;
-        for (int k = walk.k0; k < walk.k1; ++k, st.next(S)) {
-          if (!wait_phase<false>(&empty[st.s], st.phase ^ 1)) {
-            record_error(p.err, kErrTimeoutProducer);
-            ok = false;
-            break;
-          }
-          const uint32_t bar = bar0 + 8u * st.s;
+    }
+    const uint64_t pol_w = BN <= 64 ? policy_evict_first() : policy_evict_normal();  // few tokens: read once
+    const uint64_t pol_x = policy_evict_last();  // the tokens are read by every CTA
+    const uint32_t bar0 = PAIR ? cluster_addr(full, 0) : smem_u32(full);
+    MxStage st;
+    int sent = 0;
+    bool ok = true;
+    while (ok && walk.next()) {
+      const int nt = walk.tile / p.mt * (PAIR ? 2 : 1) + int(rank), mt = walk.tile % p.mt;  // 128 rows, BN tokens
+      const int yw = nt * kTileN, yx = mt * BN + int(rank) * C::BROWS, ysx = mt * BN / kMxTileRows;
+      for (int k = walk.k0; k < walk.k1; ++k, st.next(S)) {
+        if (!warp_wait_phase<false>(&empty[st.s], st.phase ^ 1)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = bar0 + 8u * st.s;
+        uint8_t* ab = smem + st.s * (C::A_BYTES + C::B_BYTES);
+        uint8_t* sf = smem + C::OFF_SA + st.s * (C::SA_BYTES + C::SX_BYTES);
+        if (leader) {
           if (rank == 0) mbar_arrive_expect_tx(&full[st.s], C::STAGE * (PAIR ? 2 : 1));
-          uint8_t* ab = smem + st.s * (C::A_BYTES + C::B_BYTES);
-          uint8_t* sf = smem + C::OFF_SA + st.s * (C::SA_BYTES + C::SX_BYTES);
           load_tile<PAIR>(ab, &tmW, bar, k * kRowB, yw, pol_w);
           load_tile<PAIR>(ab + C::A_BYTES, &tmX, bar, k * kRowB, yx, pol_x);
           // scale tiles, 64 words of 8 bytes each; what lies past the last one reads as 0
@@ -342,22 +364,21 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
 #pragma unroll
           for (int j = 0; j < C::NBT; ++j)
             load_tile<PAIR>(sf + C::SA_BYTES * (1 + j), &tmSx, bar, k * C::SB * 64, ysx + j, pol_x);
-          sent = min(sent + 1, S);
         }
+        sent = min(sent + 1, S);
       }
-      // every copy has landed before the CTA may leave: the last `sent` stages, oldest first
-      if (rank == 0)
-        for (int i = 0; i < sent; ++i) {
-          const int back = sent - i, s = st.s - back < 0 ? st.s - back + S : st.s - back;
-          if (!mbar_wait(&full[s], st.s - back < 0 ? st.phase ^ 1 : st.phase)) {
-            record_error(p.err, kErrTimeoutDrain);
-            break;
-          }
-        }
     }
+    // every copy has landed before the CTA may leave: the last `sent` stages, oldest first
+    if (rank == 0)
+      for (int i = 0; ok && i < sent; ++i) {
+        const int back = sent - i, s = st.s - back < 0 ? st.s - back + S : st.s - back;
+        ok = warp_wait_phase<false>(&full[s], st.s - back < 0 ? st.phase ^ 1 : st.phase);
+      }
+    if (!ok && leader) record_error(p.err, kErrTimeoutProducer);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool leader = elect_one();
       auto commit = [&](uint64_t* bar) {
         if (PAIR)
           mma_commit_pair(bar, 3);
@@ -373,16 +394,15 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
       bool ok = true;
       while (ok && walk.next()) {
         const int buf = seg % C::AB;
-        if (!wait_phase<PAIR>(&acc_empty[buf], ((seg / C::AB) & 1) ^ 1)) {
-          record_error(p.err, kErrTimeoutMma);
+        if (!warp_wait_phase<PAIR>(&acc_empty[buf], ((seg / C::AB) & 1) ^ 1)) {
+          ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(buf * C::ACC);
         for (int k = walk.k0; k < walk.k1; ++k, st.next(S)) {
           // the operands, then the scales, which came after them
-          if (!wait_phase<PAIR>(&full[st.s], st.phase) || !wait_phase<false>(&sf_full[st.s], st.phase)) {
-            record_error(p.err, kErrTimeoutMma);
+          if (!warp_wait_phase<false>(&full[st.s], st.phase) || !warp_wait_phase<false>(&sf_full[st.s], st.phase)) {
             ok = false;
             break;
           }
@@ -390,25 +410,29 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
           const uint64_t ad = a_desc + uint32_t(st.s) * kStep16, bd = b_desc + uint32_t(st.s) * kStep16;
           const uint32_t ta = tmem + uint32_t(C::SF0 + st.s * (C::SFA + C::SFX)), tx = ta + uint32_t(C::SFA);
           const bool half = tail && k + 1 == p.ks;
+          if (leader) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (q >= 2 && half) break;
-            const int b = FMT == FQ_NVFP4 ? q : q / 2;
-            mma_mx<FMT, PAIR>(d, ad + 2 * q, bd + 2 * q, FMT == FQ_MXFP4 && (q & 1) ? i2 : i0, ta + 4 * b,
-                              tx + 4 * b * C::NBT, q > 0 ? 1u : uint32_t(k > walk.k0));
+            for (int q = 0; q < 4; ++q) {
+              if (q >= 2 && half) break;
+              const int b = FMT == FQ_NVFP4 ? q : q / 2;
+              mma_mx<FMT, PAIR>(d, ad + 2 * q, bd + 2 * q, FMT == FQ_MXFP4 && (q & 1) ? i2 : i0, ta + 4 * b,
+                                tx + 4 * b * C::NBT, q > 0 ? 1u : uint32_t(k > walk.k0));
+            }
+            commit(&empty[st.s]);
           }
-          commit(&empty[st.s]);
         }
-        commit(&acc_full[buf]);
+        if (leader) commit(&acc_full[buf]);
         ++seg;
       }
       // nothing issued may still run when tensor memory is freed
-      commit(done);
-      if (!mbar_wait(done, 0)) record_error(p.err, kErrTimeoutDrain);
+      if (leader) commit(done);
+      ok = warp_wait_phase<false>(done, 0) && ok;
+      if (!ok && leader) record_error(p.err, kErrTimeoutMma);
     }
   } else if (warp == 2 || warp == 3) {
     // ------------------------------------------------------------ scales to tensor memory, every other tile each
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool leader = elect_one();
       const uint64_t sf_desc = sdesc_scales(smem_u32(smem + C::OFF_SA));
       constexpr uint32_t kStep16 = (C::SA_BYTES + C::SX_BYTES) >> 4, kTile16 = kMxTileBytes >> 4;
       const bool tail = p.K % kStageK != 0;
@@ -417,8 +441,7 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
       bool ok = true;
       while (ok && walk.next()) {
         for (int k = walk.k0; k < walk.k1; ++k, st.next(S)) {
-          if (!wait_phase<PAIR>(&full[st.s], st.phase)) {
-            record_error(p.err, kErrTimeoutUnpack);
+          if (!warp_wait_phase<false>(&full[st.s], st.phase)) {
             ok = false;
             break;
           }
@@ -426,31 +449,31 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
           const uint64_t sd = sf_desc + uint32_t(st.s) * kStep16;
           const uint32_t ta = tmem + uint32_t(C::SF0 + st.s * (C::SFA + C::SFX)), tx = ta + uint32_t(C::SFA);
           const bool half = tail && k + 1 == p.ks;
+          if (leader) {
 #pragma unroll
-          for (int b0 = 0; b0 < C::SB; b0 += 2) {
-            if (b0 >= C::SB / 2 && half && C::SB > 2) break;
-            if (half && C::SB == 2 && warp == 3) break;
-            const int b = b0 + (warp & 1);  // warps 2 and 3
-            copy_scales<PAIR>(ta + 4 * b, sd + b * kTile16);
+            for (int b0 = 0; b0 < C::SB; b0 += 2) {
+              if (b0 >= C::SB / 2 && half && C::SB > 2) break;
+              if (half && C::SB == 2 && warp == 3) break;
+              const int b = b0 + (warp & 1);
+              copy_scales<PAIR>(ta + 4 * b, sd + b * kTile16);
 #pragma unroll
-            for (int j = 0; j < C::NBT; ++j)
-              copy_scales<PAIR>(tx + 4 * (b * C::NBT + j), sd + (C::SB * (1 + j) + b) * kTile16);
+              for (int j = 0; j < C::NBT; ++j)
+                copy_scales<PAIR>(tx + 4 * (b * C::NBT + j), sd + (C::SB * (1 + j) + b) * kTile16);
+            }
+            if (PAIR)
+              mma_commit_pair(&sf_full[st.s], 1);
+            else
+              mma_commit(&sf_full[st.s]);
           }
-          if (PAIR)
-            mma_commit_pair(&sf_full[st.s], 1);
-          else
-            mma_commit(&sf_full[st.s]);
           sent = min(sent + 1, S);
         }
       }
       // every copy sent has been made before tensor memory is freed
-      for (int i = 0; i < sent; ++i) {
+      for (int i = 0; ok && i < sent; ++i) {
         const int back = sent - i, s = st.s - back < 0 ? st.s - back + S : st.s - back;
-        if (!mbar_wait(&sf_full[s], st.s - back < 0 ? st.phase ^ 1 : st.phase)) {
-          record_error(p.err, kErrTimeoutDrain);
-          break;
-        }
+        ok = warp_wait_phase<false>(&sf_full[s], st.s - back < 0 ? st.phase ^ 1 : st.phase);
       }
+      if (!ok && leader) record_error(p.err, kErrTimeoutUnpack);
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ finished tiles
