@@ -114,6 +114,10 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// First counter word, in a workspace's counter block, of the kernels that count a join's arrivals: the
+// words before it hold the decode GEMM's grid barrier, whose generation number is not zero.
+constexpr int kJoinCounters = 64;
+
 constexpr int kGroup = 128;
 constexpr int kMaxK = 65536;
 constexpr int kMaxQuantK = 32768;

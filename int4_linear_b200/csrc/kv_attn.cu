@@ -872,7 +872,7 @@ fq_status fq_kv_attn(const uint16_t* Q, long long ldq, int R, int Hq, const int3
   p.scale_log2 = scale * 1.4426950408889634f;
   p.window = window;
   p.Y = reinterpret_cast<__half*>(Y);
-  p.count = static_cast<unsigned*>(workspace);
+  p.count = static_cast<unsigned*>(workspace) + fq::kJoinCounters;
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + fq::sync_block_bytes());
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool p16 = cache->page_size == 16;

@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
   const int page = 1 << p.page_shift;
   pdl_launch_dependents();
   pdl_wait();
-  const int used = *p.used;
+  const int used = max(*p.used, 0);
   const int avail = p.num_free - used;
   int tok0 = 0, ask0 = 0, taken = 0;
   for (int base = 0; base < p.R; base += kPlanThreads) {

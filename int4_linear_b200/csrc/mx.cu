@@ -37,15 +37,12 @@ __device__ __forceinline__ void codes16(const __half2* h2, float inv, uint32_t (
 }
 
 // Codes of 16 values over d.
-__device__ __noinline__ void codes16_divided(const __half2* h2, float d, uint32_t (&q)[2]) {
+__device__ __forceinline__ void codes16_divided(const __half2* h2, float d, uint32_t (&q)[2]) {
   q[0] = q[1] = 0;
+#pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float2 f = __half22float2(h2[j]);
-    const uint32_t b = e2m1x2(__fdiv_rn(f.x, d), __fdiv_rn(f.y, d)) << (8 * (j & 3));
-    if (j < 4)
-      q[0] |= b;
-    else
-      q[1] |= b;
+    q[j >> 2] |= e2m1x2(__fdiv_rn(f.x, d), __fdiv_rn(f.y, d)) << (8 * (j & 3));
   }
 }
 

@@ -760,7 +760,7 @@ fq_status fq_mx_gemm(const uint8_t* Xq, const uint8_t* Sx, const float* g_x, con
   p.tiles = q.tiles;
   p.ks = q.ks;
   p.split = q.split;
-  p.count = static_cast<unsigned*>(workspace);
+  p.count = static_cast<unsigned*>(workspace) + fq::kJoinCounters;
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + fq::sync_block_bytes());
   p.err = err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

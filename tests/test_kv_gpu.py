@@ -448,3 +448,29 @@ def test_decode_steps_together():
         check_attn(y, q, o_len, o_table, o_pool, 128 ** -0.5)
     assert np.array_equal(cache.pool.cpu().numpy(), o_pool)
     assert np.array_equal(table.cpu().numpy(), o_table) and np.array_equal(lens.cpu().numpy(), o_len)
+
+
+def test_workspace_shared_with_the_fused_linear():
+    """The decode linear's one-launch form leaves a generation number in the counter block; attention
+    and the block-scaled product on the same workspace are not disturbed."""
+    from oracle import mx_oracle as MO
+    g = rng(21)
+    m, n, k = 4, 512, 1024
+    qp = fq.qparams(fq.STATIC)
+    scale = torch.full((k,), 0.3, device="cuda")
+    w = dev(g.standard_normal((n, k)).astype(np.float16))
+    wq, sw = fq.fq_quant_weight(w, fq.qparams(fq.ROW), qsm_scale=scale)
+    x = dev(g.standard_normal((m, k)).astype(np.float16))
+    need = max(fq.fq_linear_workspace_size(m, n, k, fq.STATIC), fq.fq_kv_attn_workspace_size(2, 8, 1),
+               fq.fq_mx_linear_workspace_size(m, n, 8192, MO.MXFP4))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    case = attn_case(22, [9000, 4000], 8, 1, 64)
+    args = [dev(a) for a in case[:3]] + [fq.KVCache(dev(case[3]))]
+    xm = dev(g.standard_normal((m, 8192)).astype(np.float16))
+    mq, ms = fq.fq_mx_quant(dev(g.standard_normal((n, 8192)).astype(np.float16)), MO.MXFP4)
+    y0, z0 = fq.fq_kv_attn(*args), fq.fq_mx_linear(xm, MO.MXFP4, mq, ms)
+    for _ in range(3):
+        fq.fq_linear(x, qp, wq, sw, static_scale=scale, workspace=ws, fused=True)
+        assert torch.equal(fq.fq_kv_attn(*args, workspace=ws), y0)
+        assert torch.equal(fq.fq_mx_linear(xm, MO.MXFP4, mq, ms, workspace=ws), z0)
+    check_attn(y0, *case, 128 ** -0.5)
