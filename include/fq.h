@@ -369,10 +369,11 @@ fq_status fq_kv_read(const fq_kv_cache* cache, const int32_t* slots, int T, uint
  *        has no effect.
  * Y      fp16 [R, Hq * 128] (16-byte aligned).
  * Hq a multiple of H, at most 1024; R in [1, 16384].
- * Arithmetic: products of fp16 queries and integer codes summed in float32, softmax
- * statistics and sums in float32; the weights p_i * (v scale) enter the second
- * product rounded to fp16 after scaling (2^-11 relative).  The summation order
- * is the kernel's, the same on every run for the same sizes and lengths.
+ * Arithmetic: each query head is taken in 16-bit fixed point (half a step of max|q| / 32639
+ * off), its products with the codes summed exactly; scores, softmax statistics and sums are
+ * float32; the weights p_i * (v scale) enter the second product as two fp16 numbers (2^-22
+ * relative).  The summation order is the kernel's, the same on every run for the
+ * same sizes and lengths.
  * workspace / ws_bytes: fq_kv_attn_workspace_size(R, Hq, H) bytes, 256-byte
  *   aligned, whose first FQ_WORKSPACE_SYNC_BYTES follow the rule of
  *   fq_w4a4_gemm's workspace (zero before the first call, left zero).

@@ -6,9 +6,10 @@
 // The floor is one read of the cache: 132 bytes per token and key-value head
 // against 4 * 128 operations per query head, so the work is a stream of pages
 // with the arithmetic hidden under it.  At the measured 6.55 TB/s an SM has
-// about 5.7 cycles per token and head, i.e. some 23 warp instructions; turning
-// 256 nibbles into operands alone takes 10, so the layout below moves no operand
-// through shuffles or a second pass of shared memory.
+// about 5.7 cycles per token and head, i.e. some 23 warp instructions; this kernel
+// executes 20, and with the four warps that a scheduler's registers hold issues in 54 % of the
+// cycles, waiting for products and their results: 64 requests of 8 heads and 14200
+// tokens on average (eight queries a head) take 217 us, 4.4 TB/s.
 //
 // Division.  The turns (32 tokens of one request and key-value head) of all
 // requests form one sequence, request-major; every CTA takes an equal contiguous
@@ -23,23 +24,29 @@
 // their fixed order (the sums come out the same whichever CTA that is).  With one
 // join of the warps per CTA instead of one per segment, ragged batches lost a third of their time.
 //
-// Products: mma.m16n8k16 (fp16, float32 sums).  The tensor-memory path needs
-// 128 rows of queries, and a request has G = Hq / H <= 16 of them per head, so its
-// staging of operands would cost more than the product.
-//  - scores: A = 16 tokens x 128 dims of K codes, B = 8 queries.  A lane reads 16
-//    consecutive bytes of a token's row; the order of the dims inside the product is
-//    free, so the queries are arranged once per segment to match the nibbles.  A nibble
-//    becomes the fp16 number 64 + (code + 8) by one logic operation; the constant
-//    72 sum(q) is taken off through the accumulator's initial value (an error of
-//    72 sum|q| 2^-24, 2^-15 of a logit at most for queries and keys of unit size).
-//  - sum: A = 128 dims x 16 tokens of V codes (exact), B = the weights, taken
-//    from the scores' layout by movmatrix.  A lane reads 8 bytes of each of its 4
-//    tokens and pairs two tokens' nibbles by byte permutation.
-// Weights: w = exp2(s - m) * (v scale / largest v scale so far) * 2^8 is
-// rounded to fp16 (2^-11 relative, independent errors that the sum averages; weights below
-// 2^-22 of the largest lose bits, 2^-33 of it at most each).  m is a
-// reference that moves only when a score passes it by 2^7 (checked with one vote
-// per 16 tokens), so the sums are rarely rescaled.
+// Products.  mma.sync: the tensor-memory path needs 128 rows of queries, and a request has
+// G = Hq / H <= 16 of them per head, so its staging of operands would cost more than
+// the product.
+//  - scores: m16n8k32 in integers, A = 16 tokens x 128 dims of K codes (nibbles shifted to the
+//    top of a byte: 16 code, one logic operation per four), B = 8 queries in 16-bit fixed point of
+//    their head's largest value, as a high and a low signed byte.  The sums are exact, so the score is
+//    as good as the query: half a step of max|q| / 32639.  A lane reads 16 consecutive bytes of a
+//    token's row; the order of the dims inside the product is free, so the queries are arranged once
+//    per segment to match the nibbles.  An fp16 product with the constant of 64 + (code + 8) taken off afterwards
+//    was 6 % slower and left errors of 2^-15 of a logit.
+//  - sum: m16n8k16, A = 128 dims x 16 tokens of V codes (exact; a nibble u = code + 8 is the mantissa
+//    of a subnormal fp16, so an AND makes the operand, and one product with the constant -8
+//    starts the sums), B = the weights, taken from the scores' layout by movmatrix.  A lane reads 8 bytes of
+//    each of its 4 tokens and pairs two tokens' nibbles by byte permutation.  Sixteen tokens are
+//    added up in the tensor core, whose adds cut off; the running sums are rounded float32 adds.
+// Weights: w = exp2(s - m) * (v scale / largest v scale so far) * 2^8 enters as two fp16 numbers, its
+// rounding and what that left (2^-22 relative, or 2^-33 of the largest where the second is
+// subnormal).  The rounding alone is 16 % faster on long caches (188 us for the 217 above), but leaves 1.5
+// times the error of the output's own rounding.  The second product adds to the running sums directly:
+// it is 2^-11 of them, and cutting a sum off at 2^-23 once per 16 tokens stays below the output's rounding
+// for parts of up to 65536 tokens per warp.
+// m is a reference that moves only when a score passes it by 2^7 (checked with one vote
+// per 32 tokens), so the sums are rarely rescaled.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -139,6 +146,14 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The first product of a sum.
+__device__ __forceinline__ void mma_s8_first(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+}
+
 __device__ __forceinline__ void add4(float (&a)[4], const float (&b)[4]) {
   const float2 x = fadd2(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
   const float2 y = fadd2(make_float2(a[2], a[3]), make_float2(b[2], b[3]));
@@ -159,16 +174,10 @@ __device__ __forceinline__ uint32_t bytes4(const uint32_t (&v)[4], uint32_t sel)
   return __byte_perm(__byte_perm(v[0], v[1], sel), __byte_perm(v[2], v[3], sel), 0x5410);
 }
 
-// (a & b) ^ c in one logic operation.
-__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-// Nibbles of each half word (two's complement codes q) at bits 0-3 and 4-7 -> the fp16 numbers
-// (q + 8) 2^-24 and (q + 8) 2^-20 (subnormal: the nibble is the mantissa).
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return and_xor(w, 0x000F000Fu, 0x00080008u); }
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return and_xor(w, 0x00F000F0u, 0x00800080u); }
+// Nibbles u of each half word at bits 0-3 and 4-7 -> the fp16 numbers u 2^-24 and u 2^-20 (subnormal: the
+// nibble is the mantissa).  u = q + 8: the codes' top bits are flipped beforehand.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return w & 0x000F000Fu; }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return w & 0x00F000F0u; }
 
 // The token of score row i (0..15): rows 2t, 2t + 1 of one lane's weights.  Bit 0
 // alternates within a row pair (score reads of two rows hit different banks)
@@ -570,18 +579,19 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
         const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
         int ah[NT][4], al[NT][4];
 #pragma unroll
-        for (int nn = 0; nn < NT; ++nn)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ah[nn][k] = al[nn][k] = 0;
-#pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t e0, d0, e1, d1;  // 16 q of the even and odd dims of rows g and g + 8
           unpack8_hi(kw0[j], e0, d0);
           unpack8_hi(kw1[j], e1, d1);
 #pragma unroll
           for (int nn = 0; nn < NT; ++nn) {
-            mma_s8(ah[nn], e0, e1, d0, d1, qf[nn][0][2 * j], qf[nn][0][2 * j + 1]);
-            mma_s8(al[nn], e0, e1, d0, d1, qf[nn][1][2 * j], qf[nn][1][2 * j + 1]);
+            if (j == 0) {
+              mma_s8_first(ah[nn], e0, e1, d0, d1, qf[nn][0][0], qf[nn][0][1]);
+              mma_s8_first(al[nn], e0, e1, d0, d1, qf[nn][1][0], qf[nn][1][1]);
+            } else {
+              mma_s8(ah[nn], e0, e1, d0, d1, qf[nn][0][2 * j], qf[nn][0][2 * j + 1]);
+              mma_s8(al[nn], e0, e1, d0, d1, qf[nn][1][2 * j], qf[nn][1][2 * j + 1]);
+            }
           }
         }
 #pragma unroll
@@ -660,7 +670,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t w0[NT], w1[NT];
+        uint32_t w[2][NT][2];  // weights and what their rounding left, as operands
         float c8[NT][4];  // -8 sum(w): rows g in the units of codes_lo, rows g + 8 of codes_hi
         const float v0 = vs[h][0] * vinv, v1 = vs[h][1] * vinv;
 #pragma unroll
@@ -669,12 +679,19 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
           const float p2 = exp2_approx(x[h][nn][2]), p3 = exp2_approx(x[h][nn][3]);
           l[nn][0] += p0 + p2;
           l[nn][1] += p1 + p3;
-          const __half2 a = __floats2half2_rn(p0 * v0, p1 * v0), b = __floats2half2_rn(p2 * v1, p3 * v1);
-          w0[nn] = transpose8x8(*reinterpret_cast<const uint32_t*>(&a));
-          w1[nn] = transpose8x8(*reinterpret_cast<const uint32_t*>(&b));
+          const float2 wa = make_float2(p0 * v0, p1 * v0), wb = make_float2(p2 * v1, p3 * v1);
+          const __half2 a = __float22half2_rn(wa), b = __float22half2_rn(wb);
+          // what the rounding left, as a second weight
+          const float2 ra = __half22float2(a), rb = __half22float2(b);
+          const __half2 al = __floats2half2_rn(wa.x - ra.x, wa.y - ra.y), bl = __floats2half2_rn(wb.x - rb.x, wb.y - rb.y);
+          w[0][nn][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&a));
+          w[0][nn][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&b));
+          w[1][nn][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&al));
+          w[1][nn][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&bl));
           const float zero[4] = {0.f, 0.f, 0.f, 0.f};
           // -2^-21 = -8 2^-24 and -2^-17 = -8 2^-20 as fp16
-          mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w0[nn], w1[nn], zero);
+          mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w[0][nn][0], w[0][nn][1], zero);
+          mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w[1][nn][0], w[1][nn][1], c8[nn]);
         }
         // values: lane (g, t4) holds dims [16 g, 16 g + 16) of its four tokens
         const uint2 x0 = *reinterpret_cast<const uint2*>(sp + va_off + h * 1024);
@@ -684,8 +701,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
 #pragma unroll
         for (int j = 0; j < 4; ++j) {  // four dims: half word j of the 16 dims
           const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-          const uint32_t y0 = __byte_perm(j < 2 ? x0.x : x0.y, j < 2 ? x1.x : x1.y, sel);
-          const uint32_t y1 = __byte_perm(j < 2 ? x2.x : x2.y, j < 2 ? x3.x : x3.y, sel);
+          const uint32_t y0 = __byte_perm(j < 2 ? x0.x : x0.y, j < 2 ? x1.x : x1.y, sel) ^ 0x88888888u;
+          const uint32_t y1 = __byte_perm(j < 2 ? x2.x : x2.y, j < 2 ? x3.x : x3.y, sel) ^ 0x88888888u;
           const uint32_t z0 = y0 >> 8, z1 = y1 >> 8;
           // dims 4 j (rows g, in units of 2^-24), 4 j + 1 (rows g + 8, 2^-20); 4 j + 2, 4 j + 3
           const uint32_t a0 = codes_lo(y0), a1 = codes_hi(y0), a2 = codes_lo(y1), a3 = codes_hi(y1);
@@ -693,9 +710,11 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
 #pragma unroll
           for (int nn = 0; nn < NT; ++nn) {
             float d[4];
-            mma_f16(d, a0, a1, a2, a3, w0[nn], w1[nn], c8[nn]);
+            mma_f16(o[nn][2 * j], a0, a1, a2, a3, w[1][nn][0], w[1][nn][1], o[nn][2 * j]);
+            mma_f16(d, a0, a1, a2, a3, w[0][nn][0], w[0][nn][1], c8[nn]);
             add4(o[nn][2 * j], d);
-            mma_f16(d, b0, b1, b2, b3, w0[nn], w1[nn], c8[nn]);
+            mma_f16(o[nn][2 * j + 1], b0, b1, b2, b3, w[1][nn][0], w[1][nn][1], o[nn][2 * j + 1]);
+            mma_f16(d, b0, b1, b2, b3, w[0][nn][0], w[0][nn][1], c8[nn]);
             add4(o[nn][2 * j + 1], d);
           }
         }
