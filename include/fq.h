@@ -325,7 +325,8 @@ typedef struct {
  * when its table row is too short (it asks for no pages then), when its rows
  * pass max_tokens (nor here), or when it needs pages and the pages asked for up
  * to and including it pass the free list: once that happens, no later request
- * that needs pages gets any either.  The sum of new_tokens must stay below 2^31.
+ * that needs pages gets any either.  The sum of new_tokens must stay below 2^31, and
+ * *pages_used must not be negative.
  * R in [1, 16384].  One launch, no workspace; the outputs must not overlap
  * the inputs except where stated. */
 fq_status fq_kv_plan(const int32_t* len, const int32_t* new_tokens, int R, int page_size, int32_t* block_table,
@@ -338,8 +339,8 @@ fq_status fq_kv_plan(const int32_t* len, const int32_t* new_tokens, int R, int p
  * that slices of one projection's output are taken as they are.  Each head
  * vector is quantized as by fq_quant_kv without a transform: s = fp16((max|v|
  * alpha) / 7), codes clamp(round(v / s), -8, 7), and goes to slots[t] (int32
- * [T]); rows whose slot is no place are skipped.  The slots of one call must
- * differ, else a shared slot may hold a mix of its rows.  One launch. */
+ * [T]); rows whose slot is no place are skipped.  K and V hold finite values.  The slots
+ * of one call must differ, else a shared slot may hold a mix of its rows.  One launch. */
 fq_status fq_kv_write(const uint16_t* K, long long ldk, const uint16_t* V, long long ldv, int T,
                       const int32_t* slots, float alpha_k, float alpha_v, const fq_kv_cache* cache, void* stream);
 
@@ -368,7 +369,8 @@ fq_status fq_kv_read(const fq_kv_cache* cache, const int32_t* slots, int T, uint
  *        its tokens out.  What a page holds behind the last token (NaN scales too)
  *        has no effect.
  * Y      fp16 [R, Hq * 128] (16-byte aligned).
- * Hq a multiple of H, at most 1024; R in [1, 16384].
+ * Hq a multiple of H, at most 1024; R in [1, 16384]; scale in [-65536, 65536].
+ * A query head that holds an infinity or NaN gives NaN, the others keep their values.
  * Arithmetic: each query head is taken in 16-bit fixed point (half a step of max|q| / 32639
  * off), its products with the codes summed exactly; scores, softmax statistics and sums are
  * float32; the weights p_i * (v scale) enter the second product as two fp16 numbers (2^-22

@@ -272,8 +272,10 @@ __device__ __noinline__ void join_parts(const float* all, int c_first, int parts
   }
 }
 
-// NT: tiles of 8 query heads; P16: pages of 16 tokens, so that a turn spans two.
-template <int NT, bool P16>
+// NT: tiles of 8 query heads; TWICE: at most 4 query heads, which also take columns 4-7 of the tile: there
+// the weights are what the rounding of those in columns 0-3 left, so one product does both; P16: pages of 16
+// tokens, so that a turn spans two.
+template <int NT, bool TWICE, bool P16>
 __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(const AttnParams p) {
   constexpr int HB = 8 * NT;
   // the warps' turns, then each warp's continued segment, [32 NT values][32 lanes]
@@ -429,15 +431,16 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   // Query heads of a segment: heads [q0, q0 + heads)
   auto first_head = [&](const Seg& q) { return (q.hc / p.chunks) * p.G + (q.hc % p.chunks) * HB; };
   auto head_count = [&](const Seg& q) { return min(HB, p.G - (q.hc % p.chunks) * HB); };
-  uint4 raw[NT][4];  // lane (g, t4): head g, dims [32 t4, 32 t4 + 32)
+  const int col = TWICE ? g & 3 : g;
+  uint4 raw[NT][4];  // lane (g, t4): the head of column g, dims [32 t4, 32 t4 + 32)
   auto load_queries = [&](const Seg& q) {
-    const __half* src = p.Q + static_cast<long long>(q.r) * p.ldq + (first_head(q) + g) * kHeadDim + 32 * t4;
+    const __half* src = p.Q + static_cast<long long>(q.r) * p.ldq + (first_head(q) + col) * kHeadDim + 32 * t4;
     const int heads = head_count(q);
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        raw[nn][j] = nn * 8 + g < heads ? *reinterpret_cast<const uint4*>(src + nn * 8 * kHeadDim + 8 * j)
+        raw[nn][j] = nn * 8 + col < heads ? *reinterpret_cast<const uint4*>(src + nn * 8 * kHeadDim + 8 * j)
                                         : make_uint4(0, 0, 0, 0);
   };
 
@@ -459,6 +462,12 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
           o[nn][i][k] *= f * 0x1p24f;
           o[nn][i][k + 2] *= f * 0x1p20f;
         }
+    if (TWICE) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[0][i][k] += __shfl_xor_sync(0xffffffffu, o[0][i][k], 2);
+    }
   };
   // piece 0 of a warp lies behind the turns, piece 1 takes the warp's own turns' bytes
   auto piece = [&](int w, int which) {
@@ -514,16 +523,17 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
     float unit[NT][2];  // of heads 2 t4, 2 t4 + 1, times the score's scale and 1/16 (a nibble is taken 16-fold)
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn) {
-      __half2 m2 = __float2half2_rn(0.f);
+      __half2 m2 = __float2half2_rn(0.f);  // NaN stays
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const __half2* h2 = reinterpret_cast<const __half2*>(&raw[nn][j]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) m2 = __hmax2(m2, __habs2(h2[k]));
+        for (int k = 0; k < 4; ++k) m2 = __hmax2_nan(m2, __habs2(h2[k]));
       }
-      float mq = __half2float(__hmax(__low2half(m2), __high2half(m2)));
-      mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 1));
-      mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 2));
+      uint32_t mb = __float_as_uint(__half2float(__hmax_nan(__low2half(m2), __high2half(m2))));
+      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));  // of numbers without sign, NaN the largest
+      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+      const float mq = __uint_as_float(mb);
       const float inv = mq > 0.f ? 32639.0f / mq : 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -541,7 +551,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
         qf[nn][1][2 * j] = bytes4(ev, 0x4040u) ^ 0x80808080u;
         qf[nn][1][2 * j + 1] = bytes4(od, 0x4040u) ^ 0x80808080u;
       }
-      const float u = mq * (p.scale_log2 / (16.0f * 32639.0f));
+      // a head with an infinity or NaN is NaN
+      const float u = mq <= 65504.0f ? mq * (p.scale_log2 / (16.0f * 32639.0f)) : NAN;
       unit[nn][0] = __shfl_sync(0xffffffffu, u, 8 * t4);
       unit[nn][1] = __shfl_sync(0xffffffffu, u, 8 * t4 + 4);
     }
@@ -670,7 +681,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t w[2][NT][2];  // weights and what their rounding left, as operands
+        constexpr int kW = TWICE ? 1 : 2;
+        uint32_t w[kW][NT][2];  // weights and what their rounding left, as operands
         float c8[NT][4];  // -8 sum(w): rows g in the units of codes_lo, rows g + 8 of codes_hi
         const float v0 = vs[h][0] * vinv, v1 = vs[h][1] * vinv;
 #pragma unroll
@@ -680,18 +692,22 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
           l[nn][0] += p0 + p2;
           l[nn][1] += p1 + p3;
           const float2 wa = make_float2(p0 * v0, p1 * v0), wb = make_float2(p2 * v1, p3 * v1);
-          const __half2 a = __float22half2_rn(wa), b = __float22half2_rn(wb);
-          // what the rounding left, as a second weight
+          __half2 a = __float22half2_rn(wa), b = __float22half2_rn(wb);
           const float2 ra = __half22float2(a), rb = __half22float2(b);
-          const __half2 al = __floats2half2_rn(wa.x - ra.x, wa.y - ra.y), bl = __floats2half2_rn(wb.x - rb.x, wb.y - rb.y);
-          w[0][nn][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&a));
-          w[0][nn][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&b));
-          w[1][nn][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&al));
-          w[1][nn][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&bl));
-          const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+          const float take = TWICE && t4 < 2 ? 0.f : 1.f;  // columns 0-3 keep the weight itself
+          const __half2 al = __floats2half2_rn(__fmaf_rn(-take, ra.x, wa.x), __fmaf_rn(-take, ra.y, wa.y));
+          const __half2 bl = __floats2half2_rn(__fmaf_rn(-take, rb.x, wb.x), __fmaf_rn(-take, rb.y, wb.y));
+          w[kW - 1][nn][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&al));
+          w[kW - 1][nn][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&bl));
+          if (!TWICE) {
+            w[0][nn][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&a));
+            w[0][nn][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&b));
+          }
           // -2^-21 = -8 2^-24 and -2^-17 = -8 2^-20 as fp16
+          const float zero[4] = {0.f, 0.f, 0.f, 0.f};
           mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w[0][nn][0], w[0][nn][1], zero);
-          mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w[1][nn][0], w[1][nn][1], c8[nn]);
+          if (!TWICE)
+            mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w[kW - 1][nn][0], w[kW - 1][nn][1], c8[nn]);
         }
         // values: lane (g, t4) holds dims [16 g, 16 g + 16) of its four tokens
         const uint2 x0 = *reinterpret_cast<const uint2*>(sp + va_off + h * 1024);
@@ -710,10 +726,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
 #pragma unroll
           for (int nn = 0; nn < NT; ++nn) {
             float d[4];
-            mma_f16(o[nn][2 * j], a0, a1, a2, a3, w[1][nn][0], w[1][nn][1], o[nn][2 * j]);
+            if (!TWICE) mma_f16(o[nn][2 * j], a0, a1, a2, a3, w[kW - 1][nn][0], w[kW - 1][nn][1], o[nn][2 * j]);
             mma_f16(d, a0, a1, a2, a3, w[0][nn][0], w[0][nn][1], c8[nn]);
             add4(o[nn][2 * j], d);
-            mma_f16(o[nn][2 * j + 1], b0, b1, b2, b3, w[1][nn][0], w[1][nn][1], o[nn][2 * j + 1]);
+            if (!TWICE) mma_f16(o[nn][2 * j + 1], b0, b1, b2, b3, w[kW - 1][nn][0], w[kW - 1][nn][1], o[nn][2 * j + 1]);
             mma_f16(d, b0, b1, b2, b3, w[0][nn][0], w[0][nn][1], c8[nn]);
             add4(o[nn][2 * j + 1], d);
           }
@@ -833,9 +849,9 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
 int attn_nt(int G) { return G > 8 ? 2 : 1; }
 int attn_grid(int nt) { return sm_count() * (nt == 1 ? 2 : 1); }
 
-template <int NT, bool P16>
+template <int NT, bool TWICE, bool P16>
 fq_status launch_attn(const AttnParams& p, cudaStream_t stream) {
-  auto kern = kv_attn_kernel<NT, P16>;
+  auto kern = kv_attn_kernel<NT, TWICE, P16>;
   constexpr size_t smem = size_t(kWarps) * (kDepth * kStepBytes + NT * kPieceFloats * sizeof(float));
   static std::atomic<uint64_t> allowed{0};
   if (!allow_smem(kern, smem, allowed))
@@ -872,7 +888,7 @@ fq_status fq_kv_attn(const uint16_t* Q, long long ldq, int R, int Hq, const int3
   FQ_CHECK_ARG(max_pages >= 1 && static_cast<long long>(max_pages) * cache->page_size < (1ll << 31),
                "max_pages = %d: at least 1, and fewer than 2^31 tokens", max_pages);
   FQ_CHECK_ARG(window >= 0, "window = %d must not be negative", window);
-  FQ_CHECK_ARG(scale == scale && scale - scale == 0.f, "scale must be finite");
+  FQ_CHECK_ARG(scale >= -65536.0f && scale <= 65536.0f, "scale = %g must lie in [-65536, 65536]", double(scale));
   const size_t need = fq_kv_attn_workspace_size(R, Hq, cache->H);
   if (!workspace || ws_bytes < need || !fq::aligned(workspace, 256))
     return fq::fail(FQ_ERR_INVALID, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, ws_bytes);
@@ -895,8 +911,9 @@ fq_status fq_kv_attn(const uint16_t* Q, long long ldq, int R, int Hq, const int3
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + fq::sync_block_bytes());
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool p16 = cache->page_size == 16;
-  if (nt == 1) return p16 ? fq::launch_attn<1, true>(p, cs) : fq::launch_attn<1, false>(p, cs);
-  return p16 ? fq::launch_attn<2, true>(p, cs) : fq::launch_attn<2, false>(p, cs);
+  if (nt == 2) return p16 ? fq::launch_attn<2, false, true>(p, cs) : fq::launch_attn<2, false, false>(p, cs);
+  if (p.G > 4) return p16 ? fq::launch_attn<1, false, true>(p, cs) : fq::launch_attn<1, false, false>(p, cs);
+  return p16 ? fq::launch_attn<1, true, true>(p, cs) : fq::launch_attn<1, true, false>(p, cs);
 }
 
 }  // extern "C"

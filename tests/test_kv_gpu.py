@@ -268,6 +268,33 @@ def test_attn_lengths(lens, page):
     check_attn(run_attn(*case), *case, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("page", [16, 32])
+@pytest.mark.parametrize("lens", LENS)
+def test_attn_lengths_with_six_queries_a_head(lens, page):
+    case = attn_case(1, lens, 12, 2, page)
+    check_attn(run_attn(*case), *case, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("hq,h", [(4, 1), (6, 1), (12, 1), (16, 4)])
+@pytest.mark.parametrize("page", [16, 64])
+def test_attn_long_head_layouts(hq, h, page):
+    case = attn_case(12, [9001, 1, 333], hq, h, page)
+    check_attn(run_attn(*case), *case, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("hq,h", [(4, 2), (8, 2), (16, 2), (32, 2)])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_attn_queries_that_are_not_finite(hq, h, bad):
+    q, ln, table, pool = attn_case(13, [3000, 40, 0], hq, h, 32)
+    good = run_attn(q, ln, table, pool)
+    q[0, 1, 5] = q[1, hq - 1, 127] = q[2, 0, 0] = bad
+    y = run_attn(q, ln, table, pool)
+    hit = torch.zeros(3, hq, 1, dtype=torch.bool, device="cuda")
+    hit[0, 1] = hit[1, hq - 1] = True
+    assert torch.equal(torch.isnan(y.view(3, hq, 128)), hit.expand(3, hq, 128))
+    assert torch.equal(y.view(3, hq, 128)[~hit[..., 0]], good.view(3, hq, 128)[~hit[..., 0]])
+
+
 @pytest.mark.parametrize("hq,h", [(1, 1), (2, 1), (3, 3), (5, 1), (7, 1), (8, 1), (9, 1), (16, 1), (17, 1), (40, 1),
                                   (32, 32), (24, 8), (128, 128), (71, 1), (64, 8), (36, 3)])
 def test_attn_head_layouts(hq, h):

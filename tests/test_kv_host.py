@@ -81,6 +81,14 @@ def test_kv_attn_refusals(L, change, msg):
     assert st == fq.FQ_ERR_INVALID and msg in L.fq_last_error()
 
 
+@pytest.mark.parametrize("scale", [65537.0, -65537.0, 3e38])
+def test_kv_attn_scales_that_could_overflow_are_refused(L, scale):
+    c = _cache()
+    ws = L.fq_kv_attn_workspace_size(2, 8, 4)
+    assert L.fq_kv_attn(A, 1024, 2, 8, A, A, 4, ctypes.byref(c), scale, 0, A, A, ws, None) == fq.FQ_ERR_INVALID
+    assert b"scale" in L.fq_last_error()
+
+
 def test_kv_attn_workspace_sizes(L):
     assert L.fq_kv_attn_workspace_size(1, 8, 8) == fq.SYNC_BYTES + 2 * 296 * 8 * 130 * 4
     assert L.fq_kv_attn_workspace_size(16384, 128, 8) == fq.SYNC_BYTES + 2 * 148 * 16 * 130 * 4
