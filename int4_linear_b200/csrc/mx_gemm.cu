@@ -12,15 +12,19 @@
 // third of the rate, from one thread 13 % of NVFP4's), one of warp 1 the four MMAs of a stage; warps
 // 4-7 drain finished tiles. Every stage has its own scale columns, so the stage's barriers guard both.
 //
-// More than 128 tokens run on CTA pairs (PAIR): 256 weight rows per tile, each CTA
+// More than 64 tokens run on CTA pairs (PAIR): 256 weight rows per tile, each CTA
 // holding its 128 rows, half of the tokens' rows and the scales of all of them; the even CTA's
 // thread issues for both. A stage's copies of both CTAs complete on the even CTA's barrier, and its
 // commits reach both.
 //
-// Work: whole tiles dealt to the CTAs in turn, or, where the tiles do not fill
-// the SMs evenly and K is what there is to divide, equal contiguous parts of
-// the (tile, stage) sequence; the CTA that arrives last at a divided tile adds
-// the float32 parts in the CTAs' order.
+// Work: whole tiles dealt to the CTAs in turn, or, for up to 64 tokens where that leaves SMs idle for
+// longer than a join takes, equal contiguous parts of the (tile, stage) sequence; the CTA that arrives
+// last at a divided tile adds the float32 parts in the CTAs' order.
+//
+// Bounds (2 M N K operations at four times the bf16 rate, 6.6 PFLOP/s, or the weights' bytes at 6.55 TB/s), with the
+// quantizer before it: 16 x 57344 x 8192 (M x N x K) 40.4 us, 6.2 TB/s; 2048 x 28672 x 4096 100 us,
+// 4.8 PFLOP/s, there the power limit holds the clock at 1.5-1.6 GHz; a single token's 6144 x 4096
+// takes 8.3 us, nearly all of it launch, first loads, and the way out.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -40,6 +44,7 @@ constexpr int kRowB = kStageK / 2;              // 128 bytes per row
 constexpr int kTileN = 128;                     // weight rows per tile
 constexpr int kMxGemmThreads = 256;
 constexpr int kStoreRows = 16;                  // tokens per output block
+constexpr int kJoinParts = 4;                   // parts of a divided tile read at once
 constexpr int kStoreBytes = kStoreRows * 32 * 2;  // one warp's 16 x 32 outputs
 
 struct MxGemmParams {
@@ -140,6 +145,12 @@ __device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* map, uin
         "%4}], [%2], %5;" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(pol)
         : "memory");
+}
+
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
 }
 
 // shared::cluster address of `p`'s counterpart in CTA `rank`.
@@ -326,7 +337,7 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_launch_dependents();
-  pdl_wait();
+  if (warp != 0) pdl_wait();  // the producer prefetches first
 
   MxWalk walk(p, unit, units);
   if (warp == 0) {
@@ -340,6 +351,20 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
     }
     const uint64_t pol_w = BN <= 64 ? policy_evict_first() : policy_evict_normal();  // few tokens: read once
     const uint64_t pol_x = policy_evict_last();  // the tokens are read by every CTA
+    // The first stages' weights into L2 (where a running kernel's writes go as well) while the tokens are being
+    // quantized: 42.5 -> 40.4 us for 16 x 57344 x 8192; two or four rings' worth made 777 x 5000 x 4224 slower.
+    {
+      MxWalk w = walk;
+      int ahead = 0;
+      while (ahead < S && w.next())
+        for (int k = w.k0; k < w.k1 && ahead < S; ++k, ++ahead)
+          if (leader) {
+            const int nt = w.tile / p.mt * (PAIR ? 2 : 1) + int(rank);
+            prefetch_tile(&tmW, k * kRowB, nt * kTileN);
+            prefetch_tile(&tmSw, k * C::SB * 64, nt);
+          }
+    }
+    pdl_wait();
     const uint32_t bar0 = PAIR ? cluster_addr(full, 0) : smem_u32(full);
     MxStage st;
     int sent = 0;
@@ -569,14 +594,14 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
         }
         continue;
       }
-      // a part of a tile: float32 sums to this CTA's slot, as the lanes hold them: [warp][16 tokens][16][32]
+      // a part of a tile: float32 sums to this CTA's slot, as the lanes hold them: [warp][16 tokens][4][32 lanes][4]
       const long long total = static_cast<long long>(p.tiles) * p.ks, t0 = static_cast<long long>(walk.tile) * p.ks;
       const int G = units;
       const int c_first = int(((t0 + 1) * G - 1) / total);
       const int parts = int(((t0 + p.ks) * G - 1) / total) - c_first + 1;
       const size_t slot_floats = size_t(BN) * kTileN;
       const int cols = min(BN, p.M - mt * BN);
-      const size_t mine = size_t(w) * BN * 32 + lane;
+      const size_t mine = size_t(w) * BN * 32 + lane * 4;
       float* dst = p.part + (2 * size_t(blockIdx.x) + (walk.k0 == 0 ? 1 : 0)) * slot_floats + mine;
 #pragma unroll
       for (int c = 0; c < BN; c += CH) {
@@ -587,8 +612,10 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
         for (int q = 0; q < CH / 16; ++q)
           if (c + 16 * q < cols) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              dst[((c + 16 * q) + j) * 32] = __uint_as_float(v[FR * (j >> 3) + 8 * q + (j & 7)]);
+            for (int j = 0; j < 16; j += 4) {
+              const uint32_t* f = v + FR * (j >> 3) + 8 * q + (j & 7);
+              *reinterpret_cast<uint4*>(dst + (c + 16 * q + j) * 32) = make_uint4(f[0], f[1], f[2], f[3]);
+            }
           }
       }
       release();
@@ -602,10 +629,26 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
           float acc[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-          for (int i = 0; i < parts; ++i) {
-            const float* src = p.part + (2 * size_t(c_first + i) + (i == 0)) * slot_floats + mine + c * 32;
+          for (int i = 0; i < parts; i += kJoinParts) {
+            float4 v[kJoinParts][4];  // all under way at once: the join waits for memory
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[j] += __ldcg(src + j * 32);
+            for (int u = 0; u < kJoinParts; ++u)
+              if (i + u < parts) {
+                const float* src = p.part + (2 * size_t(c_first + i + u) + (i + u == 0)) * slot_floats + mine + c * 32;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[u][j] = __ldcg(reinterpret_cast<const float4*>(src + j * 128));
+              }
+#pragma unroll
+            for (int u = 0; u < kJoinParts; ++u)
+              if (i + u < parts) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  acc[4 * j] += v[u][j].x;
+                  acc[4 * j + 1] += v[u][j].y;
+                  acc[4 * j + 2] += v[u][j].z;
+                  acc[4 * j + 3] += v[u][j].w;
+                }
+              }
           }
           uint32_t hh[8];
 #pragma unroll
@@ -633,7 +676,16 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
   }
 }
 
-// Tokens per tile, tiles and whether K is divided, from the sizes alone.
+// Tokens per tile, tiles and whether K is divided, from the sizes alone.  Measured, quantizer included, us:
+//  - pairs or single CTAs (tiles of 128 tokens): 128 x 8192 x 28672 (M x N x K) 38.1 / 39.2,
+//    128 x 57344 x 8192 51.7 / 54.2, 256 x 4096 x 4096 10.5 / 20.2, 2048 x 28672 x 4096 102 / 137;
+//    for 100 x 57344 x 2048 in NVFP4 17.7 / 17.0;
+//  - tiles of 128 or 256 tokens on pairs: 256 x 4096 x 4096 10.5 / 12.4, 777 x 5000 x 4224 19.4 / 23.8,
+//    1024 x 6144 x 4096 22.0 / 20.9, 2048 x 28672 x 4096 124 / 102: a tile of 256 takes 20 / 11 of one of 128;
+//  - divided or not: a stage of a lone tile takes 0.28 us and the join of a tile what 12 + BN / 4 stages take (the
+//    parts' way through memory, and their count on one CTA).  8 x 6144 x 4096 9.4 / 8.3, 8 x 28672 x 4096 14.4 / 13.9,
+//    8 x 57344 x 8192 40.1 / 42.4, 8 x 4096 x 14336 11.9 / 19.1, 64 x 6144 x 4096 13.0 / 9.4, 64 x 8192 x 28672
+//    27.1 / 37.8.
 struct MxPlan {
   int bn, mt, tiles, ks, split, grid;
   bool pair;
@@ -643,11 +695,11 @@ MxPlan mx_plan(int M, int N, int K) {
   MxPlan q;
   const int sms = sm_count();
   q.ks = (K + kStageK - 1) / kStageK;
-  q.pair = M > 128;
+  q.pair = M > 64;
   const int workers = q.pair ? sms / 2 : sms;
   const int nt = (N + (q.pair ? 255 : 127)) / (q.pair ? 256 : 128);
   if (!q.pair) {
-    q.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    q.bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
   } else {
     const long long t128 = static_cast<long long>(nt) * ((M + 127) / 128), t256 = static_cast<long long>(nt) * ((M + 255) / 256);
     const long long w128 = (t128 + workers - 1) / workers, w256 = (t256 + workers - 1) / workers;
@@ -655,8 +707,8 @@ MxPlan mx_plan(int M, int N, int K) {
   }
   q.mt = (M + q.bn - 1) / q.bn;
   q.tiles = nt * q.mt;
-  q.split = !q.pair && (q.bn <= 64 || (q.tiles < sms && q.ks > 1));
-  const long long units = static_cast<long long>(q.tiles) * q.ks;
+  const long long units = static_cast<long long>(q.tiles) * q.ks, waves = (q.tiles + workers - 1) / workers;
+  q.split = !q.pair && waves * q.ks > (units + workers - 1) / workers + 12 + q.bn / 4;
   q.grid = int(std::min<long long>(workers, q.split ? units : q.tiles)) * (q.pair ? 2 : 1);
   return q;
 }
@@ -682,8 +734,7 @@ fq_status launch_mx_bn(const MxPlan& q, const MxGemmParams& p, const CUtensorMap
   switch (q.bn) {
     case 16: return launch_mx<FMT, 16, false>(p, m, q.grid, stream);
     case 32: return launch_mx<FMT, 32, false>(p, m, q.grid, stream);
-    case 64: return launch_mx<FMT, 64, false>(p, m, q.grid, stream);
-    default: return launch_mx<FMT, 128, false>(p, m, q.grid, stream);
+    default: return launch_mx<FMT, 64, false>(p, m, q.grid, stream);
   }
 }
 
@@ -702,8 +753,10 @@ extern "C" {
 size_t fq_mx_gemm_workspace_size(int M, int N, int K, fq_mx_format fmt) {
   if (!fq::mx_sizes_ok(M, N, K, fmt)) return 0;
   const fq::MxPlan q = fq::mx_plan(M, N, K);
-  if (!q.split) return 0;
-  return fq::sync_block_bytes() + size_t(2) * q.grid * q.bn * fq::kTileN * sizeof(float);
+  if (q.pair) return 0;
+  // whether or not K is divided, so that the caller need not know
+  const long long ctas = std::min<long long>(fq::sm_count(), static_cast<long long>(q.tiles) * q.ks);
+  return fq::sync_block_bytes() + size_t(2) * ctas * q.bn * fq::kTileN * sizeof(float);
 }
 
 size_t fq_mx_linear_workspace_size(int M, int N, int K, fq_mx_format fmt) {

@@ -106,7 +106,7 @@ def upload(code, sb):
     return dev(MO.pack(code)), dev(MO.to_tiles(sb, fill=0xFF))    # NaN in the padding rows
 
 
-# every token-tile width, divided and whole K, ragged edges on all sides
+# every token-tile width, ragged edges on all sides
 SHAPES = [(1, 8, 128), (1, 136, 256), (5, 128, 384), (16, 1000, 512), (17, 256, 128), (32, 72, 640), (33, 520, 256),
           (64, 384, 1152), (65, 128, 256), (100, 264, 384), (128, 128, 128), (129, 136, 256), (255, 256, 512),
           (256, 128, 384), (300, 1032, 256), (513, 264, 128)]
@@ -161,6 +161,14 @@ def test_product_wide_scales(fmt, m, n, k):
         y = fq.fq_mx_gemm(xq, sx, wq, sw, fmt, f32(gx), f32(gw))
     fq.fq_check_device_error()
     check_product(y, acc, mag, k, scale)
+
+
+# divided: few tiles of many stages, tiles in many parts, parts of three tiles; whole: several tiles a CTA
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m,n,k", [(1, 8, 65536), (16, 1160, 20608), (20, 264, 16512), (32, 4096, 8320), (50, 1000, 20608),
+                                   (64, 2048, 14336), (5, 20000, 8192), (33, 40000, 640), (7, 38400, 384)])
+def test_product_divided_and_whole(fmt, m, n, k):
+    test_product_wide_scales(fmt, m, n, k)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
