@@ -217,51 +217,72 @@ constexpr int kRowThreads = 256;
 // cut first, to 7.25 s and -8.25 s, which round to 7 and -8.
 __device__ __forceinline__ uint32_t codes8(const __half2 (&v)[4], __half2 top, __half2 bottom, float inv) {
   constexpr float kFine = 1536.0f, kWhole = 12582912.0f;
-  uint32_t w = 0;
+  uint32_t even[4], odd[4];  // codes in the low bits
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 f = __half22float2(__hmax2(__hmin2(v[j], top), bottom));
     const float2 a = ffma2(f, make_float2(inv, inv), make_float2(kFine, kFine));
     const float2 q = fadd2(a, make_float2(kWhole - kFine, kWhole - kFine));
-    const uint32_t lo = __float_as_uint(q.x) & 15u, hi = __float_as_uint(q.y) & 15u;
-    w |= (lo | hi << 4) << (8 * j);
+    even[j] = __float_as_uint(q.x);
+    odd[j] = __float_as_uint(q.y);
   }
-  return w;
+  const uint32_t e = __byte_perm(__byte_perm(even[0], even[1], 0x0040), __byte_perm(even[2], even[3], 0x0040), 0x5410);
+  const uint32_t o = __byte_perm(__byte_perm(odd[0], odd[1], 0x0040), __byte_perm(odd[2], odd[3], 0x0040), 0x5410);
+  return (e & 0x0F0F0F0Fu) | ((o << 4) & 0xF0F0F0F0u);
 }
 
-// Token, head and kind (0 key, 1 value) of vector vec, a token's vectors being its H keys, then its H values.
+// Token, head and kind (0 key, 1 value) of a head vector, a token's vectors being its H keys, then its H values.
 struct KvVec {
   long long t;
   int h, which;
 };
-__device__ __forceinline__ KvVec kv_vector(long long vec, int H) {
-  const uint32_t per = 2u * uint32_t(H);
-  KvVec v;
-  v.t = (vec >> 32) == 0 ? uint32_t(vec) / per : vec / per;
-  const int h = int(vec - v.t * per);
-  v.which = h >= H;
-  v.h = v.which ? h - H : h;
-  return v;
-}
+// What the vectors of one thread, a grid apart, are apart in tokens and in a token's vectors.
+struct KvStep {
+  long long vecs, tokens;
+  int rest;
+};
+// A thread's vectors: one division to begin with instead of one per vector.
+struct KvWalk {
+  long long t, dt;
+  int r, dr, H;
+  __device__ __forceinline__ KvWalk(long long vec, const KvStep& step, int heads)
+      : dt(step.tokens), dr(step.rest), H(heads) {
+    const uint32_t per = 2u * uint32_t(H);
+    t = (vec >> 32) == 0 ? uint32_t(vec) / per : vec / per;
+    r = int(vec - t * per);
+  }
+  __device__ __forceinline__ KvVec next() {
+    const int which = r >= H;
+    const KvVec v{t, which ? r - H : r, which};
+    t += dt;
+    r += dr;
+    if (r >= 2 * H) {
+      r -= 2 * H;
+      ++t;
+    }
+    return v;
+  }
+};
 
 // One head vector per 8 lanes, each with the 8 values at 8 sub and at 64 + 8 sub (whole sectors per load and
 // store), two vectors per turn, read before their slots are known so that the loads overlap.  Bound by HBM
 // (256 bytes read, 66 written per vector) and, at 46 registers, by the 40 warps of an SM that ask for it: 16384
-// tokens of 8 heads 19.4 us, 4.4 TB/s; held to 32 registers it took 22.2 us.
+// tokens of 8 heads 17.8 us, 4.7 TB/s, 65536 66 us, 5.1 TB/s; held to 32 registers it took a seventh longer, and
+// with a division per vector for its token a tenth.
 __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const __half* __restrict__ K, long long ldk,
                                                                const __half* __restrict__ V, long long ldv, int T,
                                                                const int32_t* __restrict__ slots, float alpha_k,
-                                                               float alpha_v, KvView c) {
+                                                               float alpha_v, KvView c, KvStep step) {
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kVecs = 2;
   const int sub = threadIdx.x & 7;
   const int limit = c.num_pages << c.page_shift;
   const long long total = 2ll * T * c.H;
-  const long long step = static_cast<long long>(gridDim.x) * (kRowThreads / 8);
   // every lane of a warp takes the same number of turns (the shuffles below)
   const long long first = static_cast<long long>(blockIdx.x) * (kRowThreads / 8) + (threadIdx.x >> 3);
-  for (long long base = first - ((threadIdx.x >> 3) & 3); base < total; base += kVecs * step) {
+  KvWalk walk(first, step, c.H);
+  for (long long base = first - ((threadIdx.x >> 3) & 3); base < total; base += kVecs * step.vecs) {
     const long long vec0 = base + ((threadIdx.x >> 3) & 3);
     KvVec v[kVecs];
     uint4 raw[kVecs][2];
@@ -270,8 +291,8 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const __half* __r
     for (int u = 0; u < kVecs; ++u) {
       raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
       slot[u] = -1;
-      if (vec0 + u * step < total) {
-        v[u] = kv_vector(vec0 + u * step, c.H);
+      v[u] = walk.next();
+      if (vec0 + u * step.vecs < total) {
         const uint4* src =
             reinterpret_cast<const uint4*>((v[u].which ? V + v[u].t * ldv : K + v[u].t * ldk) + v[u].h * kHeadDim) + sub;
         raw[u][0] = src[0];
@@ -306,20 +327,22 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const __half* __r
 }
 
 // Codes and scales as fq_quant_kv wrote them: four lanes per head vector.  66 bytes read and written; 16384 tokens of 8
-// heads 7.5 us (they stay in L2), 65536 27 us, 2.6 TB/s of reads and as much of writes.
+// heads 7.2 us (they stay in L2), 65536 26 us, 2.6 TB/s of reads and as much of writes.
 __global__ void __launch_bounds__(kRowThreads) kv_store_kernel(const uint8_t* __restrict__ Kq,
                                                                const __half* __restrict__ Ks,
                                                                const uint8_t* __restrict__ Vq,
                                                                const __half* __restrict__ Vs, int T,
-                                                               const int32_t* __restrict__ slots, KvView c) {
+                                                               const int32_t* __restrict__ slots, KvView c,
+                                                               KvStep step) {
   pdl_launch_dependents();
   pdl_wait();
   const int sub = threadIdx.x & 3;
   const int limit = c.num_pages << c.page_shift;
   const long long total = 2ll * T * c.H;
-  for (long long vec = static_cast<long long>(blockIdx.x) * (kRowThreads / 4) + (threadIdx.x >> 2); vec < total;
-       vec += static_cast<long long>(gridDim.x) * (kRowThreads / 4)) {
-    const KvVec v = kv_vector(vec, c.H);
+  const long long first = static_cast<long long>(blockIdx.x) * (kRowThreads / 4) + (threadIdx.x >> 2);
+  KvWalk walk(first, step, c.H);
+  for (long long vec = first; vec < total; vec += step.vecs) {
+    const KvVec v = walk.next();
     const long long t = v.t;
     const int h = v.h, which = v.which;
     const int slot = slots[t];
@@ -335,19 +358,19 @@ __global__ void __launch_bounds__(kRowThreads) kv_store_kernel(const uint8_t* __
 
 // One head vector per 8 lanes, each with the 8 values at 8 sub and at 64 + 8 sub (whole sectors per load and
 // store), four vectors per turn so that their slots and codes are loaded together.  One rounding: the fp16 product.  Bound by
-// HBM (66 bytes read, 256 written per vector): 16384 tokens of 8 heads 14.4 us, 5.9 TB/s.
+// HBM (66 bytes read, 256 written per vector): 16384 tokens of 8 heads 14.1 us, 6.0 TB/s.
 __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const int32_t* __restrict__ slots, int T,
                                                               __half* __restrict__ K, __half* __restrict__ V,
-                                                              KvView c) {
+                                                              KvView c, KvStep step) {
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kVecs = 4;
   const int sub = threadIdx.x & 7;
   const int limit = c.num_pages << c.page_shift;
   const long long total = 2ll * T * c.H;
-  const long long step = static_cast<long long>(gridDim.x) * (kRowThreads / 8);
-  for (long long vec = static_cast<long long>(blockIdx.x) * (kRowThreads / 8) + (threadIdx.x >> 3); vec < total;
-       vec += kVecs * step) {
+  const long long first = static_cast<long long>(blockIdx.x) * (kRowThreads / 8) + (threadIdx.x >> 3);
+  KvWalk walk(first, step, c.H);
+  for (long long vec = first; vec < total; vec += kVecs * step.vecs) {
     KvVec v[kVecs];
     int slot[kVecs];
     uint2 w[kVecs];
@@ -355,10 +378,8 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const int32_t* __r
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       slot[u] = -1;
-      if (vec + u * step < total) {
-        v[u] = kv_vector(vec + u * step, c.H);
-        slot[u] = slots[v[u].t];
-      }
+      v[u] = walk.next();
+      if (vec + u * step.vecs < total) slot[u] = slots[v[u].t];
     }
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
@@ -374,7 +395,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const int32_t* __r
     }
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
-      if (vec + u * step >= total) break;
+      if (vec + u * step.vecs >= total) break;
       uint4 out[2];
       __half2* o2 = reinterpret_cast<__half2*>(out);
       const __half2 s2 = __half2half2(s[u]);
@@ -395,9 +416,14 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const int32_t* __r
   }
 }
 
-int row_grid(long long vectors, int lanes) {
-  const long long want = (vectors * lanes + kRowThreads - 1) / kRowThreads;
-  return int(std::min<long long>(std::max<long long>(want, 1), static_cast<long long>(sm_count()) * 8));
+// CTAs for 2 T H head vectors of `lanes` lanes each, and the step that they make.
+int row_grid(int T, int H, int lanes, KvStep& step) {
+  const long long vectors = 2ll * T * H, want = (vectors * lanes + kRowThreads - 1) / kRowThreads;
+  const int grid = int(std::min<long long>(std::max<long long>(want, 1), static_cast<long long>(sm_count()) * 8));
+  step.vecs = static_cast<long long>(grid) * (kRowThreads / lanes);
+  step.tokens = step.vecs / (2 * H);
+  step.rest = int(step.vecs % (2 * H));
+  return grid;
 }
 
 }  // namespace
@@ -465,9 +491,11 @@ fq_status fq_kv_write(const uint16_t* K, long long ldk, const uint16_t* V, long 
   FQ_CHECK_ARG(ldk >= row && ldv >= row && ldk % 8 == 0 && ldv % 8 == 0,
                "row strides %lld and %lld must be multiples of 8 and at least H * 128 = %lld", ldk, ldv, row);
   FQ_CHECK_ARG(alpha_k > 0.f && alpha_k <= 1.f && alpha_v > 0.f && alpha_v <= 1.f, "alpha must lie in (0, 1]");
-  fq::launch_pdl(fq::kv_write_kernel, dim3(fq::row_grid(2ll * T * cache->H, 8)), dim3(fq::kRowThreads), 0,
+  fq::KvStep step;
+  const int grid = fq::row_grid(T, cache->H, 8, step);
+  fq::launch_pdl(fq::kv_write_kernel, dim3(grid), dim3(fq::kRowThreads), 0,
                  static_cast<cudaStream_t>(stream), reinterpret_cast<const __half*>(K), ldk,
-                 reinterpret_cast<const __half*>(V), ldv, T, slots, alpha_k, alpha_v, fq::kv_view(cache));
+                 reinterpret_cast<const __half*>(V), ldv, T, slots, alpha_k, alpha_v, fq::kv_view(cache), step);
   return fq::check_launch("kv_write_kernel");
 }
 
@@ -481,9 +509,11 @@ fq_status fq_kv_store(const uint8_t* Kq, const uint16_t* Ks, const uint8_t* Vq, 
                "Kq and Vq must be non-NULL and 16-byte aligned");
   FQ_CHECK_ARG(Ks && Vs && fq::aligned(Ks, 2) && fq::aligned(Vs, 2), "Ks and Vs must be non-NULL and aligned");
   FQ_CHECK_ARG(slots && fq::aligned(slots, 4), "slots must be non-NULL and 4-byte aligned");
-  fq::launch_pdl(fq::kv_store_kernel, dim3(fq::row_grid(2ll * T * cache->H, 4)), dim3(fq::kRowThreads), 0,
+  fq::KvStep step;
+  const int grid = fq::row_grid(T, cache->H, 4, step);
+  fq::launch_pdl(fq::kv_store_kernel, dim3(grid), dim3(fq::kRowThreads), 0,
                  static_cast<cudaStream_t>(stream), Kq, reinterpret_cast<const __half*>(Ks), Vq,
-                 reinterpret_cast<const __half*>(Vs), T, slots, fq::kv_view(cache));
+                 reinterpret_cast<const __half*>(Vs), T, slots, fq::kv_view(cache), step);
   return fq::check_launch("kv_store_kernel");
 }
 
@@ -494,9 +524,11 @@ fq_status fq_kv_read(const fq_kv_cache* cache, const int32_t* slots, int T, uint
   FQ_CHECK_ARG(T >= 1, "T = %d must be >= 1", T);
   FQ_CHECK_ARG(K && V && fq::aligned(K, 16) && fq::aligned(V, 16), "K and V must be non-NULL and 16-byte aligned");
   FQ_CHECK_ARG(slots && fq::aligned(slots, 4), "slots must be non-NULL and 4-byte aligned");
-  fq::launch_pdl(fq::kv_read_kernel, dim3(fq::row_grid(2ll * T * cache->H, 8)), dim3(fq::kRowThreads), 0,
+  fq::KvStep step;
+  const int grid = fq::row_grid(T, cache->H, 8, step);
+  fq::launch_pdl(fq::kv_read_kernel, dim3(grid), dim3(fq::kRowThreads), 0,
                  static_cast<cudaStream_t>(stream), slots, T, reinterpret_cast<__half*>(K),
-                 reinterpret_cast<__half*>(V), fq::kv_view(cache));
+                 reinterpret_cast<__half*>(V), fq::kv_view(cache), step);
   return fq::check_launch("kv_read_kernel");
 }
 

@@ -175,6 +175,32 @@ def test_write_and_read_bits(t, h, page, alpha):
         assert np.array_equal(got, ref)
 
 
+@pytest.mark.parametrize("t,h", [(9001, 5), (20011, 3), (700, 127)])
+def test_many_head_vectors(t, h):
+    """Several turns of every thread, whose tokens and heads step on by other than whole tokens: written, read
+    and stored again."""
+    g = rng(14, t, h)
+    page = 32
+    x = g.standard_normal((2, t, h, 128)).astype(np.float16)
+    pages = -(-t // page) + 1
+    slots = g.permutation(pages * page)[:t].astype(np.int32)
+    kq, ks = KO.quant_rows(x[0], 1.0)
+    vq, vs = KO.quant_rows(x[1], 1.0)
+    want = KO.empty_pool(pages, h, page)
+    KO.store(want, kq, ks, vq, vs, slots)
+    cache, sl = fq.kv_cache(pages, h, page), dev(slots)
+    fq.fq_kv_write(dev(x[0]), dev(x[1]), sl, cache)
+    assert np.array_equal(cache.pool.cpu().numpy(), want)
+    for got, q, s in zip(fq.fq_kv_read(cache, sl), (kq, vq), (ks, vs)):
+        assert np.array_equal(got.cpu().numpy(), (q.astype(np.float32) * s.astype(np.float32)[..., None]).astype(np.float16))
+    views = [v.permute(0, 2, 1, 3) if v.dim() == 4 else v.permute(0, 2, 1) for v in cache.views()]
+    rows = [v.reshape(pages * page, h, -1)[sl.long()] for v in views]
+    again = fq.kv_cache(pages, h, page)
+    fq.fq_kv_store(rows[0].reshape(t, h * 64), rows[2].reshape(t, h), rows[1].reshape(t, h * 64), rows[3].reshape(t, h),
+                   sl, again)
+    assert torch.equal(again.pool, cache.pool)
+
+
 def test_store_of_transformed_codes():
     """fq_quant_kv's codes through P_h, then fq_kv_store: the pages hold the same bytes."""
     g = rng(4)
