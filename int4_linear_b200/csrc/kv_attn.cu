@@ -7,7 +7,7 @@
 // against 4 * 128 operations per query head, so the work is a stream of pages
 // with the arithmetic hidden under it.  At the measured 6.55 TB/s an SM has
 // about 5.7 cycles per token and head, i.e. some 23 warp instructions; this kernel
-// executes 20, and with the four warps that a scheduler's registers hold issues in 54 % of the
+// executes 19, and with the four warps that a scheduler's registers hold issues in 54 % of the
 // cycles, waiting for products and their results: 64 requests of 8 heads and 14200
 // tokens on average (eight queries a head) take 217 us, 4.4 TB/s.
 //
@@ -165,7 +165,7 @@ __device__ __forceinline__ void add4(float (&a)[4], const float (&b)[4]) {
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 
@@ -192,8 +192,10 @@ __device__ __forceinline__ int token_of_row(int i) {
 constexpr int kPieceFloats = 32 * 32 + 4;
 __device__ __forceinline__ int piece_offset(int i, int k, int lane) { return (4 * i + k) * 32 + lane + (i >> 1); }
 
+template <int TO = 0, int FROM = 0>
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(TO), "n"(FROM)
+               : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -345,11 +347,13 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   // what this lane copies of a turn: every 32nd 16-byte piece of the K and of the V codes, and lanes
   // 0-7 (pages of 16: 0-3 of each page) a piece of the scales
   constexpr int kHalves = P16 ? 2 : 1;
-  constexpr int kPieces = P16 ? 2 : 4;        // 512-byte pieces of one kind of codes per page taken
   constexpr int kScalePieces = P16 ? 2 : 4;   // 16-byte pieces of one kind of scales per page taken
-  const uint32_t my_ring = smem_u32(dyn) + uint32_t(warp * kDepth * kStepBytes);
-  const int sc_src = (2 * kKvRowBytes << ps) + (lane % kScalePieces) * 16 + (lane / kScalePieces & 1) * (2 << ps);
-  const uint32_t sc_dst = kStepKs + (lane % kScalePieces) * 16 + (lane / kScalePieces & 1) * (2 * kStep);
+  const uint32_t my_ring = smem_u32(dyn) + uint32_t(warp * kDepth * kStepBytes + lane * 16);
+  // its scales from and to, less the 16 lane of the codes
+  const int sc_src = (2 * kKvRowBytes << ps) + (lane % kScalePieces) * 16 + (lane / kScalePieces & 1) * (2 << ps) - lane * 16;
+  const uint32_t sc_dst = kStepKs + (lane % kScalePieces) * 16 + (lane / kScalePieces & 1) * (2 * kStep) - lane * 16;
+  const int v_src = kKvRowBytes << ps, page_mask = (1 << ps) - 1;
+  const uint32_t page_bytes = uint32_t(p.kv.H) * uint32_t(p.kv.block_bytes());  // of all heads: 2.2 MB at most
   // byte offsets inside a turn of this lane's operands
   const int row0 = token_of_row(g);           // score rows g and g + 8 of a half: tokens row0, row0 + 8
   const uint8_t* ring = dyn + warp * kDepth * kStepBytes;
@@ -358,8 +362,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   const int vb_off = kStepV + token_of_row(2 * t4 + 1) * kKvRowBytes + 8 * g;
   // A segment: turns [ta, tb) of the nt turns of a request and head.
   struct Seg {
-    int r, hc, tok0, turns, nt, ta, lo, hi;
-    long long item0;  // its request and head's first unit
+    int r, head, chunk, tok0, turns, nt, ta, lo, hi;  // key-value head, chunk of its query heads
+    long long item0;       // its request and head's first unit
+    const int32_t* row;    // its block table
+    const uint8_t* cache;  // its head in page 0, this lane's 16 bytes of codes
   };
   long long pos = first;
   auto next_segment = [&](Seg& q) {
@@ -379,7 +385,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       pos = min(item0 + units, last);
       if (tb <= ta) continue;
       q.r = wr;
-      q.hc = hc;
+      q.head = p.chunks == 1 ? hc : hc / p.chunks;
+      q.chunk = hc - q.head * p.chunks;
+      q.row = p.table + static_cast<size_t>(wr) * p.max_pages;
+      q.cache = p.kv.block(0, q.head) + lane * 16;
       q.item0 = item0;
       q.nt = nt;
       q.ta = ta;
@@ -399,29 +408,35 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
       const int t = q.tok0 + i * kStep + 16 * h;
-      const bool in = i < q.turns && (!P16 || t + 16 > q.lo) && t < q.hi;
-      v.id[h] = in ? __ldg(p.table + static_cast<size_t>(q.r) * p.max_pages + (t >> ps)) : -1;
+      // a half may lie before or behind the request's tokens
+      const bool in = i < q.turns && (!P16 || (t + 16 > q.lo && t < q.hi));
+      v.id[h] = in ? __ldg(q.row + (t >> ps)) : -1;
     }
     return v;
   };
   // Copies of turn i into ring slot `to`; returns which halves have their tokens (bits 0, 1).
   auto fetch = [&](const Seg& q, int i, const Ids& ids, int to) {
     uint32_t got = 0;
+    const uint32_t dst = my_ring + uint32_t(to * kStepBytes);
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
-      if (ids.id[h] >= 0 && ids.id[h] < p.kv.num_pages) {
-        const int off = P16 ? 0 : (q.tok0 + i * kStep) & ((1 << ps) - 1);
-        const uint8_t* src = p.kv.block(ids.id[h], q.hc / p.chunks);
-        const uint32_t dst = my_ring + uint32_t(to * kStepBytes);
-        const uint8_t* k = src + off * kKvRowBytes + lane * 16;
-        const uint8_t* v = k + (kKvRowBytes << ps);
-        const uint32_t d = dst + h * 1024 + lane * 16;
-#pragma unroll
-        for (int c = 0; c < kPieces; ++c) {
-          copy16(d + 512 * c, k + 512 * c);
-          copy16(d + kStepV + 512 * c, v + 512 * c);
+      if (uint32_t(ids.id[h]) < uint32_t(p.kv.num_pages)) {
+        const uint32_t off = P16 ? 0 : (q.tok0 + i * kStep) & page_mask;
+        const uint8_t* page = q.cache + static_cast<uint64_t>(uint32_t(ids.id[h])) * page_bytes;
+        const uint8_t* k = page + off * kKvRowBytes;
+        const uint8_t* v = k + v_src;
+        const uint32_t d = dst + h * 1024;
+        copy16<0, 0>(d, k);
+        copy16<512, 512>(d, k);
+        copy16<kStepV, 0>(d, v);
+        copy16<kStepV + 512, 512>(d, v);
+        if (!P16) {
+          copy16<1024, 1024>(d, k);
+          copy16<1536, 1536>(d, k);
+          copy16<kStepV + 1024, 1024>(d, v);
+          copy16<kStepV + 1536, 1536>(d, v);
         }
-        if (lane < 2 * kScalePieces) copy16(dst + sc_dst + h * 32, src + sc_src + 2 * off);
+        if (lane < 2 * kScalePieces) copy16(dst + sc_dst + h * 32, page + (sc_src + 2 * int(off)));
         got |= P16 ? 1u << h : 3u;
       }
     }
@@ -429,8 +444,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
     return got;
   };
   // Query heads of a segment: heads [q0, q0 + heads)
-  auto first_head = [&](const Seg& q) { return (q.hc / p.chunks) * p.G + (q.hc % p.chunks) * HB; };
-  auto head_count = [&](const Seg& q) { return min(HB, p.G - (q.hc % p.chunks) * HB); };
+  auto first_head = [&](const Seg& q) { return q.head * p.G + q.chunk * HB; };
+  auto head_count = [&](const Seg& q) { return min(HB, p.G - q.chunk * HB); };
   const int col = TWICE ? g & 3 : g;
   uint4 raw[NT][4];  // lane (g, t4): the head of column g, dims [32 t4, 32 t4 + 32)
   auto load_queries = [&](const Seg& q) {
