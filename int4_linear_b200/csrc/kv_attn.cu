@@ -9,7 +9,7 @@
 // about 5.7 cycles per token and head, i.e. some 23 warp instructions; this kernel
 // executes 19, and with the four warps that a scheduler's registers hold issues in 54 % of the
 // cycles, waiting for products and their results: 64 requests of 8 heads and 14200
-// tokens on average (eight queries a head) take 217 us, 4.4 TB/s.
+// tokens on average (eight queries a head) take 211 us, 4.5 TB/s.
 //
 // Division.  The turns (32 tokens of one request and key-value head) of all
 // requests form one sequence, request-major; every CTA takes an equal contiguous
@@ -37,8 +37,9 @@
 //  - sum: m16n8k16, A = 128 dims x 16 tokens of V codes (exact; a nibble u = code + 8 is the mantissa
 //    of a subnormal fp16, so an AND makes the operand, and one product with the constant -8
 //    starts the sums), B = the weights, taken from the scores' layout by movmatrix.  A lane reads 8 bytes of
-//    each of its 4 tokens and pairs two tokens' nibbles by byte permutation.  Sixteen tokens are
-//    added up in the tensor core, whose adds cut off; the running sums are rounded float32 adds.
+//    each of its 4 tokens and pairs two tokens' nibbles by byte permutation.  A turn's 32
+//    tokens are added up in the tensor core, whose adds cut off; the running sums are rounded float32 adds (added after
+//    every 16 tokens, attention took 2 to 6 % longer).
 // Weights: w = exp2(s - m) * (v scale / largest v scale so far) * 2^8 enters as two fp16 numbers, its
 // rounding and what that left (2^-22 relative, or 2^-33 of the largest where the second is
 // subnormal).  The rounding alone is 16 % faster on long caches (188 us for the 217 above), but leaves 1.5
@@ -694,11 +695,11 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
           }
         }
       }
+      constexpr int kW = TWICE ? 1 : 2;
+      uint32_t w[2][kW][NT][2];  // of both halves: weights and what their rounding left, as operands
+      float c8[NT][4];  // -8 sum(w): rows g in the units of codes_lo, rows g + 8 of codes_hi
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        constexpr int kW = TWICE ? 1 : 2;
-        uint32_t w[kW][NT][2];  // weights and what their rounding left, as operands
-        float c8[NT][4];  // -8 sum(w): rows g in the units of codes_lo, rows g + 8 of codes_hi
         const float v0 = vs[h][0] * vinv, v1 = vs[h][1] * vinv;
 #pragma unroll
         for (int nn = 0; nn < NT; ++nn) {
@@ -712,41 +713,63 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
           const float take = TWICE && t4 < 2 ? 0.f : 1.f;  // columns 0-3 keep the weight itself
           const __half2 al = __floats2half2_rn(__fmaf_rn(-take, ra.x, wa.x), __fmaf_rn(-take, ra.y, wa.y));
           const __half2 bl = __floats2half2_rn(__fmaf_rn(-take, rb.x, wb.x), __fmaf_rn(-take, rb.y, wb.y));
-          w[kW - 1][nn][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&al));
-          w[kW - 1][nn][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&bl));
+          w[h][kW - 1][nn][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&al));
+          w[h][kW - 1][nn][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&bl));
           if (!TWICE) {
-            w[0][nn][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&a));
-            w[0][nn][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&b));
+            w[h][0][nn][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&a));
+            w[h][0][nn][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&b));
           }
           // -2^-21 = -8 2^-24 and -2^-17 = -8 2^-20 as fp16
           const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w[0][nn][0], w[0][nn][1], zero);
+          if (h == 0)
+            mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w[h][0][nn][0], w[h][0][nn][1], zero);
+          else
+            mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w[h][0][nn][0], w[h][0][nn][1], c8[nn]);
           if (!TWICE)
-            mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w[kW - 1][nn][0], w[kW - 1][nn][1], c8[nn]);
+            mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w[h][kW - 1][nn][0], w[h][kW - 1][nn][1], c8[nn]);
         }
-        // values: lane (g, t4) holds dims [16 g, 16 g + 16) of its four tokens
-        const uint2 x0 = *reinterpret_cast<const uint2*>(sp + va_off + h * 1024);
-        const uint2 x1 = *reinterpret_cast<const uint2*>(sp + vb_off + h * 1024);
-        const uint2 x2 = *reinterpret_cast<const uint2*>(sp + va_off + h * 1024 + 8 * kKvRowBytes);
-        const uint2 x3 = *reinterpret_cast<const uint2*>(sp + vb_off + h * 1024 + 8 * kKvRowBytes);
+      }
+      // values: lane (g, t4) holds dims [16 g, 16 g + 16) of its four tokens of a half
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // four dims: half word j of the 16 dims
+      for (int jj = 0; jj < 2; ++jj) {
+        constexpr uint32_t kFlip = 0x88888888u;  // code -> code + 8
+        uint32_t xw[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          xw[h][0] = *reinterpret_cast<const uint32_t*>(sp + va_off + h * 1024 + 4 * jj) ^ kFlip;
+          xw[h][1] = *reinterpret_cast<const uint32_t*>(sp + vb_off + h * 1024 + 4 * jj) ^ kFlip;
+          xw[h][2] = *reinterpret_cast<const uint32_t*>(sp + va_off + h * 1024 + 8 * kKvRowBytes + 4 * jj) ^ kFlip;
+          xw[h][3] = *reinterpret_cast<const uint32_t*>(sp + vb_off + h * 1024 + 8 * kKvRowBytes + 4 * jj) ^ kFlip;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
           const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-          const uint32_t y0 = __byte_perm(j < 2 ? x0.x : x0.y, j < 2 ? x1.x : x1.y, sel) ^ 0x88888888u;
-          const uint32_t y1 = __byte_perm(j < 2 ? x2.x : x2.y, j < 2 ? x3.x : x3.y, sel) ^ 0x88888888u;
-          const uint32_t z0 = y0 >> 8, z1 = y1 >> 8;
-          // dims 4 j (rows g, in units of 2^-24), 4 j + 1 (rows g + 8, 2^-20); 4 j + 2, 4 j + 3
-          const uint32_t a0 = codes_lo(y0), a1 = codes_hi(y0), a2 = codes_lo(y1), a3 = codes_hi(y1);
-          const uint32_t b0 = codes_lo(z0), b1 = codes_hi(z0), b2 = codes_lo(z1), b3 = codes_hi(z1);
+          const int t = 2 * (2 * jj + j);
+          float d[NT][2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t y0 = __byte_perm(xw[h][0], xw[h][1], sel);
+            const uint32_t y1 = __byte_perm(xw[h][2], xw[h][3], sel);
+            const uint32_t z0 = y0 >> 8, z1 = y1 >> 8;
+            const uint32_t a0 = codes_lo(y0), a1 = codes_hi(y0), a2 = codes_lo(y1), a3 = codes_hi(y1);
+            const uint32_t b0 = codes_lo(z0), b1 = codes_hi(z0), b2 = codes_lo(z1), b3 = codes_hi(z1);
+#pragma unroll
+            for (int nn = 0; nn < NT; ++nn) {
+              if (!TWICE) mma_f16(o[nn][t], a0, a1, a2, a3, w[h][kW - 1][nn][0], w[h][kW - 1][nn][1], o[nn][t]);
+              if (!TWICE) mma_f16(o[nn][t + 1], b0, b1, b2, b3, w[h][kW - 1][nn][0], w[h][kW - 1][nn][1], o[nn][t + 1]);
+              if (h == 0) {
+                mma_f16(d[nn][0], a0, a1, a2, a3, w[h][0][nn][0], w[h][0][nn][1], c8[nn]);
+                mma_f16(d[nn][1], b0, b1, b2, b3, w[h][0][nn][0], w[h][0][nn][1], c8[nn]);
+              } else {
+                mma_f16(d[nn][0], a0, a1, a2, a3, w[h][0][nn][0], w[h][0][nn][1], d[nn][0]);
+                mma_f16(d[nn][1], b0, b1, b2, b3, w[h][0][nn][0], w[h][0][nn][1], d[nn][1]);
+              }
+            }
+          }
 #pragma unroll
           for (int nn = 0; nn < NT; ++nn) {
-            float d[4];
-            if (!TWICE) mma_f16(o[nn][2 * j], a0, a1, a2, a3, w[kW - 1][nn][0], w[kW - 1][nn][1], o[nn][2 * j]);
-            mma_f16(d, a0, a1, a2, a3, w[0][nn][0], w[0][nn][1], c8[nn]);
-            add4(o[nn][2 * j], d);
-            if (!TWICE) mma_f16(o[nn][2 * j + 1], b0, b1, b2, b3, w[kW - 1][nn][0], w[kW - 1][nn][1], o[nn][2 * j + 1]);
-            mma_f16(d, b0, b1, b2, b3, w[0][nn][0], w[0][nn][1], c8[nn]);
-            add4(o[nn][2 * j + 1], d);
+            add4(o[nn][t], d[nn][0]);
+            add4(o[nn][t + 1], d[nn][1]);
           }
         }
       }

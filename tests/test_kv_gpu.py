@@ -12,9 +12,10 @@ Attention.  Per output, with p the exact weights and v the cached values:
 * a weight enters as two fp16 numbers (2^-22 relative), its two exponentials and
   products are float32 (16 * 2^-24 taken): (2^-22 + 2^-20) sum p|v|, and 2^-33 of the
   largest for each of n weights whose second number is subnormal: n 2^-33 max|v|;
-* the codes are summed as code + 8 and 8 sum(w) is taken off, 16 tokens at a
-  time: 17 terms below 16 w vs each, cut at 2^-23 of the largest, i.e. at most
-  17 * 16 * 2^-23 vs in all (the weights sum to 1), vs the largest V scale; the
+* the codes are summed as code + 8 and 8 sum(w) is taken off, 32 tokens at a
+  time in two products of 16 tokens: 2 * 17 terms of at most 16 (their weights' sum) vs
+  each, the sum so far among them, cut at 2^-23 of the largest, i.e. at most 34 * 16 * 2^-23 vs
+  in all (all weights sum to 1), vs the largest V scale; the
   float32 sums over n tokens add n 2^-24 sum p|v| at most;
 * the output's own rounding: 2^-11 |y|, and 2^-25 below fp16's normal range.
 On top of these worst cases the roundings of the output are independent, so the
@@ -269,7 +270,7 @@ def check_attn(y, q, lens, table, pool, scale, window=0):
     vs = KO.views(pool)[3].astype(np.float64)
     vmax = 8 * np.abs(vs[np.isfinite(vs)]).max()
     tol = (np.expm1(2 * ds)[..., None] + 2.0 ** -22 + 2.0 ** -20 + n * 2.0 ** -24) * sa
-    tol += (n * 2.0 ** -33 + 17 * 16 * 2.0 ** -23 / 8) * vmax + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25
+    tol += (n * 2.0 ** -33 + 34 * 16 * 2.0 ** -23 / 8) * vmax + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25
     err = np.abs(y - ref)
     assert np.isfinite(y).all()
     assert (err <= tol).all(), f"worst {np.max(err / tol):.3f} of the bound"
