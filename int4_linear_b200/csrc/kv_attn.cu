@@ -9,7 +9,7 @@
 // about 5.7 cycles per token and head, i.e. some 23 warp instructions; this kernel
 // executes 19, and with the four warps that a scheduler's registers hold issues in 54 % of the
 // cycles, waiting for products and their results: 64 requests of 8 heads and 14200
-// tokens on average (eight queries a head) take 211 us, 4.5 TB/s.
+// tokens on average (eight queries a head) take 206 us, 4.6 TB/s.
 //
 // Division.  The turns (32 tokens of one request and key-value head) of all
 // requests form one sequence, request-major; every CTA takes an equal contiguous
@@ -42,8 +42,8 @@
 //    every 16 tokens, attention took 2 to 6 % longer).
 // Weights: w = exp2(s - m) * (v scale / largest v scale so far) * 2^8 enters as two fp16 numbers, its
 // rounding and what that left (2^-22 relative, or 2^-33 of the largest where the second is
-// subnormal).  The rounding alone is 16 % faster on long caches (188 us for the 217 above), but leaves 1.5
-// times the error of the output's own rounding.  The second product adds to the running sums directly:
+// subnormal).  With the rounding alone an earlier version was 14 % faster on long caches (188 us instead of 217), but
+// left 1.5 times the error of the output's own rounding.  The second product adds to the running sums directly:
 // it is 2^-11 of them, and cutting a sum off at 2^-23 once per 16 tokens stays below the output's rounding
 // for parts of up to 65536 tokens per warp.
 // m is a reference that moves only when a score passes it by 2^7 (checked with one vote
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       if (uint32_t(ids.id[h]) < uint32_t(p.kv.num_pages)) {
         const uint32_t off = P16 ? 0 : (q.tok0 + i * kStep) & page_mask;
         const uint8_t* page = q.cache + static_cast<uint64_t>(uint32_t(ids.id[h])) * page_bytes;
-        const uint8_t* k = page + off * kKvRowBytes;
+        const uint8_t* k = page + static_cast<uint64_t>(off) * kKvRowBytes;
         const uint8_t* v = k + v_src;
         const uint32_t d = dst + h * 1024;
         copy16<0, 0>(d, k);
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
           copy16<kStepV + 1024, 1024>(d, v);
           copy16<kStepV + 1536, 1536>(d, v);
         }
-        if (lane < 2 * kScalePieces) copy16(dst + sc_dst + h * 32, page + (sc_src + 2 * int(off)));
+        if (lane < 2 * kScalePieces) copy16(dst + sc_dst + h * 32, page + static_cast<uint64_t>(off) * 2 + sc_src);
         got |= P16 ? 1u << h : 3u;
       }
     }
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
         }
       }
       const int at = seg.tok0 + i * kStep;
-      if (at < seg.lo || at + kStep > seg.hi || have != 3u) {
+      if (__builtin_expect(at < seg.lo || at + kStep > seg.hi || (P16 && have != 3u), 0)) {
         // what is masked scores -inf and weighs 0, whatever its scales hold
 #pragma unroll
         for (int h = 0; h < 2; ++h)
