@@ -504,6 +504,67 @@ def test_decode_steps_together():
     assert np.array_equal(table.cpu().numpy(), o_table) and np.array_equal(lens.cpu().numpy(), o_len)
 
 
+@pytest.mark.parametrize("fmt", [fq.MXFP4, fq.NVFP4])
+def test_layer_steps_eager_and_captured(fmt):
+    """A decode layer: microscaled projection to queries, keys and values, plan, write, attention over slices of the
+    projection's rows, output projection.  One captured step, replayed, against the same calls one by one, bit for bit,
+    and the attention against the oracle on the cache that the step left."""
+    g = rng(21, fmt)
+    r, h, hq, page, max_pages, width, steps = 7, 2, 6, 32, 5, 256, 40
+    wide = (hq + 2 * h) * 128
+    gx = None if fmt == fq.MXFP4 else torch.full((1,), 0.01, device="cuda")
+    w_in = fq.fq_mx_quant(dev((g.standard_normal((wide, width)) / 16).astype(np.float16)), fmt, gx)
+    w_out = fq.fq_mx_quant(dev((g.standard_normal((width, hq * 128)) / 16).astype(np.float16)), fmt, gx)
+    free = dev(g.permutation(r * max_pages).astype(np.int32))
+    new = torch.ones(r, dtype=torch.int32, device="cuda")
+    x = torch.zeros(r, width, dtype=torch.float16, device="cuda")
+    start = g.integers(0, 30, r).astype(np.int32)
+    start[2] = 0
+
+    class State:
+        def __init__(self):
+            self.cache = fq.kv_cache(r * max_pages, h, page)
+            self.lens, self.used = dev(start), torch.zeros(1, dtype=torch.int32, device="cuda")
+            self.table = torch.full((r, max_pages), -1, dtype=torch.int32, device="cuda")
+            # every request's first page, as its prompt's step would have left it
+            zero = torch.zeros(r, dtype=torch.int32, device="cuda")
+            fq.fq_kv_plan(zero, self.lens, self.table, free, self.used, page, 0, pages_used_out=self.used)
+            fq.fq_kv_plan(zero, self.lens, self.table, free, self.used, page, 30 * r, pages_used_out=self.used)
+            self.ws = fq.fq_kv_attn_workspace(r, hq, h)
+            self.ws_in = fq.fq_mx_linear_workspace(r, wide, width, fmt)
+            self.ws_out = fq.fq_mx_linear_workspace(r, width, hq * 128, fmt)
+
+        def step(self):
+            qkv = fq.fq_mx_linear(x, fmt, *w_in, gx, gx, workspace=self.ws_in)
+            q, k, v = qkv.split([hq * 128, h * 128, h * 128], dim=1)
+            _, _, slots, _ = fq.fq_kv_plan(self.lens, new, self.table, free, self.used, page, r, lens_out=self.lens,
+                                           pages_used_out=self.used)
+            fq.fq_kv_write(k, v, slots, self.cache)
+            y = fq.fq_kv_attn(q, self.lens, self.table, self.cache, workspace=self.ws)
+            return q, y, fq.fq_mx_linear(y, fmt, *w_out, gx, gx, workspace=self.ws_out)
+
+    eager, captured = State(), State()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            out = captured.step()
+    torch.cuda.synchronize()
+    for step in range(steps):
+        x.copy_(dev(g.standard_normal((r, width)).astype(np.float16)))
+        q, y, z = eager.step()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((q, y, z), out)), step
+        assert z.isfinite().all() and z.abs().max() > 0
+    fq.fq_check_device_error()
+    assert torch.equal(eager.cache.pool, captured.cache.pool) and torch.equal(eager.table, captured.table)
+    lens = eager.lens.cpu().numpy()
+    assert np.array_equal(lens, start + steps)
+    check_attn(y, q.cpu().numpy().reshape(r, hq, 128), lens, eager.table.cpu().numpy(), eager.cache.pool.cpu().numpy(),
+               128 ** -0.5)
+
+
 def test_workspace_shared_with_the_fused_linear():
     """The decode linear's one-launch form leaves a generation number in the counter block; attention
     and the block-scaled product on the same workspace are not disturbed."""
