@@ -327,7 +327,7 @@ typedef struct {
  * to and including it pass the free list: once that happens, no later request
  * that needs pages gets any either.  The sum of new_tokens must stay below 2^31, and
  * *pages_used must not be negative.
- * R in [1, 16384].  One launch, no workspace; the outputs must not overlap
+ * R in [1, 16384], max_tokens in [0, 2^30].  One launch, no workspace; the outputs must not overlap
  * the inputs except where stated. */
 fq_status fq_kv_plan(const int32_t* len, const int32_t* new_tokens, int R, int page_size, int32_t* block_table,
                      int max_pages, const int32_t* free_pages, int num_free, const int32_t* pages_used,
@@ -368,7 +368,7 @@ fq_status fq_kv_read(const fq_kv_cache* cache, const int32_t* slots, int T, uint
  *        request's tokens are not read; an entry outside [0, num_pages) leaves
  *        its tokens out.  What a page holds behind the last token (NaN scales too)
  *        has no effect.
- * Y      fp16 [R, Hq * 128] (16-byte aligned).
+ * Y      fp16 [R, Hq * 128] (16-byte aligned), apart from the inputs.
  * Hq a multiple of H, at most 1024; R in [1, 16384]; scale in [-65536, 65536].
  * A query head that holds an infinity or NaN gives NaN, the others keep their values.
  * Arithmetic: each query head is taken in 16-bit fixed point (half a step of max|q| / 32639
@@ -425,7 +425,7 @@ fq_status fq_mx_dequant(const uint8_t* Q, const uint8_t* S, int R, int K, fq_mx_
 /* Block-scaled product: Y fp16 [M, N] (16-byte aligned) = fp16(acc * (g_x * g_w)),
  * acc = sum over blocks of (s_x s_w sum of code products), in float32 on the
  * tensor cores; g_x, g_w device float32 [1] or NULL (1).  Xq [M, K/2], Wq [N, K/2] and their
- * scales as fq_mx_quant writes them.  M >= 1, N % 8 == 0, K a multiple of 128 in [128, 65536].
+ * scales as fq_mx_quant writes them.  M, N in [1, 2^30], N % 8 == 0, K a multiple of 128 in [128, 65536].
  * workspace: fq_mx_gemm_workspace_size() bytes, 256-byte aligned, by the rule of
  * fq_w4a4_gemm's workspace (may be NULL when that size is 0). */
 fq_status fq_mx_gemm(const uint8_t* Xq, const uint8_t* Sx, const float* g_x, const uint8_t* Wq, const uint8_t* Sw,

@@ -441,8 +441,8 @@ fq_status fq_kv_plan(const int32_t* len, const int32_t* new_tokens, int R, int p
                "page_size = %d must be 16, 32, 64 or 128", page_size);
   FQ_CHECK_ARG(max_pages >= 1 && static_cast<long long>(max_pages) * page_size < (1ll << 31),
                "max_pages = %d: at least 1, and fewer than 2^31 tokens", max_pages);
-  FQ_CHECK_ARG(num_free >= 0 && max_tokens >= 0, "num_free = %d and max_tokens = %d must not be negative", num_free,
-               max_tokens);
+  FQ_CHECK_ARG(num_free >= 0 && max_tokens >= 0 && max_tokens <= (1 << 30),
+               "num_free = %d must not be negative, max_tokens = %d lie in [0, 2^30]", num_free, max_tokens);
   FQ_CHECK_ARG(len && new_tokens && block_table && pages_used && len_out && token_start && pages_used_out &&
                    (free_pages || num_free == 0) && (slots || max_tokens == 0),
                "a pointer is NULL");

@@ -738,8 +738,10 @@ fq_status launch_mx_bn(const MxPlan& q, const MxGemmParams& p, const CUtensorMap
   }
 }
 
+constexpr int kMaxRows = 1 << 30;
+
 bool mx_sizes_ok(int M, int N, int K, fq_mx_format fmt) {
-  return M >= 1 && N >= 8 && N % 8 == 0 && K >= kGroup && K <= kMaxK && K % kGroup == 0 &&
+  return M >= 1 && M <= kMaxRows && N >= 8 && N <= kMaxRows && N % 8 == 0 && K >= kGroup && K <= kMaxK && K % kGroup == 0 &&
          (fmt == FQ_MXFP4 || fmt == FQ_NVFP4);
 }
 
@@ -772,7 +774,7 @@ fq_status fq_mx_gemm(const uint8_t* Xq, const uint8_t* Sx, const float* g_x, con
   if (fmt != FQ_MXFP4 && fmt != FQ_NVFP4)
     return fq::fail(FQ_ERR_UNSUPPORTED, "format %d is not provided", int(fmt));
   FQ_CHECK_ARG(fq::mx_sizes_ok(M, N, K, fmt),
-               "sizes M = %d, N = %d, K = %d: M >= 1, N a multiple of 8, K a multiple of 128 in [128, %d]", M, N, K,
+               "sizes M = %d, N = %d, K = %d: M and N in [1, 2^30], N a multiple of 8, K one of 128 in [128, %d]", M, N, K,
                fq::kMaxK);
   for (const void* q : {static_cast<const void*>(Xq), static_cast<const void*>(Sx), static_cast<const void*>(Wq),
                         static_cast<const void*>(Sw), static_cast<const void*>(Y)})
@@ -827,7 +829,7 @@ fq_status fq_mx_linear(const uint16_t* X, long long ldx, int M, int K, fq_mx_for
   if (fmt != FQ_MXFP4 && fmt != FQ_NVFP4)
     return fq::fail(FQ_ERR_UNSUPPORTED, "format %d is not provided", int(fmt));
   FQ_CHECK_ARG(fq::mx_sizes_ok(M, N, K, fmt),
-               "sizes M = %d, N = %d, K = %d: M >= 1, N a multiple of 8, K a multiple of 128 in [128, %d]", M, N, K,
+               "sizes M = %d, N = %d, K = %d: M and N in [1, 2^30], N a multiple of 8, K one of 128 in [128, %d]", M, N, K,
                fq::kMaxK);
   // everything the second launch checks, before the first
   FQ_CHECK_ARG(Wq && Sw && Y && fq::aligned(Wq, 16) && fq::aligned(Sw, 16) && fq::aligned(Y, 16),

@@ -98,7 +98,8 @@ def test_kv_attn_workspace_sizes(L):
 
 @pytest.mark.parametrize("change,msg", [
     (dict(R=0), b"R"), (dict(R=16385), b"R"), (dict(page=24), b"page_size"), (dict(max_pages=0), b"max_pages"),
-    (dict(num_free=-1), b"num_free"), (dict(max_tokens=-1), b"max_tokens"), (dict(len=None), b"NULL"),
+    (dict(num_free=-1), b"num_free"), (dict(max_tokens=-1), b"max_tokens"),
+    (dict(max_tokens=2 ** 30 + 1), b"max_tokens"), (dict(len=None), b"NULL"),
     (dict(free=None), b"NULL"), (dict(slots=None), b"NULL"), (dict(used_out=None), b"NULL"),
     (dict(slots=A + 2), b"aligned"), (dict(table=A + 1), b"aligned")])
 def test_kv_plan_refusals(L, change, msg):

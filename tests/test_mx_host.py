@@ -55,6 +55,15 @@ def test_product_and_linear_refusals(L, change, status, msg):
     assert st == status and msg in L.fq_last_error()
 
 
+@pytest.mark.parametrize("m,n", [(2 ** 31 - 1, 8), (2 ** 30 + 1, 8), (1, 2 ** 31 - 8), (1, 2 ** 30 + 8)])
+def test_sizes_past_the_tile_arithmetic_are_refused(L, m, n):
+    assert L.fq_mx_gemm_workspace_size(m, n, 128, 0) == 0 and L.fq_mx_linear_workspace_size(m, n, 128, 0) == 0
+    assert L.fq_mx_gemm(A, A, None, A, A, None, m, n, 128, 0, A, A, 1 << 20, None) == fq.FQ_ERR_INVALID
+    assert b"sizes" in L.fq_last_error()
+    assert L.fq_mx_linear(A, 128, m, 128, 0, None, A, A, None, n, A, A, 1 << 20, None) == fq.FQ_ERR_INVALID
+    assert b"sizes" in L.fq_last_error()
+
+
 def test_sizes(L):
     assert L.fq_mx_scale_bytes(1, 128, 0) == 128 * 4 and L.fq_mx_scale_bytes(129, 256, 1) == 256 * 16
     assert L.fq_mx_scale_bytes(0, 128, 0) == 0 and L.fq_mx_scale_bytes(1, 100, 0) == 0
