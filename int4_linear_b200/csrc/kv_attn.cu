@@ -9,7 +9,7 @@
 // about 5.7 cycles per token and head, i.e. some 23 warp instructions; this kernel
 // executes 19, and with the four warps that a scheduler's registers hold issues in 54 % of the
 // cycles, waiting for products and their results: 64 requests of 8 heads and 14200
-// tokens on average (eight queries a head) take 206 us, 4.6 TB/s.
+// tokens on average (eight queries a head) take 203 us, 4.7 TB/s.
 //
 // Division.  The turns (32 tokens of one request and key-value head) of all
 // requests form one sequence, request-major; every CTA takes an equal contiguous
@@ -66,12 +66,18 @@ constexpr int kStep = 32;           // tokens per turn, taken as two halves of 1
 constexpr int kStepV = kStep * kKvRowBytes, kStepKs = 2 * kStepV, kStepVs = kStepKs + 2 * kStep;
 constexpr int kStepBytes = kStepVs + 2 * kStep;  // K codes, V codes, K scales, V scales
 constexpr int kDepth = 2;           // turns of a warp in shared memory: one taken, one under way
-constexpr int kItemCost = 1;        // what a request and head costs besides its turns, in turns
+// What a request and head costs besides its turns, in turns.  With 1, 2, 3 and 4: 17 ragged requests of 32/8 heads to
+// 8192 tokens 29.2, 25.8, 26.0, 25.6 us, 48 of 16/16 heads to 4000 59.3, 54.0, 53.2, 53.3, one of 4000 tokens 13.9,
+// 13.7, 11.9, 12.2, 64 even ones of 64/8 heads and 14200 206.7, 208.6, 208.9, 209.4.
+constexpr int kItemCost = 3;
 // Little work: a part shorter than kMinUnits, or a request and head in more than kMaxParts parts, costs
-// more in the join than it saves; one of up to kWholeUnits (4 turns a warp) is not divided.  One request
-// of 8 heads and 4000 tokens took 14.2 us with parts of 8, 16.6 us with 24, 18.8 us with 40; one head of
-// 16384 tokens 17.5 us in 64 parts, 14.7 us in 32; 8 heads of 1000 tokens 12.3 us in 4 parts each, 11.4 us whole.
-constexpr int kMinUnits = 8, kMaxParts = 32, kWholeUnits = 36;
+// more in the join than it saves.  One request of 8 heads and 4000 tokens took 14.2 us with parts of 8, 16.6 us
+// with 24, 18.8 us with 40; one head of 16384 tokens 17.5 us in 64 parts, 14.7 us in 32.
+constexpr int kMinUnits = 8, kMaxParts = 32;
+// Where every request and head can have a CTA, none is divided unless the largest has kJoinUnits (the cost of the
+// join) more than an equal part.  33 requests of 40/8 heads and 1300 tokens took 22.3 us divided, 18.2 whole, of
+// 2048 28.0 and 24.5; 8 heads of 1000 tokens 11.9 and 11.4, of 4000 11.8 and 23.3; 33 of 0 to 2000 tokens 21.6 and 23.9.
+constexpr int kJoinUnits = 28;
 constexpr int kWarps = 8;
 constexpr int kAttnThreads = kWarps * 32;
 constexpr int kMaxAttnR = 16384;
@@ -98,6 +104,9 @@ struct AttnParams {
 struct AttnSmem {
   long long pre[kAttnThreads + 1];  // units of one head before each thread's run of requests
   long long wsum[kWarps];
+  int wmax[kWarps];
+  long long part[2], total;         // this CTA's units, all units
+  int ctas;                         // CTAs that share them
   // pieces of requests and heads: 0 a warp's first segment, if it continues an earlier warp's, 1 its last
   // one, if it is cut off.  item: the first unit of the request and head, -1: no piece
   long long item[kWarps][2];
@@ -296,17 +305,22 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   const int ra = min(p.R, tid * run), rb = min(p.R, ra + run);
   constexpr int kCountBit = 44;
   long long mine = 0;
+  int largest = 0;  // units of a request and head
   for (int r = ra; r < rb; ++r) {
     const Span s = span_of(p, r);
-    if (s.t1 > s.t0) mine += (s.t1 - s.t0) + kItemCost + (1ll << kCountBit);
+    if (s.t1 > s.t0) {
+      mine += (s.t1 - s.t0) + kItemCost + (1ll << kCountBit);
+      largest = max(largest, (s.t1 - s.t0) + kItemCost);
+    }
   }
+  largest = __reduce_max_sync(0xffffffffu, largest);
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long u = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += u;
   }
-  if (lane == 31) sm.wsum[warp] = incl;
+  if (lane == 31) sm.wsum[warp] = incl, sm.wmax[warp] = largest;
   if (lane < 2) sm.item[warp][lane] = -1;
   if (tid == 0) sm.ends = sm.join[0] = sm.join[1] = 0;
   __syncthreads();
@@ -315,13 +329,32 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) incl += sm.wsum[w];
     all += sm.wsum[w];
+    largest = max(largest, sm.wmax[w]);
   }
   constexpr long long kUnits = (1ll << kCountBit) - 1;
   sm.pre[tid] = (incl - mine) & kUnits;
   const long long total = (all & kUnits) * HC;
   const long long items = (all >> kCountBit) * HC;
-  const long long wanted = total <= items * kWholeUnits ? items : min(items * kMaxParts, total / kMinUnits);
-  const int C = int(min(static_cast<long long>(gridDim.x), max(wanted, items)));
+  int C = int(min(static_cast<long long>(gridDim.x), max(min(items * kMaxParts, total / kMinUnits), items)));
+  const bool whole = items <= gridDim.x && static_cast<long long>(largest - kJoinUnits) * C <= total;
+  if (whole) {
+    C = int(items);
+    // request number cta / HC of those with tokens, head cta % HC
+    int n = cta / HC - int((incl - mine) >> kCountBit);
+    if (n >= 0 && n < int(mine >> kCountBit)) {
+      long long before = sm.pre[tid];
+      for (int r = ra; r < rb; ++r) {
+        const Span s = span_of(p, r);
+        if (s.t1 == s.t0) continue;
+        const int units = s.t1 - s.t0 + kItemCost;
+        if (n-- == 0) {
+          sm.part[0] = before * HC + static_cast<long long>(cta % HC) * units;
+          sm.part[1] = sm.part[0] + units;
+        }
+        before += units;
+      }
+    }
+  }
   for (int r = cta; r < p.R; r += gridDim.x) {  // requests without tokens
     const Span s = span_of(p, r);
     if (s.t1 == s.t0)
@@ -329,11 +362,19 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
         reinterpret_cast<uint4*>(p.Y + static_cast<size_t>(r) * p.Hq * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
   }
   if (cta >= C) return;
+  if (tid == 0) {
+    if (!whole) {
+      sm.part[0] = divide(total * cta, C);
+      sm.part[1] = divide(total * (cta + 1), C);
+    }
+    sm.total = total;
+    sm.ctas = C;
+  }
   __syncthreads();
   // this CTA's part, this warp's part of it, and the request that one starts in
-  const long long first_c = divide(total * cta, C), last_c = divide(total * (cta + 1), C);
-  const long long first = first_c + (last_c - first_c) * warp / kWarps;
-  const long long last = first_c + (last_c - first_c) * (warp + 1) / kWarps;
+  const long long units = sm.part[1] - sm.part[0];
+  const long long first = sm.part[0] + units * warp / kWarps;
+  const long long last = sm.part[0] + units * (warp + 1) / kWarps;
   int wr;
   long long before;  // units before request wr
   {
@@ -801,7 +842,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   // by the first piece 0 when that continues an earlier CTA's; a warp takes one head of it.  Lane
   // 2 w + which knows of piece (w, which).
   const long long my_item = lane < 2 * kWarps ? sm.item[lane >> 1][lane & 1] : -1;
-  const bool from_before = (lane & 1) == 0 && my_item >= 0 && my_item + kItemCost < first_c;
+  const bool from_before = (lane & 1) == 0 && my_item >= 0 && my_item + kItemCost < sm.part[0];
   const uint32_t before_mask = __ballot_sync(0xffffffffu, from_before);
   // all pieces 0 from before are of one request and head: the first leads
   uint32_t leads = __ballot_sync(0xffffffffu, (lane & 1) && my_item >= 0) | (before_mask & -before_mask);
@@ -863,8 +904,8 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
     // counted, once every thread's share of the part is written
     const int lw = sm.left[tid];
     const long long t0 = sm.item[lw][tid] + kItemCost;
-    const int c_first = cta_of_unit(t0, total, C);
-    const int parts = cta_of_unit(t0 + sm.turns[lw][tid] - 1, total, C) - c_first + 1;
+    const int c_first = cta_of_unit(t0, sm.total, sm.ctas);
+    const int parts = cta_of_unit(t0 + sm.turns[lw][tid] - 1, sm.total, sm.ctas) - c_first + 1;
     __threadfence();
     sm.join[tid] = atomicInc(&p.count[c_first], unsigned(parts - 1)) == unsigned(parts - 1);
     sm.turns[lw][tid] = parts;

@@ -351,6 +351,18 @@ def test_attn_many_short_requests():
     check_attn(run_attn(*case), *case, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("longest", [400, 9000])
+@pytest.mark.parametrize("hq,h", [(2, 1), (12, 2)])
+def test_attn_few_requests_among_many_empty_slots(longest, hq, h):
+    """Every request and head whole on a CTA of its own, or, with a long one among them, divided."""
+    g = rng(15)
+    lens = np.zeros(3000, np.int64)
+    lens[g.permutation(3000)[:140]] = g.integers(200, 400, 140)
+    lens[g.integers(0, 3000)] = longest
+    case = attn_case(15, lens.tolist(), hq, h, 32)
+    check_attn(run_attn(*case), *case, 128 ** -0.5)
+
+
 def test_attn_value_scales_of_every_magnitude():
     """V scales over eight decades within a request: the running reference moves."""
     case = attn_case(6, [900, 333], 8, 2, 16, spread=1e4)
