@@ -101,6 +101,15 @@ struct AttnParams {
   unsigned* count;                  // one counter per CTA
 };
 
+// A warp's walk over its part, and the segment it is at: turns [ta, ta + turns) of the nt turns of a request
+// and key-value head's chunk of query heads.  Kept in shared memory, since the turns leave no register for it.
+struct WarpWalk {
+  long long pos, last;  // units still to be taken
+  long long before;     // units before request r
+  long long item0;      // the first unit of the segment's request and head
+  int next, r, head, chunk, nt, ta;
+};
+
 struct AttnSmem {
   long long pre[kAttnThreads + 1];  // units of one head before each thread's run of requests
   long long wsum[kWarps];
@@ -110,6 +119,7 @@ struct AttnSmem {
   // pieces of requests and heads: 0 a warp's first segment, if it continues an earlier warp's, 1 its last
   // one, if it is cut off.  item: the first unit of the request and head, -1: no piece
   long long item[kWarps][2];
+  WarpWalk walk[kWarps];
   int ends;                         // bit w: piece 0 of warp w reaches the end of its request
   int row[kWarps][2], heads[kWarps][2], turns[kWarps][2];  // its first row of Y, heads, turns of the whole
   float m[kWarps][2][16], l[kWarps][2][16];
@@ -373,15 +383,18 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   __syncthreads();
   // this CTA's part, this warp's part of it, and the request that one starts in
   const long long units = sm.part[1] - sm.part[0];
-  const long long first = sm.part[0] + units * warp / kWarps;
-  const long long last = sm.part[0] + units * (warp + 1) / kWarps;
-  int wr;
-  long long before;  // units before request wr
+  WarpWalk& walk = sm.walk[warp];
   {
+    const long long first = sm.part[0] + units * warp / kWarps;
     const int b8 = 8 * (__popc(__ballot_sync(0xffffffffu, sm.pre[8 * lane] * HC <= first)) - 1);
     const int t = b8 + __popc(__ballot_sync(0xffffffffu, lane < 8 && sm.pre[b8 + (lane & 7)] * HC <= first)) - 1;
-    wr = t * run;
-    before = sm.pre[t] * HC;
+    if (lane == 0) {
+      walk.pos = first;
+      walk.last = sm.part[0] + units * (warp + 1) / kWarps;
+      walk.next = t * run;
+      walk.before = sm.pre[t] * HC;
+    }
+    __syncwarp();
   }
 
   const int ps = p.kv.page_shift;
@@ -402,42 +415,42 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   const int k_off = row0 * kKvRowBytes + t4 * 16;
   const int va_off = kStepV + token_of_row(2 * t4) * kKvRowBytes + 8 * g;
   const int vb_off = kStepV + token_of_row(2 * t4 + 1) * kKvRowBytes + 8 * g;
-  // A segment: turns [ta, tb) of the nt turns of a request and head.
+  // The segment under way: its first token, turns, tokens, block table and cache.
   struct Seg {
-    int r, head, chunk, tok0, turns, nt, ta, lo, hi;  // key-value head, chunk of its query heads
-    long long item0;       // its request and head's first unit
-    const int32_t* row;    // its block table
+    int tok0, turns, lo, hi;
+    const int32_t* row;
     const uint8_t* cache;  // its head in page 0, this lane's 16 bytes of codes
   };
-  long long pos = first;
   auto next_segment = [&](Seg& q) {
-    while (pos < last) {
-      const Span s = span_of(p, wr);
+    WarpWalk k = walk;
+    __syncwarp();  // read by every lane
+    while (k.pos < k.last) {
+      const Span s = span_of(p, k.next);
       const int nt = s.t1 - s.t0, units = nt ? nt + kItemCost : 0;
       const long long len_r = static_cast<long long>(units) * HC;
-      if (pos >= before + len_r) {
-        before += len_r;
-        ++wr;
+      if (k.pos >= k.before + len_r) {
+        k.before += len_r;
+        ++k.next;
         continue;
       }
-      const int hc = int(divide(pos - before, units));
-      const long long item0 = before + static_cast<long long>(hc) * units;
-      const int ta = max(0, int(pos - item0) - kItemCost);
-      const int tb = int(min(static_cast<long long>(units), last - item0)) - kItemCost;
-      pos = min(item0 + units, last);
-      if (tb <= ta) continue;
-      q.r = wr;
-      q.head = p.chunks == 1 ? hc : hc / p.chunks;
-      q.chunk = hc - q.head * p.chunks;
-      q.row = p.table + static_cast<size_t>(wr) * p.max_pages;
-      q.cache = p.kv.block(0, q.head) + lane * 16;
-      q.item0 = item0;
-      q.nt = nt;
-      q.ta = ta;
-      q.turns = tb - ta;
+      const int hc = int(divide(k.pos - k.before, units));
+      k.item0 = k.before + static_cast<long long>(hc) * units;
+      k.ta = max(0, int(k.pos - k.item0) - kItemCost);
+      const int tb = int(min(static_cast<long long>(units), k.last - k.item0)) - kItemCost;
+      k.pos = min(k.item0 + units, k.last);
+      if (tb <= k.ta) continue;
+      k.r = k.next;
+      k.head = p.chunks == 1 ? hc : hc / p.chunks;
+      k.chunk = hc - k.head * p.chunks;
+      k.nt = nt;
+      if (lane == 0) walk = k;
+      __syncwarp();
+      q.turns = tb - k.ta;
       q.lo = s.lo;
       q.hi = s.hi;
-      q.tok0 = (s.t0 + ta) * kStep;
+      q.tok0 = (s.t0 + k.ta) * kStep;
+      q.row = p.table + static_cast<size_t>(k.r) * p.max_pages;
+      q.cache = p.kv.block(0, k.head) + lane * 16;
       return true;
     }
     return false;
@@ -486,13 +499,13 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
     return got;
   };
   // Query heads of a segment: heads [q0, q0 + heads)
-  auto first_head = [&](const Seg& q) { return q.head * p.G + q.chunk * HB; };
-  auto head_count = [&](const Seg& q) { return min(HB, p.G - q.chunk * HB); };
+  auto first_head = [&]() { return walk.head * p.G + walk.chunk * HB; };
+  auto head_count = [&]() { return min(HB, p.G - walk.chunk * HB); };
   const int col = TWICE ? g & 3 : g;
   uint4 raw[NT][4];  // lane (g, t4): the head of column g, dims [32 t4, 32 t4 + 32)
-  auto load_queries = [&](const Seg& q) {
-    const __half* src = p.Q + static_cast<long long>(q.r) * p.ldq + (first_head(q) + col) * kHeadDim + 32 * t4;
-    const int heads = head_count(q);
+  auto load_queries = [&]() {
+    const __half* src = p.Q + static_cast<long long>(walk.r) * p.ldq + (first_head() + col) * kHeadDim + 32 * t4;
+    const int heads = head_count();
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn)
 #pragma unroll
@@ -530,7 +543,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   auto piece = [&](int w, int which) {
     return which ? reinterpret_cast<float*>(dyn + w * kDepth * kStepBytes) : sums + w * NT * kPieceFloats;
   };
-  auto keep = [&](const Seg& q, int which) {
+  auto keep = [&](int which) {
     float* dst = piece(warp, which);
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn) {
@@ -546,10 +559,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
         }
     }
     if (lane == 0) {
-      sm.item[warp][which] = q.item0;
-      sm.row[warp][which] = q.r * p.Hq + first_head(q);
-      sm.heads[warp][which] = head_count(q);
-      sm.turns[warp][which] = q.nt;
+      sm.item[warp][which] = walk.item0;
+      sm.row[warp][which] = walk.r * p.Hq + first_head();
+      sm.heads[warp][which] = head_count();
+      sm.turns[warp][which] = walk.nt;
     }
   };
   auto write_heads = [&](int r, int q0, int heads) {
@@ -572,7 +585,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       }
   };
   while (next_segment(seg)) {
-    load_queries(seg);
+    load_queries();
     Ids next_ids = page_ids(seg, 0);
     // queries of this segment in 16-bit fixed point, two signed bytes: q = unit (256 hi + lo); the even
     // dims of 8 in one word, the odd ones in the next
@@ -822,12 +835,13 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[nn][k] += __shfl_xor_sync(0xffffffffu, l[nn][k], d);
-    const bool to_end = seg.ta + seg.turns == seg.nt;
+    const int ta = walk.ta;
+    const bool to_end = ta + seg.turns == walk.nt;
     in_units();
-    if (seg.ta == 0 && to_end) {
-      write_heads(seg.r, first_head(seg), head_count(seg));
-    } else if (seg.ta > 0) {
-      keep(seg, 0);
+    if (ta == 0 && to_end) {
+      write_heads(walk.r, first_head(), head_count());
+    } else if (ta > 0) {
+      keep(0);
       if (lane == 0 && to_end) atomicOr(&sm.ends, 1 << warp);
     } else {
       held = true;  // cut off: this warp's last segment, kept when its turns' bytes are free
@@ -835,7 +849,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   }
   copy_wait<0>();
   __syncwarp();
-  if (held) keep(seg, 1);
+  if (held) keep(1);
   __syncthreads();
 
   // ---- pieces of one request and head, added in the order of the warps.  A group is led by a piece 1, or
