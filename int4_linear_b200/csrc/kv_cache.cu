@@ -473,9 +473,11 @@ fq_status fq_kv_plan(const int32_t* len, const int32_t* new_tokens, int R, int p
     return fq::fail(FQ_ERR_CUDA, "cannot reserve %zu bytes of shared memory", smem);
   // more CTAs only where there are rows for them: the cluster barrier costs more than it saves below
   const unsigned ncta = max_tokens > 4 * fq::kPlanThreads ? 8 : 1;
-  if (fq::launch_pdl_cluster(fq::kv_plan_kernel, dim3(ncta), dim3(fq::kPlanThreads), smem,
-                             static_cast<cudaStream_t>(stream), ncta, p) != cudaSuccess)
-    return fq::check_launch("kv_plan_kernel");
+  if (ncta == 1)
+    fq::launch_pdl(fq::kv_plan_kernel, dim3(1), dim3(fq::kPlanThreads), smem, static_cast<cudaStream_t>(stream), p);
+  else
+    fq::launch_pdl_cluster(fq::kv_plan_kernel, dim3(ncta), dim3(fq::kPlanThreads), smem,
+                           static_cast<cudaStream_t>(stream), ncta, p);
   return fq::check_launch("kv_plan_kernel");
 }
 

@@ -230,7 +230,7 @@ def _on(stream, *tensors):
                 dev = d
             elif d != dev:
                 raise ValueError(f"the tensors lie on cuda:{dev} and cuda:{d}, not on one device")
-    if stream is None and dev == torch.cuda.current_device():
+    if stream is None and dev == torch._C._cuda_getDevice():
         return _On(torch._C._cuda_getCurrentRawStream(dev))
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
