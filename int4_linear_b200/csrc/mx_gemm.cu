@@ -51,6 +51,7 @@ struct MxGemmParams {
   const float *gx, *gw;
   int M, N, K;
   int mt, tiles, ks;       // token tiles, tiles, stages per tile
+  int full;                // tiles taken whole; each one after these as two halves of its tokens (256 on pairs only)
   int split;               // 1: equal parts of the (tile, stage) sequence
   float* part;             // [2 * CTAs][BN][128]
   unsigned* count;
@@ -251,35 +252,41 @@ struct MxStage {
   }
 };
 
-// This CTA's segments: (tile, stages [k0, k1)), the same sequence for every role.
+// This CTA's segments: (tile, half of its tokens or -1, stages [k0, k1)), the same sequence for every role.
 struct MxWalk {
   long long u, u1;
-  int ks, step, split;
-  int tile, k0, k1;
-  __device__ __forceinline__ MxWalk(const MxGemmParams& p, int cta, int ctas) : ks(p.ks), step(ctas), split(p.split) {
+  int ks, step, split, full, mt, M;
+  int tile, half, k0, k1;
+  __device__ __forceinline__ MxWalk(const MxGemmParams& p, int cta, int ctas)
+      : ks(p.ks), step(ctas), split(p.split), full(p.full), mt(p.mt), M(p.M), half(-1) {
     const long long total = static_cast<long long>(p.tiles) * p.ks;
     if (split) {
       u = total * cta / ctas;
       u1 = total * (cta + 1) / ctas;
     } else {
       u = cta;
-      u1 = p.tiles;
+      u1 = 2ll * p.tiles - full;
     }
   }
   __device__ __forceinline__ bool next() {
-    if (u >= u1) return false;
-    if (split) {
-      tile = int(u / ks);
-      k0 = int(u % ks);
-      k1 = int(min(static_cast<long long>(ks), k0 + (u1 - u)));
-      u += k1 - k0;
-    } else {
-      tile = int(u);
+    while (u < u1) {
+      if (split) {
+        tile = int(u / ks);
+        k0 = int(u % ks);
+        k1 = int(min(static_cast<long long>(ks), k0 + (u1 - u)));
+        u += k1 - k0;
+        return true;
+      }
+      const long long rest = u - full;
+      tile = int(rest < 0 ? u : full + (rest >> 1));
+      half = rest < 0 ? -1 : int(rest & 1);
       k0 = 0;
       k1 = ks;
       u += step;
+      if (half == 1 && tile % mt * 256 + 128 >= M) continue;  // no tokens there
+      return true;
     }
-    return true;
+    return false;
   }
 };
 
@@ -290,6 +297,7 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
                    const __grid_constant__ CUtensorMap tmSx, const __grid_constant__ CUtensorMap tmY) {
   using C = MxCfg<FMT, BN, PAIR>;
   constexpr int S = C::S;
+  constexpr bool HALVES = PAIR && BN == 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -371,7 +379,10 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
     bool ok = true;
     while (ok && walk.next()) {
       const int nt = walk.tile / p.mt * (PAIR ? 2 : 1) + int(rank), mt = walk.tile % p.mt;  // 128 rows, BN tokens
-      const int yw = nt * kTileN, yx = mt * BN + int(rank) * C::BROWS, ysx = mt * BN / kMxTileRows;
+      // of a half tile each CTA holds 64 rows (the box brings 64 more), and the half's scales come first
+      const bool half = HALVES && walk.half >= 0;
+      const int yw = nt * kTileN, yx = mt * BN + (half ? walk.half * 128 + int(rank) * 64 : int(rank) * C::BROWS);
+      const int ysx = mt * BN / kMxTileRows + (half ? walk.half : 0);
       for (int k = walk.k0; k < walk.k1; ++k, st.next(S)) {
         if (!warp_wait_phase<false>(&empty[st.s], st.phase ^ 1)) {
           ok = false;
@@ -412,7 +423,7 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
       };
       constexpr uint32_t kStep16 = (C::A_BYTES + C::B_BYTES) >> 4;  // a stage in the descriptors' 16-byte units
       const uint64_t a_desc = sdesc_k128_sw128(smem_u32(smem)), b_desc = sdesc_k128_sw128(smem_u32(smem) + C::A_BYTES);
-      constexpr uint32_t i0 = idesc_mx<FMT>(PAIR ? 256 : 128, BN, 0), i2 = idesc_mx<FMT>(PAIR ? 256 : 128, BN, 2);
+      constexpr int kRows = PAIR ? 256 : 128, kHalf = HALVES ? 128 : BN;
       const bool tail = p.K % kStageK != 0;  // 128 values in the last stage
       MxStage st;
       int seg = 0;
@@ -425,6 +436,9 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(buf * C::ACC);
+        const bool half_tile = HALVES && walk.half >= 0;
+        const uint32_t i0 = half_tile ? idesc_mx<FMT>(kRows, kHalf, 0) : idesc_mx<FMT>(kRows, BN, 0);
+        const uint32_t i2 = half_tile ? idesc_mx<FMT>(kRows, kHalf, 2) : idesc_mx<FMT>(kRows, BN, 2);
         for (int k = walk.k0; k < walk.k1; ++k, st.next(S)) {
           // the operands, then the scales, which came after them
           if (!warp_wait_phase<false>(&full[st.s], st.phase) || !warp_wait_phase<false>(&sf_full[st.s], st.phase)) {
@@ -590,7 +604,10 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
         release();  // before the outputs are on their way
         if (!bad) {
 #pragma unroll
-          for (int c = 0; c < BN; c += kStoreRows) emit(nt, mt, c, h + c / 2);
+          for (int c = 0; c < BN; c += kStoreRows) {
+            if (HALVES && c == 128 && walk.half >= 0) break;  // a half tile's columns end here
+            emit(nt, mt, (HALVES && walk.half > 0 ? 128 : 0) + c, h + c / 2);
+          }
         }
         continue;
       }
@@ -682,12 +699,14 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
 //    for 100 x 57344 x 2048 in NVFP4 17.7 / 17.0;
 //  - tiles of 128 or 256 tokens on pairs: 256 x 4096 x 4096 10.5 / 12.4, 777 x 5000 x 4224 19.4 / 23.8,
 //    1024 x 6144 x 4096 22.0 / 20.9, 2048 x 28672 x 4096 124 / 102: a tile of 256 takes 20 / 11 of one of 128;
+//  - a last round of tiles of 256 that leaves at least half of the pairs idle, whole or as halves of 128 tokens:
+//    1024 x 6144 x 4096 22.2 / 20.0, 4096 x 4096 x 4096 47.1 / 42, 2048 x 28672 x 4096 102 / 102 (bound by power);
 //  - divided or not: a stage of a lone tile takes 0.28 us and the join of a tile what 12 + BN / 4 stages take (the
 //    parts' way through memory, and their count on one CTA).  8 x 6144 x 4096 9.4 / 8.3, 8 x 28672 x 4096 14.4 / 13.9,
 //    8 x 57344 x 8192 40.1 / 42.4, 8 x 4096 x 14336 11.9 / 19.1, 64 x 6144 x 4096 13.0 / 9.4, 64 x 8192 x 28672
 //    27.1 / 37.8.
 struct MxPlan {
-  int bn, mt, tiles, ks, split, grid;
+  int bn, mt, tiles, full, ks, split, grid;
   bool pair;
 };
 
@@ -697,19 +716,24 @@ MxPlan mx_plan(int M, int N, int K) {
   q.ks = (K + kStageK - 1) / kStageK;
   q.pair = M > 64;
   const int workers = q.pair ? sms / 2 : sms;
+  int rest = 0;
   const int nt = (N + (q.pair ? 255 : 127)) / (q.pair ? 256 : 128);
   if (!q.pair) {
     q.bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
   } else {
     const long long t128 = static_cast<long long>(nt) * ((M + 127) / 128), t256 = static_cast<long long>(nt) * ((M + 255) / 256);
-    const long long w128 = (t128 + workers - 1) / workers, w256 = (t256 + workers - 1) / workers;
-    q.bn = w128 * 11 < w256 * 20 ? 128 : 256;
+    const long long w128 = (t128 + workers - 1) / workers, last = t256 % workers;
+    const bool halves = last > 0 && 2 * last <= workers;
+    const long long w256 = 20 * (t256 / workers) + (last == 0 ? 0 : halves ? 11 : 20);
+    q.bn = w128 * 11 <= w256 ? 128 : 256;
+    if (q.bn == 256 && halves) rest = int(last);
   }
   q.mt = (M + q.bn - 1) / q.bn;
   q.tiles = nt * q.mt;
+  q.full = q.tiles - rest;
   const long long units = static_cast<long long>(q.tiles) * q.ks, waves = (q.tiles + workers - 1) / workers;
   q.split = !q.pair && waves * q.ks > (units + workers - 1) / workers + 12 + q.bn / 4;
-  q.grid = int(std::min<long long>(workers, q.split ? units : q.tiles)) * (q.pair ? 2 : 1);
+  q.grid = int(std::min<long long>(workers, q.split ? units : q.tiles + rest)) * (q.pair ? 2 : 1);
   return q;
 }
 
@@ -813,6 +837,7 @@ fq_status fq_mx_gemm(const uint8_t* Xq, const uint8_t* Sx, const float* g_x, con
   p.K = K;
   p.mt = q.mt;
   p.tiles = q.tiles;
+  p.full = q.full;
   p.ks = q.ks;
   p.split = q.split;
   p.count = static_cast<unsigned*>(workspace) + fq::kJoinCounters;

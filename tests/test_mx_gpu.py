@@ -171,6 +171,14 @@ def test_product_divided_and_whole(fmt, m, n, k):
     test_product_wide_scales(fmt, m, n, k)
 
 
+# pairs: a last round of whole tiles, of half tiles, with a last token tile that has one half only, ragged in it
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m,n,k", [(1024, 6144, 384), (1000, 6400, 256), (850, 5000, 640), (1100, 5120, 128), (513, 6528, 384),
+                                   (1536, 3328, 512), (512, 14336, 128), (700, 19000, 256)])
+def test_product_last_round(fmt, m, n, k):
+    test_product_wide_scales(fmt, m, n, k)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("m,n,k", [(1, 512, 1024), (16, 1024, 2048), (77, 512, 640), (513, 768, 1024)])
 def test_linear(fmt, m, n, k):
