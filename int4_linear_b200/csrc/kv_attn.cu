@@ -7,9 +7,9 @@
 // against 4 * 128 operations per query head, so the work is a stream of pages
 // with the arithmetic hidden under it.  At the measured 6.55 TB/s an SM has
 // about 5.7 cycles per token and head, i.e. some 23 warp instructions; this kernel
-// executes 19, and with the four warps that a scheduler's registers hold issues in 54 % of the
+// executes 18, and with the four warps that a scheduler's registers hold issues in 54 % of the
 // cycles, waiting for products and their results: 64 requests of 8 heads and 14200
-// tokens on average (eight queries a head) take 203 us, 4.7 TB/s.
+// tokens on average (eight queries a head) take 201 us, 4.8 TB/s.
 //
 // Division.  The turns (32 tokens of one request and key-value head) of all
 // requests form one sequence, request-major; every CTA takes an equal contiguous
