@@ -213,14 +213,13 @@ constexpr int kRowThreads = 256;
 // v and s have 11 bits each, so v / s is a tie (k + 1/2) or at least 2^-12 from one.  v * inv, off by
 // less than 2^-18, is therefore first rounded to a multiple of 2^-13 (by adding 1.5 * 2^10), which makes a tie
 // exact and moves nothing else across one, then to an integer (by adding 1.5 * 2^23), ties to even:
-// two float32 operations where an IEEE division and its rounding take some fifteen.  Values past the clamp are
-// cut first, to 7.25 s and -8.25 s, which round to 7 and -8.
-__device__ __forceinline__ uint32_t codes8(const __half2 (&v)[4], __half2 top, __half2 bottom, float inv) {
+// two float32 operations where an IEEE division and its rounding take some fifteen.  Quotients lie in [-8.25, 7.25].
+__device__ __forceinline__ uint32_t codes8(const __half2 (&v)[4], float inv) {
   constexpr float kFine = 1536.0f, kWhole = 12582912.0f;
   uint32_t even[4], odd[4];  // codes in the low bits
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 f = __half22float2(__hmax2(__hmin2(v[j], top), bottom));
+    const float2 f = __half22float2(v[j]);
     const float2 a = ffma2(f, make_float2(inv, inv), make_float2(kFine, kFine));
     const float2 q = fadd2(a, make_float2(kWhole - kFine, kWhole - kFine));
     even[j] = __float_as_uint(q.x);
@@ -266,9 +265,9 @@ struct KvWalk {
 
 // One head vector per 8 lanes, each with the 8 values at 8 sub and at 64 + 8 sub (whole sectors per load and
 // store), two vectors per turn, read before their slots are known so that the loads overlap.  Bound by HBM
-// (256 bytes read, 66 written per vector) and, at 46 registers, by the 40 warps of an SM that ask for it: 16384
-// tokens of 8 heads 17.8 us, 4.7 TB/s, 65536 66 us, 5.1 TB/s; held to 32 registers it took a seventh longer, and
-// with a division per vector for its token a tenth.
+// (256 bytes read, 66 written per vector) and, at 58 registers, by the 32 warps of an SM that ask for it: 16384
+// tokens of 8 heads 16.5 us, 5.1 TB/s; with five or six CTAs per SM 17.1, with one or three vectors per turn 17.5 and
+// 17.1, with every value clamped 17.8, with a division per vector for its token 19.5.
 __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const __half* __restrict__ K, long long ldk,
                                                                const __half* __restrict__ V, long long ldv, int T,
                                                                const int32_t* __restrict__ slots, float alpha_k,
@@ -302,7 +301,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const __half* __r
     }
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
-      const __half2(&h2)[8] = reinterpret_cast<const __half2(&)[8]>(raw[u]);
+      __half2(&h2)[8] = reinterpret_cast<__half2(&)[8]>(raw[u]);
       __half2 m2 = __habs2(h2[0]);
 #pragma unroll
       for (int j = 1; j < 8; ++j) m2 = __hmax2(m2, __habs2(h2[j]));
@@ -310,12 +309,19 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const __half* __r
 #pragma unroll
       for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (slot[u] < 0 || slot[u] >= limit) continue;
-      const __half sh = __float2half_rn(__fdiv_rn(__fmul_rn(m, v[u].which ? alpha_v : alpha_k), 7.0f));
+      const float alpha = v[u].which ? alpha_v : alpha_k;
+      const __half sh = __float2half_rn(__fdiv_rn(__fmul_rn(m, alpha), 7.0f));
       const float s = __half2float(sh);
       const float inv = s > 0.f ? __fdividef(1.0f, s) : 0.f;  // s = 0: codes 0
-      const __half2 top = __float2half2_rn(7.25f * s), bottom = __float2half2_rn(-8.25f * s);
-      const uint32_t w0 = codes8(reinterpret_cast<const __half2(&)[4]>(h2[0]), top, bottom, inv);
-      const uint32_t w1 = codes8(reinterpret_cast<const __half2(&)[4]>(h2[4]), top, bottom, inv);
+      if (alpha < 1.0f || s < 0x1p-14f) {
+        // values may pass the clamp: cut to 7.25 s and -8.25 s, which round to 7 and -8 (otherwise s is the largest
+        // magnitude / 7, at most 2^-11 off, and none does)
+        const __half2 top = __float2half2_rn(7.25f * s), bottom = __float2half2_rn(-8.25f * s);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h2[j] = __hmax2(__hmin2(h2[j], top), bottom);
+      }
+      const uint32_t w0 = codes8(reinterpret_cast<const __half2(&)[4]>(h2[0]), inv);
+      const uint32_t w1 = codes8(reinterpret_cast<const __half2(&)[4]>(h2[4]), inv);
       uint8_t* page = c.block(slot[u] >> c.page_shift, v[u].h);
       const int off = slot[u] & ((1 << c.page_shift) - 1);
       uint32_t* row = reinterpret_cast<uint32_t*>(page + c.codes(v[u].which) + off * kKvRowBytes) + sub;
