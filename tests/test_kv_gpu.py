@@ -577,6 +577,28 @@ def test_layer_steps_eager_and_captured(fmt):
                128 ** -0.5)
 
 
+def test_two_streams_at_once():
+    """Attention and the microscaled linear on two streams, each with its own workspaces: the results of one alone."""
+    g = rng(22)
+    cases = [attn_case(22 + i, g.integers(1, 3000, 9).tolist(), 16, 2, 32) for i in range(2)]
+    x = dev(g.standard_normal((24, 2048)).astype(np.float16))
+    w = fq.fq_mx_quant(dev((g.standard_normal((1024, 2048)) / 32).astype(np.float16)), fq.MXFP4)
+    args = [tuple(map(dev, c[:3])) + (fq.KVCache(dev(c[3])),) for c in cases]
+    alone = [(fq.fq_kv_attn(*a), fq.fq_mx_linear(x, fq.MXFP4, *w)) for a in args]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [(fq.fq_kv_attn_workspace(9, 16, 2), fq.fq_mx_linear_workspace(24, 1024, 2048, fq.MXFP4)) for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(30):
+        for i, (a, s, ws) in enumerate(zip(args, streams, spaces)):
+            got[i].append((fq.fq_kv_attn(*a, workspace=ws[0], stream=s),
+                           fq.fq_mx_linear(x, fq.MXFP4, *w, workspace=ws[1], stream=s)))
+    torch.cuda.synchronize()
+    fq.fq_check_device_error()
+    for (y, z), outs in zip(alone, got):
+        assert all(torch.equal(y, a) and torch.equal(z, b) for a, b in outs)
+
+
 def test_workspace_shared_with_the_fused_linear():
     """The decode linear's one-launch form leaves a generation number in the counter block; attention
     and the block-scaled product on the same workspace are not disturbed."""
