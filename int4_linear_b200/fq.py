@@ -179,10 +179,13 @@ def _raise(status: int):
         raise FqError(status, f"{L.fq_status_string(status).decode()}: {L.fq_last_error().decode()}")
 
 
+_Tensor = torch.Tensor
+
+
 def _check(t, dtype, name):
     if t is None:
         return
-    if type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+    if t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous():
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -202,26 +205,23 @@ def _s(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-class _On:
-    """`with` block in which a device and a stream are current (see _on)."""
-    __slots__ = ("handle", "stack")
-
-    def __init__(self, handle, stack=None):
-        self.handle, self.stack = handle, stack
-
-    def __enter__(self):
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.stack is not None:
-            self.stack.close()
-        return False
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # None: a torch without CUDA
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _on(stream, *tensors):
+def _enter(stream, *tensors):
     """The device of `tensors` (all on one) made current and, where a stream is given, that
-    stream, so that what is allocated inside belongs to the stream that uses it.  Yields the
-    stream's handle.  The usual case, the current device and stream, enters nothing."""
+    stream, so that what is allocated meanwhile belongs to the stream that uses it.  Returns the stream's
+    handle and what the caller closes in the end: None in the usual case, the current device and stream,
+    where nothing is entered."""
+    if stream is None:
+        dev = tensors[0].get_device()
+        for t in tensors:
+            if t is not None and t.get_device() != dev:
+                break
+        else:
+            if dev == _current_device():
+                return _current_stream(dev), None
     dev = -1
     for t in tensors:
         if t is not None:
@@ -230,8 +230,6 @@ def _on(stream, *tensors):
                 dev = d
             elif d != dev:
                 raise ValueError(f"the tensors lie on cuda:{dev} and cuda:{d}, not on one device")
-    if stream is None and dev == torch._C._cuda_getDevice():
-        return _On(torch._C._cuda_getCurrentRawStream(dev))
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(stream, device=dev)
@@ -241,7 +239,7 @@ def _on(stream, *tensors):
     stack.enter_context(torch.cuda.device(dev))
     if stream is not None:
         stack.enter_context(torch.cuda.stream(stream))
-    return _On(torch._C._cuda_getCurrentRawStream(dev), stack)
+    return _current_stream(dev), stack
 
 
 def _check_shape(t, shape, name):
@@ -252,6 +250,15 @@ def _check_shape(t, shape, name):
 def _check_rows(t, name, width):
     """fp16 rows of `width` values, any distance apart: [T, width] or [T, H, 128] with dense rows.
     Returns (T, the distance in elements)."""
+    if t.__class__ is _Tensor and t.dtype is torch.float16 and t.is_cuda:  # the usual cases
+        shape = t.shape
+        n = len(shape)
+        if n == 2 and shape[1] == width and shape[0] > 1:
+            ld, one = t.stride()
+            if one == 1:
+                return shape[0], ld
+        elif n == 3 and shape[1] * shape[2] == width and shape[0] > 0 and t.is_contiguous():
+            return shape[0], width
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.float16:
@@ -453,8 +460,9 @@ def fq_kv_plan(lens, new_tokens, block_table, free_pages, pages_used, page_size:
                          f"{tuple(table_shape)}")
     _check_shape(new_tokens, (r,), "new_tokens")
     _check_shape(pages_used, (1,), "pages_used")
-    with _on(stream, lens, new_tokens, block_table, free_pages, pages_used, lens_out, token_start, slots,
-             pages_used_out) as s:
+    s, entered = _enter(stream, lens, new_tokens, block_table, free_pages, pages_used, lens_out, token_start, slots,
+                        pages_used_out)
+    try:
         if lens_out is None and token_start is None and slots is None and pages_used_out is None:
             # one allocation for the four
             lens_out, token_start, slots, pages_used_out = torch.unsafe_split_with_sizes(
@@ -472,6 +480,9 @@ def fq_kv_plan(lens, new_tokens, block_table, free_pages, pages_used, page_size:
                                 table_shape[1], free_pages.data_ptr() or None, free_pages.numel(),
                                 pages_used.data_ptr(), lens_out.data_ptr(), token_start.data_ptr(),
                                 slots.data_ptr() or None, max_tokens, pages_used_out.data_ptr(), s))
+    finally:
+        if entered is not None:
+            entered.close()
     return lens_out, token_start, slots, pages_used_out
 
 
@@ -489,9 +500,13 @@ def fq_kv_write(K, V, slots, cache: KVCache, alpha_k: float = 1.0, alpha_v: floa
     if tv != t:
         raise ValueError(f"K has {t} rows, V {tv}")
     _check_slots(slots, t)
-    with _on(stream, K, V, slots, cache.pool) as s:
+    s, entered = _enter(stream, K, V, slots, cache.pool)
+    try:
         _raise(lib().fq_kv_write(K.data_ptr(), ldk, V.data_ptr(), ldv, t, slots.data_ptr(), alpha_k, alpha_v,
                                  cache._ref, s))
+    finally:
+        if entered is not None:
+            entered.close()
 
 
 def fq_kv_store(Kq, Ks, Vq, Vs, slots, cache: KVCache, stream=None):
@@ -503,9 +518,13 @@ def fq_kv_store(Kq, Ks, Vq, Vs, slots, cache: KVCache, stream=None):
         _check(x, dt, name)
         _check_shape(x, (t, w), name)
     _check_slots(slots, t)
-    with _on(stream, Kq, Ks, Vq, Vs, slots, cache.pool) as s:
+    s, entered = _enter(stream, Kq, Ks, Vq, Vs, slots, cache.pool)
+    try:
         _raise(lib().fq_kv_store(Kq.data_ptr(), Ks.data_ptr(), Vq.data_ptr(), Vs.data_ptr(), t, slots.data_ptr(),
                                  cache._ref, s))
+    finally:
+        if entered is not None:
+            entered.close()
 
 
 def fq_kv_read(cache: KVCache, slots, K=None, V=None, stream=None):
@@ -513,16 +532,22 @@ def fq_kv_read(cache: KVCache, slots, K=None, V=None, stream=None):
     t = slots.numel()
     _check_slots(slots, t)
     shape = (t, cache.heads, 128)
-    with _on(stream, slots, cache.pool, K, V) as s:
-        for x, name in ((K, "K"), (V, "V")):
-            if x is not None:
-                _check(x, torch.float16, name)
-                _check_shape(x, shape, name)
+    s, entered = _enter(stream, slots, cache.pool, K, V)
+    try:
         if K is None:
             K = slots.new_empty(shape, dtype=torch.float16)
+        else:
+            _check(K, torch.float16, "K")
+            _check_shape(K, shape, "K")
         if V is None:
-            V = slots.new_empty(shape, dtype=torch.float16)
+            V = torch.empty_like(K)
+        else:
+            _check(V, torch.float16, "V")
+            _check_shape(V, shape, "V")
         _raise(lib().fq_kv_read(cache._ref, slots.data_ptr(), t, K.data_ptr(), V.data_ptr(), s))
+    finally:
+        if entered is not None:
+            entered.close()
     return K, V
 
 
@@ -553,7 +578,8 @@ def fq_kv_attn(Q, lens, block_table, cache: KVCache, scale: float | None = None,
     if rows != r or width < 128 or width % 128:
         raise ValueError(f"Q must have {r} rows of Hq * 128 values, got shape {tuple(q_shape)}")
     hq = width // 128
-    with _on(stream, Q, lens, block_table, cache.pool, Y, workspace) as s:
+    s, entered = _enter(stream, Q, lens, block_table, cache.pool, Y, workspace)
+    try:
         if Y is None:
             Y = Q.new_empty((r, width))
         else:
@@ -567,6 +593,9 @@ def fq_kv_attn(Q, lens, block_table, cache: KVCache, scale: float | None = None,
         _raise(lib().fq_kv_attn(Q.data_ptr(), ldq, r, hq, lens.data_ptr(), block_table.data_ptr(), table_shape[1],
                                 cache._ref, _HEAD_SCALE if scale is None else scale, window, Y.data_ptr(),
                                 workspace.data_ptr(), workspace.numel(), s))
+    finally:
+        if entered is not None:
+            entered.close()
     return Y
 
 
@@ -602,7 +631,8 @@ def fq_mx_quant(X, fmt: int, g=None, Q=None, S=None, stream=None):
     tiled scales).  fmt MXFP4 or NVFP4 (g: its float32 [1] tensor scale on the device, None: 1)."""
     r, k, ldx = _check_x(X, "X")
     _check_g(g, "g")
-    with _on(stream, X, g, Q, S) as s:
+    s, entered = _enter(stream, X, g, Q, S)
+    try:
         if Q is None:
             Q = X.new_empty((r, k // 2), dtype=torch.uint8)
         if S is None:
@@ -612,6 +642,9 @@ def fq_mx_quant(X, fmt: int, g=None, Q=None, S=None, stream=None):
         _check(Q, torch.uint8, "Q")
         _check_shape(Q, (r, k // 2), "Q")
         _raise(lib().fq_mx_quant(X.data_ptr(), ldx, r, k, fmt, _p(g), Q.data_ptr(), S.data_ptr() or None, s))
+    finally:
+        if entered is not None:
+            entered.close()
     return Q, S
 
 
@@ -619,13 +652,17 @@ def fq_mx_dequant(Q, S, fmt: int, g=None, X=None, stream=None):
     """Microscaled codes back to fp16 [R, K]."""
     r, k = _check_mx(Q, S, fmt, "X")
     _check_g(g, "g")
-    with _on(stream, Q, S, g, X) as s:
+    s, entered = _enter(stream, Q, S, g, X)
+    try:
         if X is None:
             X = Q.new_empty((r, k), dtype=torch.float16)
         else:
             _check(X, torch.float16, "X")
             _check_shape(X, (r, k), "X")
         _raise(lib().fq_mx_dequant(Q.data_ptr(), S.data_ptr(), r, k, fmt, _p(g), X.data_ptr(), s))
+    finally:
+        if entered is not None:
+            entered.close()
     return X
 
 
@@ -667,11 +704,15 @@ def fq_mx_gemm(Xq, Sx, Wq, Sw, fmt: int, g_x=None, g_w=None, Y=None, workspace=N
         raise ValueError(f"Xq has K = {k}, Wq {kw}")
     _check_g(g_x, "g_x")
     _check_g(g_w, "g_w")
-    with _on(stream, Xq, Sx, Wq, Sw, g_x, g_w, Y, workspace) as s:
+    s, entered = _enter(stream, Xq, Sx, Wq, Sw, g_x, g_w, Y, workspace)
+    try:
         Y = _mx_out(Xq, Y, m, n)
         ws, wsb = _workspace(fq_mx_gemm_workspace_size(m, n, k, fmt), Xq.device, workspace)
         _raise(lib().fq_mx_gemm(Xq.data_ptr(), Sx.data_ptr(), _p(g_x), Wq.data_ptr(), Sw.data_ptr(), _p(g_w), m, n, k,
                                 fmt, Y.data_ptr(), _p(ws), wsb, s))
+    finally:
+        if entered is not None:
+            entered.close()
     return Y
 
 
@@ -684,7 +725,8 @@ def fq_mx_linear(X, fmt: int, Wq, Sw, g_x=None, g_w=None, Y=None, workspace=None
         raise ValueError(f"X has K = {k}, Wq {kw}")
     _check_g(g_x, "g_x")
     _check_g(g_w, "g_w")
-    with _on(stream, X, Wq, Sw, g_x, g_w, Y, workspace) as s:
+    s, entered = _enter(stream, X, Wq, Sw, g_x, g_w, Y, workspace)
+    try:
         Y = _mx_out(X, Y, m, n)
         if workspace is None:
             workspace = fq_mx_linear_workspace(m, n, k, fmt, X.device)
@@ -692,6 +734,9 @@ def fq_mx_linear(X, fmt: int, Wq, Sw, g_x=None, g_w=None, Y=None, workspace=None
             _check(workspace, torch.uint8, "workspace")
         _raise(lib().fq_mx_linear(X.data_ptr(), ldx, m, k, fmt, _p(g_x), Wq.data_ptr(), Sw.data_ptr(), _p(g_w), n,
                                   Y.data_ptr(), workspace.data_ptr(), workspace.numel(), s))
+    finally:
+        if entered is not None:
+            entered.close()
     return Y
 
 
