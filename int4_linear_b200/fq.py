@@ -253,10 +253,10 @@ def _check_rows(t, name, width):
     if t.__class__ is _Tensor and t.dtype is torch.float16 and t.is_cuda:  # the usual cases
         shape = t.shape
         n = len(shape)
-        if n == 2 and shape[1] == width and shape[0] > 1:
+        if n == 2 and shape[1] == width and shape[0] > 0:
             ld, one = t.stride()
             if one == 1:
-                return shape[0], ld
+                return shape[0], ld if shape[0] > 1 else width
         elif n == 3 and shape[1] * shape[2] == width and shape[0] > 0 and t.is_contiguous():
             return shape[0], width
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -604,22 +604,26 @@ def fq_mx_scale_bytes(rows: int, k: int, fmt: int) -> int:
     return lib().fq_mx_scale_bytes(rows, k, fmt)
 
 
+_MX_NAMES = {"X": ("Xq", "Sx"), "W": ("Wq", "Sw")}
+
+
 def _check_mx(Q, S, fmt, name):
     """(rows, K) of microscaled codes Q [rows, K/2] with their tiled scales S."""
-    _check(Q, torch.uint8, name + "q")
-    _check(S, torch.uint8, "S" + name.lower())
+    codes, scales = _MX_NAMES[name]
+    _check(Q, torch.uint8, codes)
+    _check(S, torch.uint8, scales)
     shape = Q.shape
     if len(shape) != 2:
-        raise ValueError(f"{name}q must be [rows, K/2]")
+        raise ValueError(f"{codes} must be [rows, K/2]")
     rows, k = shape[0], 2 * shape[1]
     need = (rows + 127) // 128 * 128 * (k // (16 if fmt == NVFP4 else 32))
     if S.numel() != need:
-        raise ValueError(f"S{name.lower()} must hold {need} bytes, got {S.numel()}")
+        raise ValueError(f"{scales} must hold {need} bytes, got {S.numel()}")
     return rows, k
 
 
 def _check_x(X, name):
-    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+    if not isinstance(X, torch.Tensor) or len(X.shape) != 2:
         raise ValueError(f"{name} must be a CUDA tensor [rows, K]")
     k = X.shape[1]
     r, ldx = _check_rows(X, name, k)
