@@ -706,13 +706,13 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
 //    8 x 57344 x 8192 40.1 / 42.4, 8 x 4096 x 14336 11.9 / 19.1, 64 x 6144 x 4096 13.0 / 9.4, 64 x 8192 x 28672
 //    27.1 / 37.8.
 struct MxPlan {
-  int bn, mt, tiles, full, ks, split, grid;
+  int bn, mt, tiles, full, ks, split, grid, sms;
   bool pair;
 };
 
 MxPlan mx_plan(int M, int N, int K) {
   MxPlan q;
-  const int sms = sm_count();
+  const int sms = q.sms = sm_count();
   q.ks = (K + kStageK - 1) / kStageK;
   q.pair = M > 64;
   const int workers = q.pair ? sms / 2 : sms;
@@ -771,24 +771,76 @@ bool mx_sizes_ok(int M, int N, int K, fq_mx_format fmt) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+size_t mx_gemm_workspace(const MxPlan& q) {
+  if (q.pair) return 0;
+  // whether or not K is divided, so that the caller need not know
+  const long long ctas = std::min<long long>(q.sms, static_cast<long long>(q.tiles) * q.ks);
+  return sync_block_bytes() + size_t(2) * ctas * q.bn * kTileN * sizeof(float);
+}
+
+// The linear layer's workspace: the product's part, the tokens' codes, their scales.
+struct MxLinearLayout {
+  size_t codes, scales, bytes;
+  MxLinearLayout(const MxPlan& q, int M, int K, fq_mx_format fmt) {
+    codes = up256(std::max(sync_block_bytes(), mx_gemm_workspace(q)));
+    scales = codes + up256(size_t(M) * (K / 2));
+    bytes = scales + fq_mx_scale_bytes(M, K, fmt);
+  }
+};
+
+// The product by a plan of its sizes, all arguments but Xq's and Sx's checked.
+fq_status mx_gemm(const MxPlan& q, const uint8_t* Xq, const uint8_t* Sx, const float* g_x, const uint8_t* Wq,
+                  const uint8_t* Sw, const float* g_w, int M, int N, int K, fq_mx_format fmt, uint16_t* Y,
+                  void* workspace, void* stream) {
+  FQ_CHECK_ARG(static_cast<long long>((N + 127) / 128) * q.mt < (1ll << 31), "M = %d and N = %d: too many tiles", M, N);
+  unsigned* err = device_error_word();
+  if (!err) return fail(FQ_ERR_CUDA, "device error word unavailable");
+  // weights, tokens, their scales (rows of 128-row tiles, 8-byte words), outputs
+  CUtensorMap m[5];
+  const int sb = fmt == FQ_NVFP4 ? 4 : 2;
+  const uint64_t sw = uint64_t(K / mx_block(fmt) / kMxTileBlocks) * (kMxTileBytes / 8);
+  fq_status st = make_tmap_2d(&m[0], Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, N, K / 2, kRowB, kTileN,
+                              CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == FQ_OK)
+    st = make_tmap_2d(&m[1], Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, M, K / 2, kRowB,
+                      q.pair ? q.bn / 2 : q.bn, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st == FQ_OK)
+    st = make_tmap_2d(&m[2], Sw, CU_TENSOR_MAP_DATA_TYPE_INT64, sw, (N + 127) / 128, sw * 8, sb * 64, 1);
+  if (st == FQ_OK)
+    st = make_tmap_2d(&m[3], Sx, CU_TENSOR_MAP_DATA_TYPE_INT64, sw, (M + 127) / 128, sw * 8, sb * 64, 1);
+  if (st == FQ_OK)
+    st = make_tmap_2d(&m[4], Y, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, N, M, size_t(N) * 2, 32, kStoreRows,
+                      CU_TENSOR_MAP_SWIZZLE_64B);
+  if (st != FQ_OK) return st;
+  MxGemmParams p{};
+  p.gx = g_x;
+  p.gw = g_w;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.mt = q.mt;
+  p.tiles = q.tiles;
+  p.full = q.full;
+  p.ks = q.ks;
+  p.split = q.split;
+  p.count = static_cast<unsigned*>(workspace) + kJoinCounters;
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sync_block_bytes());
+  p.err = err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return fmt == FQ_MXFP4 ? launch_mx_bn<FQ_MXFP4>(q, p, m, s) : launch_mx_bn<FQ_NVFP4>(q, p, m, s);
+}
+
 }  // namespace
 }  // namespace fq
 
 extern "C" {
 
 size_t fq_mx_gemm_workspace_size(int M, int N, int K, fq_mx_format fmt) {
-  if (!fq::mx_sizes_ok(M, N, K, fmt)) return 0;
-  const fq::MxPlan q = fq::mx_plan(M, N, K);
-  if (q.pair) return 0;
-  // whether or not K is divided, so that the caller need not know
-  const long long ctas = std::min<long long>(fq::sm_count(), static_cast<long long>(q.tiles) * q.ks);
-  return fq::sync_block_bytes() + size_t(2) * ctas * q.bn * fq::kTileN * sizeof(float);
+  return fq::mx_sizes_ok(M, N, K, fmt) ? fq::mx_gemm_workspace(fq::mx_plan(M, N, K)) : 0;
 }
 
 size_t fq_mx_linear_workspace_size(int M, int N, int K, fq_mx_format fmt) {
-  if (!fq::mx_sizes_ok(M, N, K, fmt)) return 0;
-  return fq::up256(std::max(fq::sync_block_bytes(), fq_mx_gemm_workspace_size(M, N, K, fmt))) +
-         fq::up256(size_t(M) * (K / 2)) + fq_mx_scale_bytes(M, K, fmt);
+  return fq::mx_sizes_ok(M, N, K, fmt) ? fq::MxLinearLayout(fq::mx_plan(M, N, K), M, K, fmt).bytes : 0;
 }
 
 fq_status fq_mx_gemm(const uint8_t* Xq, const uint8_t* Sx, const float* g_x, const uint8_t* Wq, const uint8_t* Sw,
@@ -805,46 +857,11 @@ fq_status fq_mx_gemm(const uint8_t* Xq, const uint8_t* Sx, const float* g_x, con
     FQ_CHECK_ARG(q && fq::aligned(q, 16), "Xq, Sx, Wq, Sw and Y must be non-NULL and 16-byte aligned");
   FQ_CHECK_ARG(fq::aligned(g_x, 4) && fq::aligned(g_w, 4), "g_x and g_w must be 4-byte aligned");
   FQ_CHECK_ARG(fmt == FQ_NVFP4 || (!g_x && !g_w), "FQ_MXFP4 has no tensor scales: g_x and g_w must be NULL");
-  const size_t need = fq_mx_gemm_workspace_size(M, N, K, fmt);
+  const fq::MxPlan q = fq::mx_plan(M, N, K);
+  const size_t need = fq::mx_gemm_workspace(q);
   if (need && (!workspace || ws_bytes < need || !fq::aligned(workspace, 256)))
     return fq::fail(FQ_ERR_INVALID, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, ws_bytes);
-  const fq::MxPlan q = fq::mx_plan(M, N, K);
-  FQ_CHECK_ARG(static_cast<long long>((N + 127) / 128) * q.mt < (1ll << 31), "M = %d and N = %d: too many tiles", M, N);
-  unsigned* err = fq::device_error_word();
-  if (!err) return fq::fail(FQ_ERR_CUDA, "device error word unavailable");
-  // weights, tokens, their scales (rows of 128-row tiles, 8-byte words), outputs
-  CUtensorMap m[5];
-  const int sb = fmt == FQ_NVFP4 ? 4 : 2;
-  const uint64_t sw = uint64_t(K / fq::mx_block(fmt) / fq::kMxTileBlocks) * (fq::kMxTileBytes / 8);
-  fq_status st = fq::make_tmap_2d(&m[0], Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, N, K / 2, fq::kRowB, fq::kTileN,
-                                  CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st == FQ_OK)
-    st = fq::make_tmap_2d(&m[1], Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, K / 2, M, K / 2, fq::kRowB,
-                          q.pair ? q.bn / 2 : q.bn, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st == FQ_OK)
-    st = fq::make_tmap_2d(&m[2], Sw, CU_TENSOR_MAP_DATA_TYPE_INT64, sw, (N + 127) / 128, sw * 8, sb * 64, 1);
-  if (st == FQ_OK)
-    st = fq::make_tmap_2d(&m[3], Sx, CU_TENSOR_MAP_DATA_TYPE_INT64, sw, (M + 127) / 128, sw * 8, sb * 64, 1);
-  if (st == FQ_OK)
-    st = fq::make_tmap_2d(&m[4], Y, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, N, M, size_t(N) * 2, 32, fq::kStoreRows,
-                          CU_TENSOR_MAP_SWIZZLE_64B);
-  if (st != FQ_OK) return st;
-  fq::MxGemmParams p{};
-  p.gx = g_x;
-  p.gw = g_w;
-  p.M = M;
-  p.N = N;
-  p.K = K;
-  p.mt = q.mt;
-  p.tiles = q.tiles;
-  p.full = q.full;
-  p.ks = q.ks;
-  p.split = q.split;
-  p.count = static_cast<unsigned*>(workspace) + fq::kJoinCounters;
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + fq::sync_block_bytes());
-  p.err = err;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return fmt == FQ_MXFP4 ? fq::launch_mx_bn<FQ_MXFP4>(q, p, m, s) : fq::launch_mx_bn<FQ_NVFP4>(q, p, m, s);
+  return fq::mx_gemm(q, Xq, Sx, g_x, Wq, Sw, g_w, M, N, K, fmt, Y, workspace, stream);
 }
 
 fq_status fq_mx_linear(const uint16_t* X, long long ldx, int M, int K, fq_mx_format fmt, const float* g_x,
@@ -861,16 +878,14 @@ fq_status fq_mx_linear(const uint16_t* X, long long ldx, int M, int K, fq_mx_for
                "Wq, Sw and Y must be non-NULL and 16-byte aligned");
   FQ_CHECK_ARG(fq::aligned(g_x, 4) && fq::aligned(g_w, 4), "g_x and g_w must be 4-byte aligned");
   FQ_CHECK_ARG(fmt == FQ_NVFP4 || (!g_x && !g_w), "FQ_MXFP4 has no tensor scales: g_x and g_w must be NULL");
-  const size_t need = fq_mx_linear_workspace_size(M, N, K, fmt);
-  if (!workspace || ws_bytes < need || !fq::aligned(workspace, 256))
-    return fq::fail(FQ_ERR_INVALID, "workspace of %zu bytes (256-byte aligned) required, got %zu", need, ws_bytes);
+  const fq::MxPlan q = fq::mx_plan(M, N, K);
+  const fq::MxLinearLayout at(q, M, K, fmt);
+  if (!workspace || ws_bytes < at.bytes || !fq::aligned(workspace, 256))
+    return fq::fail(FQ_ERR_INVALID, "workspace of %zu bytes (256-byte aligned) required, got %zu", at.bytes, ws_bytes);
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  const size_t gws = fq::up256(std::max(fq::sync_block_bytes(), fq_mx_gemm_workspace_size(M, N, K, fmt)));
-  uint8_t* xq = base + gws;
-  uint8_t* sx = xq + fq::up256(size_t(M) * (K / 2));
-  const fq_status st = fq_mx_quant(X, ldx, M, K, fmt, g_x, xq, sx, stream);
+  const fq_status st = fq_mx_quant(X, ldx, M, K, fmt, g_x, base + at.codes, base + at.scales, stream);
   if (st != FQ_OK) return st;
-  return fq_mx_gemm(xq, sx, g_x, Wq, Sw, g_w, M, N, K, fmt, Y, base, gws, stream);
+  return fq::mx_gemm(q, base + at.codes, base + at.scales, g_x, Wq, Sw, g_w, M, N, K, fmt, Y, base, stream);
 }
 
 }  // extern "C"
