@@ -4,6 +4,7 @@ Usage: python -m int4_linear_b200.build   (or call build()).
 """
 from __future__ import annotations
 
+import fcntl
 import os
 import subprocess
 import sys
@@ -42,6 +43,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
+    # one process builds at a time; the others find its library (the lock goes with the file object)
+    with open(os.path.join(objdir, "lock"), "w") as lock:
+        fcntl.flock(lock, fcntl.LOCK_EX)
+        if force or _stale():
+            _build(objdir, force, verbose)
+    return LIB
+
+
+def _build(objdir: str, force: bool, verbose: bool) -> None:
     newest = max(os.path.getmtime(os.path.join(CSRC, h)) for h in HEADERS)
     objs = [os.path.join(objdir, s.replace(".cu", ".o")) for s in SOURCES]
 
@@ -49,10 +59,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         src, obj = os.path.join(CSRC, job[0]), job[1]
         if not force and os.path.exists(obj) and os.path.getmtime(obj) > max(newest, os.path.getmtime(src)):
             return
-        cmd = [_nvcc(), *NVCC_FLAGS, "-c", src, "-o", obj]
+        cmd = [_nvcc(), *NVCC_FLAGS, "-c", src, "-o", obj + ".tmp.o"]
         if verbose:
             print(" ".join(cmd))
         subprocess.run(cmd, check=True)
+        os.replace(obj + ".tmp.o", obj)  # an object that is there is whole
 
     with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as pool:
         list(pool.map(compile_one, zip(SOURCES, objs)))
@@ -62,7 +73,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
