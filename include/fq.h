@@ -371,8 +371,8 @@ fq_status fq_kv_read(const fq_kv_cache* cache, const int32_t* slots, int T, uint
  * Y      fp16 [R, Hq * 128] (16-byte aligned), apart from the inputs.
  * Hq a multiple of H, at most 1024; R in [1, 16384]; scale in [-65536, 65536].
  * A query head that holds an infinity or NaN gives NaN, the others keep their values.
- * Arithmetic: each query head is taken in 16-bit fixed point (half a step of max|q| / 32639
- * off), its products with the codes summed exactly; scores, softmax statistics and sums are
+ * Arithmetic: query values of at least 2^-11 of their head's largest enter exactly, smaller ones
+ * within 2^-22 of it, and their products with the codes are summed exactly; scores, softmax statistics and sums are
  * float32; the weights p_i * (v scale) enter the second product as two fp16 numbers (2^-22
  * relative).  The summation order is the kernel's, the same on every run for the
  * same sizes and lengths.

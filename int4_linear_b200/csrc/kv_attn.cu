@@ -28,12 +28,15 @@
 // G = Hq / H <= 16 of them per head, so its staging of operands would cost more than
 // the product.
 //  - scores: m16n8k32 in integers, A = 16 tokens x 128 dims of K codes (nibbles shifted to the
-//    top of a byte: 16 code, one logic operation per four), B = 8 queries in 16-bit fixed point of
-//    their head's largest value, as a high and a low signed byte.  The sums are exact, so the score is
-//    as good as the query: half a step of max|q| / 32639.  A lane reads 16 consecutive bytes of a
-//    token's row; the order of the dims inside the product is free, so the queries are arranged once
-//    per segment to match the nibbles.  An fp16 product with the constant of 64 + (code + 8) taken off afterwards
-//    was 6 % slower and left errors of 2^-15 of a logit.
+//    top of a byte: 16 code, one logic operation per four), B = 8 queries as whole multiples of 2^-22 of the
+//    power of two above their head's largest value, in three signed bytes: an fp16 value of at least 2^-11 of
+//    the largest is such a multiple, a smaller one is off by at most 2^-22 of the largest.  The sums are exact, so
+//    three float32 roundings are all else that a score has.  With two bytes (half a step of max|q| / 32639) long caches
+//    took 201 instead of 219 us, but a query channel 30 (100) times the others left errors of 1.4 to 1.8 (2.9 to 6.2) times
+//    the output's own rounding, scores of standard deviation 14 up to 1.19 times; now it is 1.0 everywhere.  Up to four query heads take the tile's other four columns for their
+//    second byte.  A lane reads 16 consecutive bytes of a token's row; the order of the dims inside the
+//    product is free, so the queries are arranged once per segment to match the nibbles.  An fp16 product with
+//    the constant of 64 + (code + 8) taken off afterwards left errors of 2^-15 of a logit.
 //  - sum: m16n8k16, A = 128 dims x 16 tokens of V codes (exact; a nibble u = code + 8 is the mantissa
 //    of a subnormal fp16, so an AND makes the operand, and one product with the constant -8
 //    starts the sums), B = the weights, taken from the scores' layout by movmatrix.  A lane reads 8 bytes of
@@ -85,6 +88,7 @@ constexpr float kSlack = 7.0f;      // log2 of how far a score may pass the refe
 constexpr float kLowest = -1e30f;   // the reference before the first score
 constexpr float kWeightScale = 256.0f;
 constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it leaves a rounded integer in the low bits
+constexpr int kRoundBits = 0x4B400000;
 
 struct AttnParams {
   const __half* Q;
@@ -166,12 +170,16 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The first product of a sum.
+// The first product of a sum, which starts from kRound's bits: below 2^22 in magnitude, the sum is then a float32 number's
+// mantissa, and whole_numbers() takes it out without a conversion.
 __device__ __forceinline__ void mma_s8_first(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(kRoundBits));
+}
+__device__ __forceinline__ float2 whole_numbers(int a, int b) {
+  return fadd2(make_float2(__int_as_float(a), __int_as_float(b)), make_float2(-kRound, -kRound));
 }
 
 __device__ __forceinline__ void add4(float (&a)[4], const float (&b)[4]) {
@@ -514,6 +522,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
                                         : make_uint4(0, 0, 0, 0);
   };
 
+  constexpr int kQ = TWICE ? 2 : 3;  // products per 32 dims of a score
   Seg seg;
   int slot = 0;         // ring slot of the turn to be taken
   float o[NT][8][4];
@@ -587,9 +596,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   while (next_segment(seg)) {
     load_queries();
     Ids next_ids = page_ids(seg, 0);
-    // queries of this segment in 16-bit fixed point, two signed bytes: q = unit (256 hi + lo); the even
-    // dims of 8 in one word, the odd ones in the next
-    uint32_t qf[NT][2][8];
+    // queries of this segment in units of 2^(E-22), 2^E the power of two above the head's largest value, as three
+    // signed bytes: q = unit (65536 hi + 256 mid + lo), |hi| <= 64; the even dims of 8 in one word, the odd ones in
+    // the next.  TWICE: columns 0-3 of the first product hold hi and columns 4-7 mid, of the second lo and 0.
+    uint32_t qf[NT][kQ][8];
     float unit[NT][2];  // of heads 2 t4, 2 t4 + 1, times the score's scale and 1/16 (a nibble is taken 16-fold)
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn) {
@@ -603,26 +613,38 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       uint32_t mb = __float_as_uint(__half2float(__hmax_nan(__low2half(m2), __high2half(m2))));
       mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));  // of numbers without sign, NaN the largest
       mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
-      const float mq = __uint_as_float(mb);
-      const float inv = mq > 0.f ? 32639.0f / mq : 0.f;
+      // the largest value is 0 or has the float32 exponent mb >> 23 in [103, 142] (fp16's range); E = (mb >> 23) - 126
+      const bool finite = mb < 0x7F800000u;
+      const float inv = mb && finite ? __uint_as_float((275u - (mb >> 23)) << 23) : 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const __half2* h2 = reinterpret_cast<const __half2*>(&raw[nn][j]);
-        uint32_t ev[4], od[4];  // round(q inv) + 128 in the low 16 bits
+        uint32_t ev[4], od[4];  // round(q inv) + 128 * 256 + 128
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = __half22float2(h2[k]);
-          ev[k] = __float_as_uint(__fmaf_rn(f.x, inv, kRound + 128.0f));
-          od[k] = __float_as_uint(__fmaf_rn(f.y, inv, kRound + 128.0f));
+          ev[k] = __float_as_uint(__fmaf_rn(f.x, inv, kRound)) - uint32_t(kRoundBits - 32896);
+          od[k] = __float_as_uint(__fmaf_rn(f.y, inv, kRound)) - uint32_t(kRoundBits - 32896);
         }
-        // byte 1 is hi; byte 0 is lo + 128
-        qf[nn][0][2 * j] = bytes4(ev, 0x5151u);
-        qf[nn][0][2 * j + 1] = bytes4(od, 0x5151u);
-        qf[nn][1][2 * j] = bytes4(ev, 0x4040u) ^ 0x80808080u;
-        qf[nn][1][2 * j + 1] = bytes4(od, 0x4040u) ^ 0x80808080u;
+        // byte 2 is hi; byte 1 is mid + 128, byte 0 lo + 128
+        if (TWICE) {
+          const bool upper = g < 4;
+          const uint32_t sel = upper ? 0x6262u : 0x5151u, flip = upper ? 0u : 0x80808080u;
+          qf[nn][0][2 * j] = bytes4(ev, sel) ^ flip;
+          qf[nn][0][2 * j + 1] = bytes4(od, sel) ^ flip;
+          qf[nn][1][2 * j] = upper ? bytes4(ev, 0x4040u) ^ 0x80808080u : 0u;
+          qf[nn][1][2 * j + 1] = upper ? bytes4(od, 0x4040u) ^ 0x80808080u : 0u;
+        } else {
+          qf[nn][0][2 * j] = bytes4(ev, 0x6262u);
+          qf[nn][0][2 * j + 1] = bytes4(od, 0x6262u);
+          qf[nn][1][2 * j] = bytes4(ev, 0x5151u) ^ 0x80808080u;
+          qf[nn][1][2 * j + 1] = bytes4(od, 0x5151u) ^ 0x80808080u;
+          qf[nn][kQ - 1][2 * j] = bytes4(ev, 0x4040u) ^ 0x80808080u;
+          qf[nn][kQ - 1][2 * j + 1] = bytes4(od, 0x4040u) ^ 0x80808080u;
+        }
       }
-      // a head with an infinity or NaN is NaN
-      const float u = mq <= 65504.0f ? mq * (p.scale_log2 / (16.0f * 32639.0f)) : NAN;
+      // 2^(E-22) scale / 16; a head with an infinity or NaN is NaN
+      const float u = !finite ? NAN : mb ? __uint_as_float(((mb >> 23) - 21u) << 23) * (p.scale_log2 / 16.0f) : 0.f;
       unit[nn][0] = __shfl_sync(0xffffffffu, u, 8 * t4);
       unit[nn][1] = __shfl_sync(0xffffffffu, u, 8 * t4 + 4);
     }
@@ -658,27 +680,40 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
         const uint4 k0 = *reinterpret_cast<const uint4*>(sp + k_off + h * 1024);
         const uint4 k1 = *reinterpret_cast<const uint4*>(sp + k_off + h * 1024 + 8 * kKvRowBytes);
         const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
-        int ah[NT][4], al[NT][4];
+        int a[NT][kQ][4];  // sums of the products with hi, mid and lo
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t e0, d0, e1, d1;  // 16 q of the even and odd dims of rows g and g + 8
           unpack8_hi(kw0[j], e0, d0);
           unpack8_hi(kw1[j], e1, d1);
 #pragma unroll
-          for (int nn = 0; nn < NT; ++nn) {
-            if (j == 0) {
-              mma_s8_first(ah[nn], e0, e1, d0, d1, qf[nn][0][0], qf[nn][0][1]);
-              mma_s8_first(al[nn], e0, e1, d0, d1, qf[nn][1][0], qf[nn][1][1]);
-            } else {
-              mma_s8(ah[nn], e0, e1, d0, d1, qf[nn][0][2 * j], qf[nn][0][2 * j + 1]);
-              mma_s8(al[nn], e0, e1, d0, d1, qf[nn][1][2 * j], qf[nn][1][2 * j + 1]);
+          for (int nn = 0; nn < NT; ++nn)
+#pragma unroll
+            for (int b = 0; b < kQ; ++b) {
+              if (j == 0)
+                mma_s8_first(a[nn][b], e0, e1, d0, d1, qf[nn][b][0], qf[nn][b][1]);
+              else
+                mma_s8(a[nn][b], e0, e1, d0, d1, qf[nn][b][2 * j], qf[nn][b][2 * j + 1]);
             }
-          }
         }
 #pragma unroll
         for (int nn = 0; nn < NT; ++nn)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sc[h][nn][k] = float(ah[nn][k] * 256 + al[nn][k]) * unit[nn][k & 1];
+          for (int k = 0; k < 4; k += 2) {
+            const float2 c256 = make_float2(256.0f, 256.0f);
+            float2 s = whole_numbers(a[nn][0][k], a[nn][0][k + 1]);
+            if (TWICE) {  // 65536 hi + lo, and 256 mid of the same heads four columns on
+              const float c = t4 < 2 ? 65536.0f : 256.0f;
+              s = ffma2(s, make_float2(c, c), whole_numbers(a[nn][1][k], a[nn][1][k + 1]));
+              s = fadd2(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, 2), __shfl_xor_sync(0xffffffffu, s.y, 2)));
+            } else {
+              s = ffma2(s, c256, whole_numbers(a[nn][1][k], a[nn][1][k + 1]));
+              s = ffma2(s, c256, whole_numbers(a[nn][kQ - 1][k], a[nn][kQ - 1][k + 1]));
+            }
+            s = fmul2(s, make_float2(unit[nn][0], unit[nn][1]));
+            sc[h][nn][k] = s.x;
+            sc[h][nn][k + 1] = s.y;
+          }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           ks[h][k] = __half2float(*reinterpret_cast<const __half*>(sp + kStepKs + 2 * (row0 + 16 * h + 8 * k)));

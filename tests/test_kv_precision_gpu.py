@@ -1,0 +1,56 @@
+"""Decode attention's error against that of its output's own rounding.
+
+The root mean square of y - (float64 result) is compared with the rounding of that
+result to fp16, which no kernel can avoid.  What the kernel's arithmetic adds is
+independent of it, so an addition of up to 0.4 of it leaves the sum within
+sqrt(1 + 0.4^2) < 1.1 of the rounding alone.
+"""
+import numpy as np
+import pytest
+import torch
+
+from int4_linear_b200 import fq
+from oracle import kv_oracle as KO
+from tests.test_kv_gpu import attn_case, run_attn
+
+pytestmark = pytest.mark.gpu
+
+HEADS = [(8, 2), (12, 2), (32, 2)]   # up to 4, up to 8, more query heads per key-value head
+
+
+def error_over_rounding(y, ref):
+    """rms(y - ref) over rms(fp16(ref) - ref)."""
+    d = y.cpu().numpy().astype(np.float64).reshape(ref.shape) - ref
+    r = ref.astype(np.float16).astype(np.float64) - ref
+    assert np.isfinite(d).all()
+    return np.sqrt((d ** 2).mean() / (r ** 2).mean())
+
+
+@pytest.mark.parametrize("hq,h", HEADS)
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("outlier", [1, 30, 100])
+def test_queries_with_an_outlier_channel(hq, h, page, outlier):
+    """A query channel `outlier` times the others' size, which the keys hardly use.  Values of at least 2^-11 of a
+    head's largest enter exactly, smaller ones within 2^-22 of it (evenly spread: rms 2^-22 / sqrt(3)).  With codes of rms
+    sqrt((8^2 + ... + 7^2) / 16) = 4.64, K scales of rms 0.25, scale 128^-0.5 and a largest value of at most 4.5 x 100, all
+    128 channels among the smaller ones, a score is off by 450 2^-22 / sqrt(3) sqrt(128) 4.64 0.25 / sqrt(128) = 7.2e-5
+    (rms), each weight by that much of itself, and the output of independent values by that much of its own size: 0.35 of
+    the rounding of fp16 numbers (2^-11 / sqrt(3) of the power of two below them, i.e. over 0.73 of 2^-11 / sqrt(3) =
+    2.05e-4 of them).  The float32 roundings of a score are below 2^-21 of its terms."""
+    q, lens, table, pool = attn_case(31, [1000, 77, 4000], hq, h, page)
+    q[..., 6] *= np.float16(outlier)
+    if outlier > 1:
+        kq, _, _, _ = KO.views(pool)
+        kq[..., 3] &= 0xF0                       # channel 6: code 0
+    ref = KO.attention(q, lens, table, pool, 128 ** -0.5)[0]
+    assert error_over_rounding(run_attn(q, lens, table, pool), ref) <= 1.1
+
+
+@pytest.mark.parametrize("hq,h", HEADS)
+def test_scores_that_spread_widely(hq, h):
+    """Ordinary heads whose scores have a standard deviation of about 14.  Queries: 54 2^-22 / sqrt(3) of at most
+    4.64 0.25 sqrt(128) / sqrt(128) each, 9e-6; a score of up to 90 (in powers of two) is rounded three times and once
+    less its reference, 4 x 90 x 2^-24 / sqrt(3) = 1.3e-5: below 0.1 of the output's rounding."""
+    q, lens, table, pool = attn_case(32, [2000, 300, 5000], hq, h, 32, qstd=12.0)
+    ref = KO.attention(q, lens, table, pool, 128 ** -0.5)[0]
+    assert error_over_rounding(run_attn(q, lens, table, pool), ref) <= 1.1
