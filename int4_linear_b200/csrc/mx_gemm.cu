@@ -404,12 +404,12 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
         sent = min(sent + 1, S);
       }
     }
-    // every copy has landed before the CTA may leave: the last `sent` stages, oldest first
-    if (rank == 0)
-      for (int i = 0; ok && i < sent; ++i) {
-        const int back = sent - i, s = st.s - back < 0 ? st.s - back + S : st.s - back;
-        ok = warp_wait_phase<false>(&full[s], st.s - back < 0 ? st.phase ^ 1 : st.phase);
-      }
+    // Before the CTA may leave, every copy has landed and the products' arrival for it, which a pair's even CTA
+    // sends to both, has come: the last `sent` stages, oldest first.
+    for (int i = 0; ok && i < sent; ++i) {
+      const int back = sent - i, s = st.s - back < 0 ? st.s - back + S : st.s - back;
+      ok = warp_wait_phase<false>(&empty[s], st.s - back < 0 ? st.phase ^ 1 : st.phase);
+    }
     if (!ok && leader) record_error(p.err, kErrTimeoutProducer);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
@@ -467,6 +467,10 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
       if (leader) commit(done);
       ok = warp_wait_phase<false>(done, 0) && ok;
       if (!ok && leader) record_error(p.err, kErrTimeoutMma);
+    } else if (!warp_wait_phase<false>(done, 0) && lane == 0) {
+      // the odd CTA stays until the products, which read its shared and tensor memory, are done and their
+      // last arrival has come here too
+      record_error(p.err, kErrTimeoutMma);
     }
   } else if (warp == 2 || warp == 3) {
     // ------------------------------------------------------------ scales to tensor memory, every other tile each
@@ -679,7 +683,8 @@ __global__ void __launch_bounds__(kMxGemmThreads, 1)
   }
   __syncwarp();
   tc_fence_before();
-  // a pair: neither CTA leaves while the other may still signal it or read its operands
+  // a pair: neither CTA leaves while the other's threads may still signal it (what its tensor core sends and
+  // reads has been waited for above)
   if (PAIR)
     cluster_sync();
   else
