@@ -33,10 +33,11 @@
 //    the largest is such a multiple, a smaller one is off by at most 2^-22 of the largest.  The sums are exact, so
 //    three float32 roundings are all else that a score has.  With two bytes (half a step of max|q| / 32639) long caches
 //    took 201 instead of 219 us, but a query channel 30 (100) times the others left errors of 1.4 to 1.8 (2.9 to 6.2) times
-//    the output's own rounding, scores of standard deviation 14 up to 1.19 times; now it is 1.0 everywhere.  Up to four query heads take the tile's other four columns for their
-//    second byte.  A lane reads 16 consecutive bytes of a token's row; the order of the dims inside the
-//    product is free, so the queries are arranged once per segment to match the nibbles.  An fp16 product with
-//    the constant of 64 + (code + 8) taken off afterwards left errors of 2^-15 of a logit.
+//    the output's own rounding, scores of standard deviation 14 up to 1.19 times; now it is 1.0 everywhere.  Up to
+//    four query heads take the tile's other four columns for their second byte.  A lane reads 16 consecutive bytes
+//    of a token's row; the order of the dims inside the product is free, so the queries are arranged once per
+//    segment to match the nibbles.  An fp16 product with the constant of 64 + (code + 8) taken off afterwards left
+//    errors of 2^-15 of a logit.
 //  - sum: m16n8k16, A = 128 dims x 16 tokens of V codes (exact; a nibble u = code + 8 is the mantissa
 //    of a subnormal fp16, so an AND makes the operand, and one product with the constant -8
 //    starts the sums), B = the weights, taken from the scores' layout by movmatrix.  A lane reads 8 bytes of
@@ -46,9 +47,9 @@
 // Weights: w = exp2(s - m) * (v scale / largest v scale so far) * 2^8 enters as two fp16 numbers, its
 // rounding and what that left (2^-22 relative, or 2^-33 of the largest where the second is
 // subnormal).  With the rounding alone an earlier version was 14 % faster on long caches (188 us instead of 217), but
-// left 1.5 times the error of the output's own rounding.  The second product adds to the running sums directly:
-// it is 2^-11 of them, and cutting a sum off at 2^-23 once per 16 tokens stays below the output's rounding
-// for parts of up to 65536 tokens per warp.
+// left 1.5 times the error of the output's own rounding.  The second product joins the turn's sums: added to the running
+// ones directly, whose sum it cuts off at 2^-23 once per 16 tokens, it took 2 % less time, but a warp's part of 227
+// thousand tokens came out 8e-5 too small, and longer ones by more.
 // m is a reference that moves only when a score passes it by 2^7 (checked with one vote
 // per 32 tokens), so the sums are rarely rescaled.
 #include <cuda_fp16.h>
@@ -844,14 +845,16 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
             const uint32_t b0 = codes_lo(z0), b1 = codes_hi(z0), b2 = codes_lo(z1), b3 = codes_hi(z1);
 #pragma unroll
             for (int nn = 0; nn < NT; ++nn) {
-              if (!TWICE) mma_f16(o[nn][t], a0, a1, a2, a3, w[h][kW - 1][nn][0], w[h][kW - 1][nn][1], o[nn][t]);
-              if (!TWICE) mma_f16(o[nn][t + 1], b0, b1, b2, b3, w[h][kW - 1][nn][0], w[h][kW - 1][nn][1], o[nn][t + 1]);
               if (h == 0) {
                 mma_f16(d[nn][0], a0, a1, a2, a3, w[h][0][nn][0], w[h][0][nn][1], c8[nn]);
                 mma_f16(d[nn][1], b0, b1, b2, b3, w[h][0][nn][0], w[h][0][nn][1], c8[nn]);
               } else {
                 mma_f16(d[nn][0], a0, a1, a2, a3, w[h][0][nn][0], w[h][0][nn][1], d[nn][0]);
                 mma_f16(d[nn][1], b0, b1, b2, b3, w[h][0][nn][0], w[h][0][nn][1], d[nn][1]);
+              }
+              if (!TWICE) {
+                mma_f16(d[nn][0], a0, a1, a2, a3, w[h][kW - 1][nn][0], w[h][kW - 1][nn][1], d[nn][0]);
+                mma_f16(d[nn][1], b0, b1, b2, b3, w[h][kW - 1][nn][0], w[h][kW - 1][nn][1], d[nn][1]);
               }
             }
           }

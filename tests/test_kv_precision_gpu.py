@@ -54,3 +54,28 @@ def test_scores_that_spread_widely(hq, h):
     q, lens, table, pool = attn_case(32, [2000, 300, 5000], hq, h, 32, qstd=12.0)
     ref = KO.attention(q, lens, table, pool, 128 ** -0.5)[0]
     assert error_over_rounding(run_attn(q, lens, table, pool), ref) <= 1.1
+
+
+@pytest.mark.parametrize("hq,h", [(32, 8), (64, 8), (128, 8)])
+def test_long_parts_have_no_bias(hq, h):
+    """512 requests of 131072 tokens and 8 heads: some 227 thousand tokens (up to 8 query heads; twice that with more) for
+    each of the GPU's warps.  All tables name the same 64 pages again and again, so that the result is that of one round of
+    them.  Values are positive, so cutting sums off instead of rounding them would make every output smaller.
+    The mean of a request's outputs, relative to theirs: n = 14188 (twice that) rounded additions of a softmax
+    sum in each of the 8 lanes that share a head, 2^-24 / sqrt(3) each (rms), the same in every round of 512 different ones,
+    are n 2^-24 / (sqrt(3) sqrt(512)) of a lane's sum and that over sqrt(8 hq) in the mean (an output's own sums take half as many,
+    and 128 outputs a head: less than a sixth of it); the outputs' roundings are 2^-11 / sqrt(3) at most over
+    sqrt(128 hq).  Four times both."""
+    page, pages, r, n = 128, 64, 512, 131072
+    q, lens, table, pool = attn_case(33, [pages * page], hq, h, page)
+    _, vq, _, _ = KO.views(pool)
+    vq &= 0x77                                   # codes 0 to 7
+    ref = KO.attention(q, lens, table, pool, 128 ** -0.5)[0]
+    period = table[0, :pages]
+    long_table = np.tile(period, (r, n // (pages * page)))
+    y = run_attn(np.repeat(q, r, 0), np.full(r, n, np.int32), long_table, pool)
+    y = y.cpu().numpy().astype(np.float64).reshape(r, hq, 128)
+    bias = (y - ref).mean((1, 2)) / ref.mean()
+    adds = 14188 * (2 if hq > 64 else 1)
+    sums = adds * 2.0 ** -24 * np.sqrt(512 / 3) / 512 / np.sqrt(8 * hq) * 7 / 6
+    assert np.abs(bias).max() <= 4 * (sums + 2.0 ** -11 / np.sqrt(3) / np.sqrt(128 * hq))
