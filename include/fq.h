@@ -373,8 +373,8 @@ fq_status fq_kv_read(const fq_kv_cache* cache, const int32_t* slots, int T, uint
  * A query head that holds an infinity or NaN gives NaN, the others keep their values.
  * Arithmetic: query values of at least 2^-11 of their head's largest enter exactly, smaller ones
  * within 2^-22 of it, and their products with the codes are summed exactly; scores, softmax statistics and sums are
- * float32; the weights p_i * (v scale) enter the second product as two fp16 numbers (2^-22
- * relative).  The summation order is the kernel's, the same on every run for the
+ * float32; the weights p_i * (v scale) enter the second product as two fp16 numbers, within 2^-22
+ * of themselves or 2^-33 of the head's largest one, whichever is more.  The summation order is the kernel's, the same on every run for the
  * same sizes and lengths.
  * workspace / ws_bytes: fq_kv_attn_workspace_size(R, Hq, H) bytes, 256-byte
  *   aligned, whose first FQ_WORKSPACE_SYNC_BYTES follow the rule of

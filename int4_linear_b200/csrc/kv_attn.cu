@@ -44,13 +44,15 @@
 //    each of its 4 tokens and pairs two tokens' nibbles by byte permutation.  A turn's 32
 //    tokens are added up in the tensor core, whose adds cut off; the running sums are rounded float32 adds (added after
 //    every 16 tokens, attention took 2 to 6 % longer).
-// Weights: w = exp2(s - m) * (v scale / largest v scale so far) * 2^8 enters as two fp16 numbers, its
-// rounding and what that left (2^-22 relative, or 2^-33 of the largest where the second is
-// subnormal).  With the rounding alone an earlier version was 14 % faster on long caches (188 us instead of 217), but
+// Weights: w = exp2(s - m) * (v scale), times 2^8 over the head's largest w so far, enters as two fp16 numbers, its
+// rounding and what that left (2^-22 relative, or 2^-33 of that largest where the second is
+// subnormal).  Taken relative to the largest v scale instead, they were lost beside a token of no weight with a much
+// larger v scale: errors of 1.05, 5, 21 and 170 times the output's own rounding at 2^14, 2^18, 2^20 and 2^23 times
+// theirs, at the same speed.  With the rounding alone an earlier version was 14 % faster on long caches (188 us instead of 217), but
 // left 1.5 times the error of the output's own rounding.  The second product joins the turn's sums: added to the running
 // ones directly, whose sum it cuts off at 2^-23 once per 16 tokens, it took 2 % less time, but a warp's part of 227
 // thousand tokens came out 8e-5 too small, and longer ones by more.
-// m is a reference that moves only when a score passes it by 2^7 (checked with one vote
+// m and the largest w are references that move only when a weight passes one by 2^7 (checked with one vote
 // per 32 tokens), so the sums are rarely rescaled.
 #include <cuda_fp16.h>
 
@@ -85,9 +87,10 @@ constexpr int kJoinUnits = 28;
 constexpr int kWarps = 8;
 constexpr int kAttnThreads = kWarps * 32;
 constexpr int kMaxAttnR = 16384;
-constexpr float kSlack = 7.0f;      // log2 of how far a score may pass the reference
+constexpr float kSlack = 128.0f;    // how far a weight may pass its reference
 constexpr float kLowest = -1e30f;   // the reference before the first score
 constexpr float kWeightScale = 256.0f;
+constexpr float kLeastWeight = 0x1p-100f;  // largest weights below this count as this: far from any that an output shows
 constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it leaves a rounded integer in the low bits
 constexpr int kRoundBits = 0x4B400000;
 
@@ -528,20 +531,21 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   int slot = 0;         // ring slot of the turn to be taken
   float o[NT][8][4];
   float m[NT][2], l[NT][2];
-  float vcap = 0.f, vinv = 0.f;  // largest v scale so far, and 2^8 over it
+  float winv[NT][2];             // 2^8 over the largest weight p * (v scale) so far
   bool held = false;             // the last segment is cut off and stays in registers
   static_assert(NT * kPieceFloats * 4 <= kDepth * kStepBytes, "a piece fits a warp's turns");
-  auto in_units = [&]() {  // rows g hold 2^-24, rows g + 8 2^-20 of the sums, both over 2^8 / vcap
-    const float f = vcap * (1.0f / kWeightScale);
+  auto in_units = [&]() {  // rows g hold 2^-24, rows g + 8 2^-20 of the sums, both times winv
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int k = 0; k < 2; ++k) {
+        const float f = 1.0f / winv[nn][k];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int i = 0; i < 8; ++i) {
           o[nn][i][k] *= f * 0x1p24f;
           o[nn][i][k + 2] *= f * 0x1p20f;
         }
+      }
     if (TWICE) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -649,7 +653,6 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       unit[nn][0] = __shfl_sync(0xffffffffu, u, 8 * t4);
       unit[nn][1] = __shfl_sync(0xffffffffu, u, 8 * t4 + 4);
     }
-    vcap = vinv = 0.f;
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn) {
 #pragma unroll
@@ -658,6 +661,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
         for (int k = 0; k < 4; ++k) o[nn][i][k] = 0.f;
       m[nn][0] = m[nn][1] = kLowest;
       l[nn][0] = l[nn][1] = 0.f;
+      winv[nn][0] = winv[nn][1] = kWeightScale / kLeastWeight;
     }
 
     uint32_t coming = 0;  // halves of the turn under way
@@ -739,28 +743,29 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
             }
           }
       }
-      // log2 of the weights before the v scale, and whether one passes its reference by too much
-      const float vtop = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
-      float x[2][NT][4], top = -INFINITY;
+      // log2 of the weights before the v scale, and whether one of them passes its reference, or a weight the largest
+      // so far, by too much: 2^top > 2^7 or 2^top vtop winv > 2^15, in one comparison (vtop and top may be of
+      // two tokens of the lane, so this asks a little early)
+      const float vtop = fmaxf(fmaxf(fabsf(vs[0][0]), fabsf(vs[0][1])), fmaxf(fabsf(vs[1][0]), fabsf(vs[1][1])));
+      float x[2][NT][4], far = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int nn = 0; nn < NT; ++nn)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              x[h][nn][2 * i + k] = __fmaf_rn(sc[h][nn][2 * i + k], ks[h][i], -m[nn][k]);
+              top = fmaxf(top, x[h][nn][2 * i + k]);
+            }
+          far = fmaxf(far, exp2_approx(top) * fmaxf(vtop * winv[nn][k], kWeightScale));
+        }
+      if (__any_sync(0xffffffffu, far > kWeightScale * kSlack)) {
+        // new references: the largest score of each head, the largest weight
 #pragma unroll
         for (int nn = 0; nn < NT; ++nn)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[h][nn][k] = __fmaf_rn(sc[h][nn][k], ks[h][k >> 1], -m[nn][k & 1]);
-            top = fmaxf(top, x[h][nn][k]);
-          }
-      if (__any_sync(0xffffffffu, top > kSlack || vtop > vcap)) {
-        // new references: the largest score of each head, the largest v scale
-        float vm = fmaxf(vtop, vcap);
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, d));
-        const float vf = vm > 0.f ? vcap / vm : 0.f;
-        vcap = vm;
-        vinv = vm > 0.f ? kWeightScale / vm : 0.f;
-#pragma unroll
-        for (int nn = 0; nn < NT; ++nn) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float mx = m[nn][k];
@@ -771,33 +776,42 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
             for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
             const float f = exp2_approx(m[nn][k] - mx);
             m[nn][k] = mx;
+            float wm = kLeastWeight;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              x[h][nn][k] = __fmaf_rn(sc[h][nn][k], ks[h][0], -mx);
-              x[h][nn][k + 2] = __fmaf_rn(sc[h][nn][k + 2], ks[h][1], -mx);
-            }
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                x[h][nn][2 * i + k] = __fmaf_rn(sc[h][nn][2 * i + k], ks[h][i], -mx);
+                wm = fmaxf(wm, exp2_approx(x[h][nn][2 * i + k]) * fabsf(vs[h][i]));
+              }
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, d));
+            // the largest weight so far, by the new reference
+            wm = fmaxf(wm, f * (kWeightScale / winv[nn][k]));
+            const float wi = kWeightScale / wm, fw = f * (wi / winv[nn][k]);
+            winv[nn][k] = wi;
             l[nn][k] *= f;
 #pragma unroll
             for (int i8 = 0; i8 < 8; ++i8) {
-              o[nn][i8][k] *= f * vf;
-              o[nn][i8][k + 2] *= f * vf;
+              o[nn][i8][k] *= fw;
+              o[nn][i8][k + 2] *= fw;
             }
           }
-        }
       }
       constexpr int kW = TWICE ? 1 : 2;
       uint32_t w[2][kW][NT][2];  // of both halves: weights and what their rounding left, as operands
       float c8[NT][4];  // -8 sum(w): rows g in the units of codes_lo, rows g + 8 of codes_hi
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float v0 = vs[h][0] * vinv, v1 = vs[h][1] * vinv;
 #pragma unroll
         for (int nn = 0; nn < NT; ++nn) {
           const float p0 = exp2_approx(x[h][nn][0]), p1 = exp2_approx(x[h][nn][1]);
           const float p2 = exp2_approx(x[h][nn][2]), p3 = exp2_approx(x[h][nn][3]);
           l[nn][0] += p0 + p2;
           l[nn][1] += p1 + p3;
-          const float2 wa = make_float2(p0 * v0, p1 * v0), wb = make_float2(p2 * v1, p3 * v1);
+          const float2 wi = make_float2(winv[nn][0], winv[nn][1]);
+          const float2 wa = fmul2(make_float2(p0, p1), fmul2(make_float2(vs[h][0], vs[h][0]), wi));
+          const float2 wb = fmul2(make_float2(p2, p3), fmul2(make_float2(vs[h][1], vs[h][1]), wi));
           __half2 a = __float22half2_rn(wa), b = __float22half2_rn(wb);
           const float2 ra = __half22float2(a), rb = __half22float2(b);
           const float take = TWICE && t4 < 2 ? 0.f : 1.f;  // columns 0-3 keep the weight itself

@@ -79,3 +79,34 @@ def test_long_parts_have_no_bias(hq, h):
     adds = 14188 * (2 if hq > 64 else 1)
     sums = adds * 2.0 ** -24 * np.sqrt(512 / 3) / 512 / np.sqrt(8 * hq) * 7 / 6
     assert np.abs(bias).max() <= 4 * (sums + 2.0 ** -11 / np.sqrt(3) / np.sqrt(128 * hq))
+
+
+def large_value_scale(hq, h, page, at, log2_ratio):
+    """A case whose requests hold one token, number `at`, with a V scale of 2^15, 2^log2_ratio times the most that the others
+    have, and a score some 85 below them (query channel 6 is 30, and only that token's key uses it): its weight times its
+    scale is 2^-107, nothing beside theirs."""
+    q, lens, table, pool = attn_case(34, [40, 700, 33], hq, h, page)
+    q[..., 6] = 30
+    kq, _, ks, vs = KO.views(pool)
+    kq[..., 3] &= 0xF0
+    vs *= np.float16(2.0 ** (13 - log2_ratio))   # from 0.05 .. 0.4 to below 2^(15 - log2_ratio)
+    for i, n in enumerate(lens):
+        t = at % n
+        pg, off = table[i, t // page], t % page
+        kq[pg, :, off] = 0
+        kq[pg, :, off, 3] = 8                    # code -8
+        ks[pg, :, off] = 4.0
+        vs[pg, :, off] = 2.0 ** 15
+    return q, lens, table, pool
+
+
+@pytest.mark.parametrize("hq,h", HEADS)
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("at", [0, 20, -1])
+@pytest.mark.parametrize("log2_ratio", [14, 18, 20, 23])
+def test_one_large_value_scale_without_weight(hq, h, page, at, log2_ratio):
+    """The weights of the other tokens are within 2^-22 of themselves, or 2^-33 of the largest p times (v scale)."""
+    q, lens, table, pool = large_value_scale(hq, h, page, at, log2_ratio)
+    ref = KO.attention(q, lens, table, pool, 128 ** -0.5)[0]
+    assert np.sqrt((ref ** 2).mean()) > 2.0 ** -13   # fp16's normal range
+    assert error_over_rounding(run_attn(q, lens, table, pool), ref) <= 1.1
