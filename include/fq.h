@@ -339,7 +339,8 @@ fq_status fq_kv_plan(const int32_t* len, const int32_t* new_tokens, int R, int p
  * that slices of one projection's output are taken as they are.  Each head
  * vector is quantized as by fq_quant_kv without a transform: s = fp16((max|v|
  * alpha) / 7), codes clamp(round(v / s), -8, 7), and goes to slots[t] (int32
- * [T]); rows whose slot is no place are skipped.  K and V hold finite values.  The slots
+ * [T]); rows whose slot is no place are skipped.  A head vector that holds
+ * an infinity or NaN gets a NaN scale (0x7FFF; its codes have no meaning), so that what reads it is NaN.  The slots
  * of one call must differ, else a shared slot may hold a mix of its rows.  One launch. */
 fq_status fq_kv_write(const uint16_t* K, long long ldk, const uint16_t* V, long long ldv, int T,
                       const int32_t* slots, float alpha_k, float alpha_v, const fq_kv_cache* cache, void* stream);
@@ -370,7 +371,8 @@ fq_status fq_kv_read(const fq_kv_cache* cache, const int32_t* slots, int T, uint
  *        has no effect.
  * Y      fp16 [R, Hq * 128] (16-byte aligned), apart from the inputs.
  * Hq a multiple of H, at most 1024; R in [1, 16384]; scale in [-65536, 65536].
- * A query head that holds an infinity or NaN gives NaN, the others keep their values.
+ * A query head that holds an infinity or NaN gives NaN, and so do all query heads of a key-value head one of
+ * whose tokens has a NaN scale; the others keep their values.
  * Arithmetic: query values of at least 2^-11 of their head's largest enter exactly, smaller ones
  * within 2^-22 of it, and their products with the codes are summed exactly; scores, softmax statistics and sums are
  * float32; the weights p_i * (v scale) enter the second product as two fp16 numbers, within 2^-22

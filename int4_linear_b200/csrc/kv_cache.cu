@@ -230,6 +230,12 @@ __device__ __forceinline__ uint32_t codes8(const __half2 (&v)[4], float inv) {
   return (e & 0x0F0F0F0Fu) | ((o << 4) & 0xF0F0F0F0u);
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // Token, head and kind (0 key, 1 value) of a head vector, a token's vectors being its H keys, then its H values.
 struct KvVec {
   long long t;
@@ -304,13 +310,14 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const __half* __r
       __half2(&h2)[8] = reinterpret_cast<__half2(&)[8]>(raw[u]);
       __half2 m2 = __habs2(h2[0]);
 #pragma unroll
-      for (int j = 1; j < 8; ++j) m2 = __hmax2(m2, __habs2(h2[j]));
-      float m = __half2float(__hmax(__low2half(m2), __high2half(m2)));
+      for (int j = 1; j < 8; ++j) m2 = __hmax2_nan(m2, __habs2(h2[j]));
+      float m = __half2float(__hmax_nan(__low2half(m2), __high2half(m2)));
 #pragma unroll
-      for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int o = 4; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (slot[u] < 0 || slot[u] >= limit) continue;
+      m = __fmaf_rn(m, 0.0f, m);  // an infinity becomes NaN
       const float alpha = v[u].which ? alpha_v : alpha_k;
-      const __half sh = __float2half_rn(__fdiv_rn(__fmul_rn(m, alpha), 7.0f));
+      const __half sh = __float2half_rn(__fdiv_rn(__fmul_rn(m, alpha), 7.0f));  // NaN: 0x7FFF
       const float s = __half2float(sh);
       const float inv = s > 0.f ? __fdividef(1.0f, s) : 0.f;  // s = 0: codes 0
       if (alpha < 1.0f || s < 0x1p-14f) {

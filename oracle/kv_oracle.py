@@ -42,11 +42,15 @@ def plan(lens, new, table, free, used, page, max_tokens):
 
 
 def quant_rows(x, alpha=1.0):
-    """Codes int8 [..., 128] and fp16 scales [...] of head vectors x (fp16)."""
+    """Codes int8 [..., 128] and fp16 scales [...] of head vectors x (fp16).  Vectors with an infinity or
+    NaN have the NaN scale 0x7FFF (and here codes 0)."""
     v = np.asarray(x, np.float16).astype(np.float32)
+    finite = np.isfinite(v).all(-1)
+    v = np.where(finite[..., None], v, np.float32(0))
     amax = np.abs(v).max(-1)
     s = ((amax * np.float32(alpha)).astype(np.float32) / np.float32(7.0)).astype(np.float16)
-    return O.quantize(v, s.astype(np.float32)[..., None]).astype(np.int8), s
+    return (O.quantize(v, s.astype(np.float32)[..., None]).astype(np.int8),
+            np.where(finite, s, np.array(0x7FFF, np.uint16).view(np.float16)))
 
 
 def empty_pool(pages, heads, page):
