@@ -257,7 +257,7 @@ def _check_rows(t, name, width):
             ld, one = t.stride()
             if one == 1:
                 return shape[0], ld if shape[0] > 1 else width
-        elif n == 3 and shape[1] * shape[2] == width and shape[0] > 0 and t.is_contiguous():
+        elif n == 3 and shape[2] == 128 and shape[1] * 128 == width and shape[0] > 0 and t.is_contiguous():
             return shape[0], width
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -267,8 +267,10 @@ def _check_rows(t, name, width):
     if len(shape) == 2:
         n, dense = shape[1], strides[1] == 1 or shape[1] == 1
     elif len(shape) == 3:
-        n = shape[1] * shape[2]
-        dense = (strides[2] == 1 or shape[2] == 1) and (strides[1] == shape[2] or shape[1] == 1)
+        if shape[2] != 128:
+            raise ValueError(f"{name} must be [T, heads, 128] or [T, heads * 128], got shape {tuple(shape)}")
+        n = shape[1] * 128
+        dense = strides[2] == 1 and (strides[1] == 128 or shape[1] == 1)
     else:
         n = dense = None
     if n != width or shape[0] < 1:
