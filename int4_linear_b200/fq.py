@@ -247,6 +247,25 @@ def _check_shape(t, shape, name):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _check_int(value, most, name):
+    """A whole number in [0, most]: what passes 32 bits would reach the library cut off."""
+    if not 0 <= value <= most:
+        raise ValueError(f"{name} = {value} must lie in [0, {most}]")
+
+
+_INT_MAX = 2 ** 31 - 1
+
+
+def _size(fn, *sizes) -> int:
+    """The bytes that `fn` says for these sizes; 0, as it says for others out of range, where one passes 32 bits."""
+    return fn(*sizes) if all(-_INT_MAX <= n <= _INT_MAX for n in sizes) else 0
+
+
+def _check_fmt(fmt):
+    if fmt != MXFP4 and fmt != NVFP4:
+        raise FqError(FQ_ERR_UNSUPPORTED, f"unsupported parameters: format {fmt} is not provided")
+
+
 def _check_rows(t, name, width):
     """fp16 rows of `width` values, any distance apart: [T, width] or [T, H, 128] with dense rows.
     Returns (T, the distance in elements)."""
@@ -462,6 +481,12 @@ def fq_kv_plan(lens, new_tokens, block_table, free_pages, pages_used, page_size:
                          f"{tuple(table_shape)}")
     _check_shape(new_tokens, (r,), "new_tokens")
     _check_shape(pages_used, (1,), "pages_used")
+    max_pages, num_free = table_shape[1], free_pages.numel()
+    if not (0 <= page_size <= _INT_MAX and 0 <= max_tokens <= 1 << 30 and max_pages <= _INT_MAX and num_free <= _INT_MAX):
+        _check_int(page_size, _INT_MAX, "page_size")
+        _check_int(max_tokens, 1 << 30, "max_tokens")
+        _check_int(max_pages, _INT_MAX, "max_pages")
+        _check_int(num_free, _INT_MAX, "the number of free pages")
     s, entered = _enter(stream, lens, new_tokens, block_table, free_pages, pages_used, lens_out, token_start, slots,
                         pages_used_out)
     try:
@@ -479,7 +504,7 @@ def fq_kv_plan(lens, new_tokens, block_table, free_pages, pages_used, page_size:
             lens_out, token_start, slots, pages_used_out = (
                 lens.new_empty(n) if t is None else t for t, n in zip(given, sizes))
         _raise(lib().fq_kv_plan(lens.data_ptr(), new_tokens.data_ptr(), r, page_size, block_table.data_ptr(),
-                                table_shape[1], free_pages.data_ptr() or None, free_pages.numel(),
+                                max_pages, free_pages.data_ptr() or None, num_free,
                                 pages_used.data_ptr(), lens_out.data_ptr(), token_start.data_ptr(),
                                 slots.data_ptr() or None, max_tokens, pages_used_out.data_ptr(), s))
     finally:
@@ -554,7 +579,7 @@ def fq_kv_read(cache: KVCache, slots, K=None, V=None, stream=None):
 
 
 def fq_kv_attn_workspace_size(R: int, Hq: int, H: int) -> int:
-    return lib().fq_kv_attn_workspace_size(R, Hq, H)
+    return _size(lib().fq_kv_attn_workspace_size, R, Hq, H)
 
 
 def fq_kv_attn_workspace(R: int, Hq: int, H: int, device="cuda"):
@@ -579,6 +604,9 @@ def fq_kv_attn(Q, lens, block_table, cache: KVCache, scale: float | None = None,
     rows, ldq = _check_rows(Q, "Q", width)
     if rows != r or width < 128 or width % 128:
         raise ValueError(f"Q must have {r} rows of Hq * 128 values, got shape {tuple(q_shape)}")
+    if not (0 <= window <= _INT_MAX and table_shape[1] <= _INT_MAX):
+        _check_int(window, _INT_MAX, "window")
+        _check_int(table_shape[1], _INT_MAX, "max_pages")
     hq = width // 128
     s, entered = _enter(stream, Q, lens, block_table, cache.pool, Y, workspace)
     try:
@@ -603,7 +631,7 @@ def fq_kv_attn(Q, lens, block_table, cache: KVCache, scale: float | None = None,
 
 def fq_mx_scale_bytes(rows: int, k: int, fmt: int) -> int:
     """Bytes of the tiled scales of a [rows, K] tensor, padding included."""
-    return lib().fq_mx_scale_bytes(rows, k, fmt)
+    return _size(lib().fq_mx_scale_bytes, rows, k, fmt)
 
 
 _MX_NAMES = {"X": ("Xq", "Sx"), "W": ("Wq", "Sw")}
@@ -611,6 +639,7 @@ _MX_NAMES = {"X": ("Xq", "Sx"), "W": ("Wq", "Sw")}
 
 def _check_mx(Q, S, fmt, name):
     """(rows, K) of microscaled codes Q [rows, K/2] with their tiled scales S."""
+    _check_fmt(fmt)
     codes, scales = _MX_NAMES[name]
     _check(Q, torch.uint8, codes)
     _check(S, torch.uint8, scales)
@@ -635,6 +664,7 @@ def _check_x(X, name):
 def fq_mx_quant(X, fmt: int, g=None, Q=None, S=None, stream=None):
     """fp16 [R, K] (rows any distance apart) to microscaled 4-bit codes: (Q uint8 [R, K/2], S uint8, the
     tiled scales).  fmt MXFP4 or NVFP4 (g: its float32 [1] tensor scale on the device, None: 1)."""
+    _check_fmt(fmt)
     r, k, ldx = _check_x(X, "X")
     _check_g(g, "g")
     s, entered = _enter(stream, X, g, Q, S)
@@ -673,11 +703,11 @@ def fq_mx_dequant(Q, S, fmt: int, g=None, X=None, stream=None):
 
 
 def fq_mx_gemm_workspace_size(m: int, n: int, k: int, fmt: int) -> int:
-    return lib().fq_mx_gemm_workspace_size(m, n, k, fmt)
+    return _size(lib().fq_mx_gemm_workspace_size, m, n, k, fmt)
 
 
 def fq_mx_linear_workspace_size(m: int, n: int, k: int, fmt: int) -> int:
-    return lib().fq_mx_linear_workspace_size(m, n, k, fmt)
+    return _size(lib().fq_mx_linear_workspace_size, m, n, k, fmt)
 
 
 def fq_mx_linear_workspace(m: int, n: int, k: int, fmt: int, device="cuda"):

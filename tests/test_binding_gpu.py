@@ -1,4 +1,4 @@
-"""Refusals of the binding: shapes of one size but another meaning.  Nothing is launched."""
+"""Refusals of the binding: shapes of one size but another meaning, numbers that pass 32 bits.  Nothing is launched."""
 import pytest
 import torch
 
@@ -22,3 +22,29 @@ def test_head_vectors_of_another_length():
     for q in (torch.zeros(3, 16, 64, **f16), torch.zeros(3, 4, 256, **f16), torch.zeros(3, 128, 8, **f16)):
         with pytest.raises(ValueError, match="128"):
             fq.fq_kv_attn(q, torch.zeros(3, **i32), torch.zeros(3, 1, **i32), cache)
+
+
+@pytest.mark.parametrize("window", [-1, 2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 32])
+def test_windows_that_pass_32_bits(window):
+    with pytest.raises(ValueError, match="window"):
+        fq.fq_kv_attn(torch.zeros(1, 2, 128, **f16), torch.zeros(1, **i32), torch.zeros(1, 1, **i32),
+                      fq.kv_cache(2, 2, 16), window=window)
+
+
+@pytest.mark.parametrize("page_size,max_tokens", [(2 ** 32 + 16, 4), (-16, 4), (16, -1), (16, 2 ** 32 + 4), (16, 2 ** 30 + 1)])
+def test_plan_numbers_that_pass_32_bits(page_size, max_tokens):
+    one, table = torch.zeros(1, **i32), torch.zeros(1, 2, **i32)
+    with pytest.raises(ValueError, match="page_size|max_tokens"):
+        fq.fq_kv_plan(one, one, table, one, one, page_size, max_tokens)
+
+
+@pytest.mark.parametrize("fmt", [2, -1, 2 ** 32, 2 ** 32 + 1])
+def test_formats_that_are_none(fmt):
+    """2^32 + 1 would be checked as one format and computed as the other, whose scales are twice as many."""
+    x = torch.zeros(8, 128, **f16)
+    q, s = fq.fq_mx_quant(x, fq.MXFP4)
+    for call in (lambda: fq.fq_mx_quant(x, fmt), lambda: fq.fq_mx_dequant(q, s, fmt), lambda: fq.fq_mx_gemm(q, s, q, s, fmt),
+                 lambda: fq.fq_mx_linear(x, fmt, q, s)):
+        with pytest.raises(fq.FqError, match="format") as e:
+            call()
+        assert e.value.status == fq.FQ_ERR_UNSUPPORTED
