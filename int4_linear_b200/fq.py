@@ -740,6 +740,8 @@ def fq_mx_gemm(Xq, Sx, Wq, Sw, fmt: int, g_x=None, g_w=None, Y=None, workspace=N
         raise ValueError(f"Xq has K = {k}, Wq {kw}")
     _check_g(g_x, "g_x")
     _check_g(g_w, "g_w")
+    if workspace is not None:
+        _check(workspace, torch.uint8, "workspace")
     s, entered = _enter(stream, Xq, Sx, Wq, Sw, g_x, g_w, Y, workspace)
     try:
         Y = _mx_out(Xq, Y, m, n)

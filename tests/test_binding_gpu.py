@@ -1,4 +1,5 @@
-"""Refusals of the binding: shapes of one size but another meaning, numbers that pass 32 bits.  Nothing is launched."""
+"""Refusals of the binding: shapes of one size but another meaning, numbers that pass 32 bits, workspaces that are no
+plain bytes.  Nothing is launched."""
 import pytest
 import torch
 
@@ -48,3 +49,13 @@ def test_formats_that_are_none(fmt):
         with pytest.raises(fq.FqError, match="format") as e:
             call()
         assert e.value.status == fq.FQ_ERR_UNSUPPORTED
+
+
+def test_product_workspaces_that_are_no_plain_bytes():
+    """Bytes of a strided or repeated view do not lie where its length says."""
+    x = torch.zeros(8, 128, **f16)
+    q, s = fq.fq_mx_quant(x, fq.MXFP4)
+    n = fq.fq_mx_gemm_workspace_size(8, 8, 128, fq.MXFP4)
+    for ws in (torch.zeros(2 * n, **u8)[::2], torch.zeros(1, **u8).expand(n), torch.zeros(n, **i32), torch.zeros(n, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="workspace"):
+            fq.fq_mx_gemm(q, s, q, s, fq.MXFP4, workspace=ws)
