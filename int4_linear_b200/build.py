@@ -30,8 +30,25 @@ def _nvcc() -> str:
     return p if os.path.exists(p) else "nvcc"
 
 
+def _stamp() -> str:
+    """The file that names the compiler and flags of the objects beside it."""
+    return os.path.join(HERE, "_build", "flags")
+
+
+def _flags() -> str:
+    return "\n".join([_nvcc(), *NVCC_FLAGS])
+
+
+def _other_flags() -> bool:
+    try:
+        with open(_stamp()) as f:
+            return f.read() != _flags()
+    except OSError:
+        return True
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or _other_flags():
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, h) for h in HEADERS]
@@ -53,6 +70,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 def _build(objdir: str, force: bool, verbose: bool) -> None:
     newest = max(os.path.getmtime(os.path.join(CSRC, h)) for h in HEADERS)
+    force = force or _other_flags()
+    if os.path.exists(_stamp()):
+        os.remove(_stamp())  # until all objects are of one set of flags
     objs = [os.path.join(objdir, s.replace(".cu", ".o")) for s in SOURCES]
 
     def compile_one(job):
@@ -67,6 +87,8 @@ def _build(objdir: str, force: bool, verbose: bool) -> None:
 
     with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as pool:
         list(pool.map(compile_one, zip(SOURCES, objs)))
+    with open(_stamp(), "w") as f:
+        f.write(_flags())
     tmp = LIB + ".tmp"
     cmd = [_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-cudart", "static", "-o", tmp, *objs]
     if verbose:
