@@ -319,7 +319,8 @@ typedef struct {
  *               row of each request in the step's ragged token batch;
  *   slots       int32 [max_tokens]: the slot of each of those rows; -1 from
  *               token_start[R] on, so that a captured step of max_tokens rows
- *               may hold fewer tokens;
+ *               may hold fewer tokens, and where the page's id lies outside
+ *               [0, 2^31 / page_size);
  *   pages_used_out int32 [1] (may be pages_used itself): pages_used + the pages taken.
  * A request is refused as a whole, with slots -1, len_out = len and no pages,
  * when its table row is too short (it asks for no pages then), when its rows

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
         const int pos = l + (i - s_start[r]);
         const int pi = pos >> p.page_shift, held = (l + page - 1) >> p.page_shift;
         const int id = pi < held ? p.table[size_t(r) * p.max_pages + pi] : p.free_pages[used + s_first[r] + pi - held];
-        slot[u] = id * page + (pos & (page - 1));
+        if (uint32_t(id) < 1u << (31 - p.page_shift)) slot[u] = id * page + (pos & (page - 1));  // no page of any cache otherwise
       }
     }
 #pragma unroll

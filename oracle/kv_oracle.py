@@ -33,7 +33,9 @@ def plan(lens, new, table, free, used, page, max_tokens):
             taken += want - held
             for i in range(k):
                 p = n + i
-                slots[row + i] = int(table[r, p // page]) * page + p % page
+                pg = int(table[r, p // page])
+                if 0 <= pg < 2 ** 31 // page:
+                    slots[row + i] = pg * page + p % page
         out.append(n + k if ok else n)
         row += k
         start.append(row)
