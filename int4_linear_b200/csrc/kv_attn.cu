@@ -38,12 +38,14 @@
 //    of a token's row; the order of the dims inside the product is free, so the queries are arranged once per
 //    segment to match the nibbles.  An fp16 product with the constant of 64 + (code + 8) taken off afterwards left
 //    errors of 2^-15 of a logit.
-//  - sum: m16n8k16, A = 128 dims x 16 tokens of V codes (exact; a nibble u = code + 8 is the mantissa
-//    of a subnormal fp16, so an AND makes the operand, and one product with the constant -8
-//    starts the sums), B = the weights, taken from the scores' layout by movmatrix.  A lane reads 8 bytes of
-//    each of its 4 tokens and pairs two tokens' nibbles by byte permutation.  A turn's 32
-//    tokens are added up in the tensor core, whose adds cut off; the running sums are rounded float32 adds (added after
-//    every 16 tokens, attention took 2 to 6 % longer).
+//  - sum: m16n8k16, A = 128 dims x 16 tokens of V codes (exact; a logic operation makes a subnormal
+//    fp16 number of a nibble, a multiply-add the code), B = the weights, taken from the scores' layout by
+//    movmatrix.  A lane reads 8 bytes of each of its 4 tokens and pairs two tokens' nibbles by byte permutation.  A turn's
+//    32 tokens are added up in the tensor core, which cuts every term off at 2^-23 of the largest or finer; the
+//    running sums are rounded float32 adds (added after every 16 tokens, attention took 2 to 6 % longer).
+//    With the subnormal numbers as operands, and -8 sum(w) added by one more product, long caches took 2 % less
+//    time, but the tensor core aligns its terms by a subnormal operand's exponent, 2^6 times the number's own, and
+//    the terms were cut off that much earlier: 10 to 18 % of the outputs came out rounded to the wrong side, now 0.2 %.
 // Weights: w = exp2(s - m) * (v scale), times 2^8 over the head's largest w so far, enters as two fp16 numbers, its
 // rounding and what that left (2^-22 relative, or 2^-33 of that largest where the second is
 // subnormal).  Taken relative to the largest v scale instead, they were lost beside a token of no weight with a much
@@ -206,10 +208,16 @@ __device__ __forceinline__ uint32_t bytes4(const uint32_t (&v)[4], uint32_t sel)
   return __byte_perm(__byte_perm(v[0], v[1], sel), __byte_perm(v[2], v[3], sel), 0x5410);
 }
 
-// Nibbles u of each half word at bits 0-3 and 4-7 -> the fp16 numbers u 2^-24 and u 2^-20 (subnormal: the
-// nibble is the mantissa).  u = q + 8: the codes' top bits are flipped beforehand.
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return w & 0x000F000Fu; }
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return w & 0x00F000F0u; }
+// Nibbles u of each half word at bits 0-3 and 4-7 -> the fp16 numbers q 2^-10, u = q + 8: the codes' top bits are flipped
+// beforehand (here, in the same operation, took 4 % longer).  A nibble is the mantissa of the subnormal number u 2^-24
+// or u 2^-20, and one exact multiply-add takes it to q 2^-10.
+__device__ __forceinline__ uint32_t codes_from(uint32_t u, uint16_t factor) {
+  const __half2 q = __hfma2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(factor)),
+                            __half2half2(__ushort_as_half(0xA000)));  // -8 2^-10
+  return *reinterpret_cast<const uint32_t*>(&q);
+}
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return codes_from(w & 0x000F000Fu, 0x7400); }  // 2^14
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return codes_from(w & 0x00F000F0u, 0x6400); }  // 2^10
 
 // The token of score row i (0..15): rows 2t, 2t + 1 of one lane's weights.  Bit 0
 // alternates within a row pair (score reads of two rows hit different banks)
@@ -534,16 +542,16 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   float winv[NT][2];             // 2^8 over the largest weight p * (v scale) so far
   bool held = false;             // the last segment is cut off and stays in registers
   static_assert(NT * kPieceFloats * 4 <= kDepth * kStepBytes, "a piece fits a warp's turns");
-  auto in_units = [&]() {  // rows g hold 2^-24, rows g + 8 2^-20 of the sums, both times winv
+  auto in_units = [&]() {  // the registers hold 2^-10 of the sums, times winv
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float f = 1.0f / winv[nn][k];
+        const float f = 0x1p10f / winv[nn][k];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          o[nn][i][k] *= f * 0x1p24f;
-          o[nn][i][k + 2] *= f * 0x1p20f;
+          o[nn][i][k] *= f;
+          o[nn][i][k + 2] *= f;
         }
       }
     if (TWICE) {
@@ -800,7 +808,6 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       }
       constexpr int kW = TWICE ? 1 : 2;
       uint32_t w[2][kW][NT][2];  // of both halves: weights and what their rounding left, as operands
-      float c8[NT][4];  // -8 sum(w): rows g in the units of codes_lo, rows g + 8 of codes_hi
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -823,14 +830,6 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
             w[h][0][nn][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&a));
             w[h][0][nn][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&b));
           }
-          // -2^-21 = -8 2^-24 and -2^-17 = -8 2^-20 as fp16
-          const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-          if (h == 0)
-            mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w[h][0][nn][0], w[h][0][nn][1], zero);
-          else
-            mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w[h][0][nn][0], w[h][0][nn][1], c8[nn]);
-          if (!TWICE)
-            mma_f16(c8[nn], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w[h][kW - 1][nn][0], w[h][kW - 1][nn][1], c8[nn]);
         }
       }
       // values: lane (g, t4) holds dims [16 g, 16 g + 16) of its four tokens of a half
@@ -860,8 +859,9 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
 #pragma unroll
             for (int nn = 0; nn < NT; ++nn) {
               if (h == 0) {
-                mma_f16(d[nn][0], a0, a1, a2, a3, w[h][0][nn][0], w[h][0][nn][1], c8[nn]);
-                mma_f16(d[nn][1], b0, b1, b2, b3, w[h][0][nn][0], w[h][0][nn][1], c8[nn]);
+                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(d[nn][0], a0, a1, a2, a3, w[h][0][nn][0], w[h][0][nn][1], zero);
+                mma_f16(d[nn][1], b0, b1, b2, b3, w[h][0][nn][0], w[h][0][nn][1], zero);
               } else {
                 mma_f16(d[nn][0], a0, a1, a2, a3, w[h][0][nn][0], w[h][0][nn][1], d[nn][0]);
                 mma_f16(d[nn][1], b0, b1, b2, b3, w[h][0][nn][0], w[h][0][nn][1], d[nn][1]);

@@ -110,3 +110,30 @@ def test_one_large_value_scale_without_weight(hq, h, page, at, log2_ratio):
     ref = KO.attention(q, lens, table, pool, 128 ** -0.5)[0]
     assert np.sqrt((ref ** 2).mean()) > 2.0 ** -13   # fp16's normal range
     assert error_over_rounding(run_attn(q, lens, table, pool), ref) <= 1.1
+
+
+def gaussian_case(seed, lens, hq, h, page):
+    """Keys and values as fq_kv_write caches Gaussian ones, some key channels three times the others; queries of
+    standard deviation 1.5: scores of some 1.8."""
+    g = np.random.Generator(np.random.PCG64([seed, hq, h, page]))
+    q, lens, table, pool = attn_case(seed, lens, hq, h, page)
+    n = sum(lens)
+    x = g.standard_normal((2, n, h, 128)).astype(np.float32)
+    x[0, ..., ::16] *= 3
+    slots = [table[i, t // page] * page + t % page for i, m in enumerate(lens) for t in range(m)]
+    KO.store(pool, *KO.quant_rows(x[0]), *KO.quant_rows(x[1]), np.array(slots))
+    return (q.astype(np.float32) * 1.5).astype(np.float16), lens, table, pool
+
+
+@pytest.mark.parametrize("hq,h", HEADS)
+@pytest.mark.parametrize("page", [16, 64])
+def test_ordinary_heads(hq, h, page):
+    """A turn's at most 68 terms are cut off at 2^-23 of the largest one, at most 8 times the largest weight: sqrt(68 / 3)
+    2^-23 8 = 4.6e-6 of that weight (rms).  An output of values of rms 2.3 or more (the codes of Gaussian vectors, whose
+    largest is 7) is at least 2.3 times the root of the weights' squares, so the cuts are 2e-6 of it.  Four float32
+    roundings of scores below 16 (in powers of two) and an exponential within 2^-22 are 1e-6 of each weight.  Together
+    e = 3e-6 / 2.05e-4 = 0.015 of the output's rounding: sqrt(1 + e^2), and four standard deviations 2 e / sqrt(n) of the chance
+    products of both for n >= 2048 outputs: 1.0001 + 0.0027."""
+    q, lens, table, pool = gaussian_case(35, [1000, 8000], hq, h, page)
+    ref = KO.attention(q, lens, table, pool, 128 ** -0.5)[0]
+    assert error_over_rounding(run_attn(q, lens, table, pool), ref) <= 1.0028
