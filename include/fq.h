@@ -374,8 +374,8 @@ fq_status fq_kv_read(const fq_kv_cache* cache, const int32_t* slots, int T, uint
  * Hq a multiple of H, at most 1024; R in [1, 16384]; scale in [-65536, 65536].
  * A query head that holds an infinity or NaN gives NaN, and so do all query heads of a key-value head one of
  * whose tokens has a NaN scale; the others keep their values.
- * Arithmetic: query values of at least 2^-11 of their head's largest enter exactly, smaller ones
- * within 2^-22 of it, and their products with the codes are summed exactly; scores, softmax statistics and sums are
+ * Arithmetic: query values enter exactly (with up to 4 query heads per key-value head, values below
+ * 2^-11 of their head's largest within 2^-22 of it); scores, softmax statistics and sums are
  * float32; the weights p_i * (v scale) enter the second product as two fp16 numbers, within 2^-22
  * of themselves or 2^-33 of the head's largest one, whichever is more.  The summation order is the kernel's, the same on every run for the
  * same sizes and lengths.

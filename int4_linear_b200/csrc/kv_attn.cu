@@ -27,17 +27,19 @@
 // Products.  mma.sync: the tensor-memory path needs 128 rows of queries, and a request has
 // G = Hq / H <= 16 of them per head, so its staging of operands would cost more than
 // the product.
-//  - scores: m16n8k32 in integers, A = 16 tokens x 128 dims of K codes (nibbles shifted to the
-//    top of a byte: 16 code, one logic operation per four), B = 8 queries as whole multiples of 2^-22 of the
+//  - scores, up to four query heads: m16n8k32 in integers, A = 16 tokens x 128 dims of K codes (nibbles shifted to
+//    the top of a byte: 16 code, one logic operation per four), B = the queries as whole multiples of 2^-22 of the
 //    power of two above their head's largest value, in three signed bytes: an fp16 value of at least 2^-11 of
 //    the largest is such a multiple, a smaller one is off by at most 2^-22 of the largest.  The sums are exact, so
-//    three float32 roundings are all else that a score has.  With two bytes (half a step of max|q| / 32639) long caches
-//    took 201 instead of 219 us, but a query channel 30 (100) times the others left errors of 1.4 to 1.8 (2.9 to 6.2) times
-//    the output's own rounding, scores of standard deviation 14 up to 1.19 times; now it is 1.0 everywhere.  Up to
-//    four query heads take the tile's other four columns for their second byte.  A lane reads 16 consecutive bytes
-//    of a token's row; the order of the dims inside the product is free, so the queries are arranged once per
-//    segment to match the nibbles.  An fp16 product with the constant of 64 + (code + 8) taken off afterwards left
-//    errors of 2^-15 of a logit.
+//    three float32 roundings are all else that a score has.  The tile's other four columns take the second byte.
+//  - scores, more query heads: m16n8k16, A = 16 tokens x 128 dims of K codes as fp16 numbers (as the values', below), B =
+//    the queries as they are; a sum's 128 terms are cut off at 2^-23 of the largest or finer.  With three bytes and integers
+//    16 query heads took 39.1 instead of 35.7 us (33 requests of 64/4 heads and 4096 tokens), 64 long
+//    requests of 64/8 heads 229 instead of 232; with this way for four query heads too 12 x 32/32 heads took 35.0 instead of 32.9.
+//    With queries in two bytes (half a step of max|q| / 32639) a query channel 30 (100) times the others left errors of
+//    1.4 to 1.8 (2.9 to 6.2) times the output's own rounding, scores of standard deviation 14 up to 1.19 times;
+//    now it is 1.0 everywhere.  A lane reads 16 consecutive bytes of a token's row; the order of the dims inside
+//    the product is free, so the queries are arranged once per segment to match the nibbles.
 //  - sum: m16n8k16, A = 128 dims x 16 tokens of V codes (exact; a logic operation makes a subnormal
 //    fp16 number of a nibble, a multiply-add the code), B = the weights, taken from the scores' layout by
 //    movmatrix.  A lane reads 8 bytes of each of its 4 tokens and pairs two tokens' nibbles by byte permutation.  A turn's
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
                                         : make_uint4(0, 0, 0, 0);
   };
 
-  constexpr int kQ = TWICE ? 2 : 3;  // products per 32 dims of a score
+  constexpr uint32_t kFlip = 0x88888888u;  // code -> code + 8
   Seg seg;
   int slot = 0;         // ring slot of the turn to be taken
   float o[NT][8][4];
@@ -609,11 +611,10 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
   while (next_segment(seg)) {
     load_queries();
     Ids next_ids = page_ids(seg, 0);
-    // queries of this segment in units of 2^(E-22), 2^E the power of two above the head's largest value, as three
-    // signed bytes: q = unit (65536 hi + 256 mid + lo), |hi| <= 64; the even dims of 8 in one word, the odd ones in
-    // the next.  TWICE: columns 0-3 of the first product hold hi and columns 4-7 mid, of the second lo and 0.
-    uint32_t qf[NT][kQ][8];
-    float unit[NT][2];  // of heads 2 t4, 2 t4 + 1, times the score's scale and 1/16 (a nibble is taken 16-fold)
+    // queries of this segment as the products' second operands
+    uint32_t qf[NT][16];
+    float unit[2];     // of the sums of heads 2 t4, 2 t4 + 1, times the score's scale
+    uint32_t most[NT];  // bits of the largest value of column g's head, as float32: at least 0x7F800000 if it is not finite
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn) {
       __half2 m2 = __float2half2_rn(0.f);  // NaN stays
@@ -625,41 +626,51 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       }
       uint32_t mb = __float_as_uint(__half2float(__hmax_nan(__low2half(m2), __high2half(m2))));
       mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));  // of numbers without sign, NaN the largest
-      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+      most[nn] = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+    }
+    if (TWICE) {
+      // three signed bytes of multiples of 2^(E-22), 2^E the power of two above the head's largest value: q =
+      // 2^(E-22) (65536 hi + 256 mid + lo), |hi| <= 64; the even dims of 8 in one word, the odd ones in the next.  The
+      // first product's columns 0-3 hold hi and 4-7 mid, the second's lo and 0.
+      const uint32_t mb = most[0];
       // the largest value is 0 or has the float32 exponent mb >> 23 in [103, 142] (fp16's range); E = (mb >> 23) - 126
       const bool finite = mb < 0x7F800000u;
       const float inv = mb && finite ? __uint_as_float((275u - (mb >> 23)) << 23) : 0.f;
+      const bool upper = g < 4;
+      const uint32_t sel = upper ? 0x6262u : 0x5151u, flip = upper ? 0u : 0x80808080u;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const __half2* h2 = reinterpret_cast<const __half2*>(&raw[nn][j]);
-        uint32_t ev[4], od[4];  // round(q inv) + 128 * 256 + 128
+        const __half2* h2 = reinterpret_cast<const __half2*>(&raw[0][j]);
+        uint32_t ev[4], od[4];  // round(q inv) + 128 * 256 + 128: byte 2 is hi, byte 1 mid + 128, byte 0 lo + 128
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = __half22float2(h2[k]);
           ev[k] = __float_as_uint(__fmaf_rn(f.x, inv, kRound)) - uint32_t(kRoundBits - 32896);
           od[k] = __float_as_uint(__fmaf_rn(f.y, inv, kRound)) - uint32_t(kRoundBits - 32896);
         }
-        // byte 2 is hi; byte 1 is mid + 128, byte 0 lo + 128
-        if (TWICE) {
-          const bool upper = g < 4;
-          const uint32_t sel = upper ? 0x6262u : 0x5151u, flip = upper ? 0u : 0x80808080u;
-          qf[nn][0][2 * j] = bytes4(ev, sel) ^ flip;
-          qf[nn][0][2 * j + 1] = bytes4(od, sel) ^ flip;
-          qf[nn][1][2 * j] = upper ? bytes4(ev, 0x4040u) ^ 0x80808080u : 0u;
-          qf[nn][1][2 * j + 1] = upper ? bytes4(od, 0x4040u) ^ 0x80808080u : 0u;
-        } else {
-          qf[nn][0][2 * j] = bytes4(ev, 0x6262u);
-          qf[nn][0][2 * j + 1] = bytes4(od, 0x6262u);
-          qf[nn][1][2 * j] = bytes4(ev, 0x5151u) ^ 0x80808080u;
-          qf[nn][1][2 * j + 1] = bytes4(od, 0x5151u) ^ 0x80808080u;
-          qf[nn][kQ - 1][2 * j] = bytes4(ev, 0x4040u) ^ 0x80808080u;
-          qf[nn][kQ - 1][2 * j + 1] = bytes4(od, 0x4040u) ^ 0x80808080u;
-        }
+        qf[0][2 * j] = bytes4(ev, sel) ^ flip;
+        qf[0][2 * j + 1] = bytes4(od, sel) ^ flip;
+        qf[0][8 + 2 * j] = upper ? bytes4(ev, 0x4040u) ^ 0x80808080u : 0u;
+        qf[0][8 + 2 * j + 1] = upper ? bytes4(od, 0x4040u) ^ 0x80808080u : 0u;
       }
-      // 2^(E-22) scale / 16; a head with an infinity or NaN is NaN
+      // 2^(E-22) scale / 16 (a nibble is taken 16-fold); a head with an infinity or NaN is NaN
       const float u = !finite ? NAN : mb ? __uint_as_float(((mb >> 23) - 21u) << 23) * (p.scale_log2 / 16.0f) : 0.f;
-      unit[nn][0] = __shfl_sync(0xffffffffu, u, 8 * t4);
-      unit[nn][1] = __shfl_sync(0xffffffffu, u, 8 * t4 + 4);
+      unit[0] = __shfl_sync(0xffffffffu, u, 8 * t4);
+      unit[1] = __shfl_sync(0xffffffffu, u, 8 * t4 + 4);
+    } else {
+      // as they are, dims d and d + 4 of 8 in a word, as the nibbles lie; a head with an infinity or NaN is NaN
+#pragma unroll
+      for (int nn = 0; nn < NT; ++nn)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 nan = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+          const uint4 r = most[nn] < 0x7F800000u ? raw[nn][j] : nan;
+          qf[nn][4 * j] = __byte_perm(r.x, r.z, 0x5410);
+          qf[nn][4 * j + 1] = __byte_perm(r.x, r.z, 0x7632);
+          qf[nn][4 * j + 2] = __byte_perm(r.y, r.w, 0x5410);
+          qf[nn][4 * j + 3] = __byte_perm(r.y, r.w, 0x7632);
+        }
+      unit[0] = unit[1] = p.scale_log2 * 0x1p10f;  // codes are taken as multiples of 2^-10
     }
 #pragma unroll
     for (int nn = 0; nn < NT; ++nn) {
@@ -693,40 +704,53 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
         const uint4 k0 = *reinterpret_cast<const uint4*>(sp + k_off + h * 1024);
         const uint4 k1 = *reinterpret_cast<const uint4*>(sp + k_off + h * 1024 + 8 * kKvRowBytes);
         const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
-        int a[NT][kQ][4];  // sums of the products with hi, mid and lo
+        if (TWICE) {
+          int a[2][4];  // sums of the products with hi and mid, and with lo
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t e0, d0, e1, d1;  // 16 q of the even and odd dims of rows g and g + 8
-          unpack8_hi(kw0[j], e0, d0);
-          unpack8_hi(kw1[j], e1, d1);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t e0, d0, e1, d1;  // 16 q of the even and odd dims of rows g and g + 8
+            unpack8_hi(kw0[j], e0, d0);
+            unpack8_hi(kw1[j], e1, d1);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              if (j == 0)
+                mma_s8_first(a[b], e0, e1, d0, d1, qf[0][8 * b], qf[0][8 * b + 1]);
+              else
+                mma_s8(a[b], e0, e1, d0, d1, qf[0][8 * b + 2 * j], qf[0][8 * b + 2 * j + 1]);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            // 65536 hi + lo, and 256 mid of the same heads four columns on
+            const float c = t4 < 2 ? 65536.0f : 256.0f;
+            float2 s = ffma2(whole_numbers(a[0][k], a[0][k + 1]), make_float2(c, c), whole_numbers(a[1][k], a[1][k + 1]));
+            s = fadd2(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, 2), __shfl_xor_sync(0xffffffffu, s.y, 2)));
+            s = fmul2(s, make_float2(unit[0], unit[1]));
+            sc[h][0][k] = s.x;
+            sc[h][0][k + 1] = s.y;
+          }
+        } else {
+          float a[NT][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t x0 = kw0[j] ^ kFlip, x1 = kw1[j] ^ kFlip, z0 = x0 >> 8, z1 = x1 >> 8;
+            const uint32_t e0 = codes_lo(x0), e1 = codes_lo(x1), d0 = codes_hi(x0), d1 = codes_hi(x1);
+            const uint32_t f0 = codes_lo(z0), f1 = codes_lo(z1), g0 = codes_hi(z0), g1 = codes_hi(z1);
+#pragma unroll
+            for (int nn = 0; nn < NT; ++nn) {
+              const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+              if (j == 0)
+                mma_f16(a[nn], e0, e1, d0, d1, qf[nn][0], qf[nn][1], zero);
+              else
+                mma_f16(a[nn], e0, e1, d0, d1, qf[nn][4 * j], qf[nn][4 * j + 1], a[nn]);
+              mma_f16(a[nn], f0, f1, g0, g1, qf[nn][4 * j + 2], qf[nn][4 * j + 3], a[nn]);
+            }
+          }
 #pragma unroll
           for (int nn = 0; nn < NT; ++nn)
 #pragma unroll
-            for (int b = 0; b < kQ; ++b) {
-              if (j == 0)
-                mma_s8_first(a[nn][b], e0, e1, d0, d1, qf[nn][b][0], qf[nn][b][1]);
-              else
-                mma_s8(a[nn][b], e0, e1, d0, d1, qf[nn][b][2 * j], qf[nn][b][2 * j + 1]);
-            }
+            for (int k = 0; k < 4; ++k) sc[h][nn][k] = a[nn][k] * unit[k & 1];
         }
-#pragma unroll
-        for (int nn = 0; nn < NT; ++nn)
-#pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            const float2 c256 = make_float2(256.0f, 256.0f);
-            float2 s = whole_numbers(a[nn][0][k], a[nn][0][k + 1]);
-            if (TWICE) {  // 65536 hi + lo, and 256 mid of the same heads four columns on
-              const float c = t4 < 2 ? 65536.0f : 256.0f;
-              s = ffma2(s, make_float2(c, c), whole_numbers(a[nn][1][k], a[nn][1][k + 1]));
-              s = fadd2(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, 2), __shfl_xor_sync(0xffffffffu, s.y, 2)));
-            } else {
-              s = ffma2(s, c256, whole_numbers(a[nn][1][k], a[nn][1][k + 1]));
-              s = ffma2(s, c256, whole_numbers(a[nn][kQ - 1][k], a[nn][kQ - 1][k + 1]));
-            }
-            s = fmul2(s, make_float2(unit[nn][0], unit[nn][1]));
-            sc[h][nn][k] = s.x;
-            sc[h][nn][k + 1] = s.y;
-          }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           ks[h][k] = __half2float(*reinterpret_cast<const __half*>(sp + kStepKs + 2 * (row0 + 16 * h + 8 * k)));
@@ -835,7 +859,6 @@ __global__ void __launch_bounds__(kAttnThreads, NT == 1 ? 2 : 1) kv_attn_kernel(
       // values: lane (g, t4) holds dims [16 g, 16 g + 16) of its four tokens of a half
 #pragma unroll
       for (int jj = 0; jj < 2; ++jj) {
-        constexpr uint32_t kFlip = 0x88888888u;  // code -> code + 8
         uint32_t xw[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

@@ -76,3 +76,23 @@ def test_attention_shows_it(hq, h, which, bad, page):
     assert torch.equal(torch.isnan(shown[0]), hit)
     assert torch.equal(shown[0][~hit], good[0][~hit])
     assert torch.equal(shown[1], good[1]) and shown[1].isfinite().all()
+
+
+@pytest.mark.parametrize("hq,h", [(4, 1), (8, 1), (16, 1)])
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("code", [0x00, 0x77, 0x88])
+def test_query_whose_scores_would_be_infinite(hq, h, bad, code):
+    """One infinite value times codes of one sign would give every token a score of minus infinity, i.e. no weight at
+    all: the head is NaN all the same."""
+    cache = fq.kv_cache(1, h, 16)
+    kq, vq, ks, vs = cache.views()
+    kq[:] = code
+    vq[:] = 0x11
+    ks[:] = vs[:] = 1
+    q = torch.ones(1, hq, 128, dtype=torch.float16, device="cuda")
+    q[0, 1, 17] = bad
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    y = fq.fq_kv_attn(q, one * 9, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), cache).view(hq, 128)
+    hit = torch.zeros(hq, 128, dtype=torch.bool, device="cuda")
+    hit[1] = True
+    assert torch.equal(torch.isnan(y), hit) and (y[~hit] == 1).all()
