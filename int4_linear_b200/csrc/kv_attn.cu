@@ -7,9 +7,9 @@
 // against 4 * 128 operations per query head, so the work is a stream of pages
 // with the arithmetic hidden under it.  At the measured 6.55 TB/s an SM has
 // about 5.7 cycles per token and head, i.e. some 23 warp instructions; this kernel
-// executes 18, and with the four warps that a scheduler's registers hold issues in 54 % of the
+// executes as many, and with the four warps that a scheduler's registers hold issues in 59 % of the
 // cycles, waiting for products and their results: 64 requests of 8 heads and 14200
-// tokens on average (eight queries a head) take 201 us, 4.8 TB/s.
+// tokens on average (eight queries a head) take 232 us, 4.1 TB/s.
 //
 // Division.  The turns (32 tokens of one request and key-value head) of all
 // requests form one sequence, request-major; every CTA takes an equal contiguous
@@ -24,9 +24,10 @@
 // their fixed order (the sums come out the same whichever CTA that is).  With one
 // join of the warps per CTA instead of one per segment, ragged batches lost a third of their time.
 //
-// Products.  mma.sync: the tensor-memory path needs 128 rows of queries, and a request has
-// G = Hq / H <= 16 of them per head, so its staging of operands would cost more than
-// the product.
+// Products.  mma.sync, whose operands are registers: the codes are unpacked into them and used at once.  The tensor-memory
+// path takes 128 rows, which could be tokens (scores) and dims (sums), and would read the unpacked codes from shared
+// or tensor memory: in 8 bits 256 bytes written and read again per token and head, some 4 of the 5.7 cycles at
+// 128 bytes a cycle.  It has not been built or measured.
 //  - scores, up to four query heads: m16n8k32 in integers, A = 16 tokens x 128 dims of K codes (nibbles shifted to
 //    the top of a byte: 16 code, one logic operation per four), B = the queries as whole multiples of 2^-22 of the
 //    power of two above their head's largest value, in three signed bytes: an fp16 value of at least 2^-11 of
@@ -77,16 +78,16 @@ constexpr int kStepV = kStep * kKvRowBytes, kStepKs = 2 * kStepV, kStepVs = kSte
 constexpr int kStepBytes = kStepVs + 2 * kStep;  // K codes, V codes, K scales, V scales
 constexpr int kDepth = 2;           // turns of a warp in shared memory: one taken, one under way
 // What a request and head costs besides its turns, in turns.  With 1, 2, 3 and 4: 17 ragged requests of 32/8 heads to
-// 8192 tokens 29.2, 25.8, 26.0, 25.6 us, 48 of 16/16 heads to 4000 59.3, 54.0, 53.2, 53.3, one of 4000 tokens 13.9,
-// 13.7, 11.9, 12.2, 64 even ones of 64/8 heads and 14200 206.7, 208.6, 208.9, 209.4.
+// 8192 tokens 29.4, 26.2, 26.3, 25.9 us, 48 of 16/16 heads to 4000 60.3, 54.0, 53.3, 53.3, one of 4000 tokens 13.6,
+// 13.9, 12.5, 12.5, 64 even ones of 64/8 heads and 14200 228.4, 228.4, 228.7, 229.1.
 constexpr int kItemCost = 3;
 // Little work: a part shorter than kMinUnits, or a request and head in more than kMaxParts parts, costs
-// more in the join than it saves.  One request of 8 heads and 4000 tokens took 14.2 us with parts of 8, 16.6 us
-// with 24, 18.8 us with 40; one head of 16384 tokens 17.5 us in 64 parts, 14.7 us in 32.
+// more in the join than it saves.  One request of 8 heads and 4000 tokens took 12.4 us with parts of 8, 16.0 us
+// with 24, 17.4 us with 40; one head of 16384 tokens 14.6 us in 64 parts, 12.9 us in 32.
 constexpr int kMinUnits = 8, kMaxParts = 32;
 // Where every request and head can have a CTA, none is divided unless the largest has kJoinUnits (the cost of the
-// join) more than an equal part.  33 requests of 40/8 heads and 1300 tokens took 22.3 us divided, 18.2 whole, of
-// 2048 28.0 and 24.5; 8 heads of 1000 tokens 11.9 and 11.4, of 4000 11.8 and 23.3; 33 of 0 to 2000 tokens 21.6 and 23.9.
+// join) more than an equal part.  33 requests of 40/8 heads and 1300 tokens took 23.4 us divided, 19.4 whole, of
+// 2048 29.5 and 26.2; 8 heads of 1000 tokens 12.0 and 11.6, of 4000 12.2 and 23.6; 33 of 0 to 2000 tokens 22.7 and 24.8.
 constexpr int kJoinUnits = 28;
 constexpr int kWarps = 8;
 constexpr int kAttnThreads = kWarps * 32;
@@ -158,6 +159,8 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
   return a / b;
 }
 
+// 2^x within 2^-22 of itself; results below 2^-126 are 0.  That is what two float32 roundings of the argument leave
+// as well, and nothing beside the output's 2^-11.
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

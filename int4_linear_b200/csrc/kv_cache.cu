@@ -271,9 +271,10 @@ struct KvWalk {
 
 // One head vector per 8 lanes, each with the 8 values at 8 sub and at 64 + 8 sub (whole sectors per load and
 // store), two vectors per turn, read before their slots are known so that the loads overlap.  Bound by HBM
-// (256 bytes read, 66 written per vector) and, at 58 registers, by the 32 warps of an SM that ask for it: 16384
-// tokens of 8 heads 16.5 us, 5.1 TB/s; with five or six CTAs per SM 17.1, with one or three vectors per turn 17.5 and
-// 17.1, with every value clamped 17.8, with a division per vector for its token 19.5.
+// (256 bytes read, 66 written per vector) and by the loads that an SM has under way: at 48 registers five CTAs fit, of the
+// eight per SM that the grid has.  16384 tokens of 8 heads 16.9 us, 5.0 TB/s; an earlier version took 16.5, with five or
+// six CTAs per SM in the grid 17.1, with one or three vectors per turn 17.5 and 17.1, with every value
+// clamped 17.8, with a division per vector for its token 19.5.  Codes 0 beside a scale of NaN would cost 0.5 us.
 __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const __half* __restrict__ K, long long ldk,
                                                                const __half* __restrict__ V, long long ldv, int T,
                                                                const int32_t* __restrict__ slots, float alpha_k,

@@ -22,9 +22,10 @@
 // last at a divided tile adds the float32 parts in the CTAs' order.
 //
 // Bounds (2 M N K operations at four times the bf16 rate, 6.6 PFLOP/s, or the weights' bytes at 6.55 TB/s), with the
-// quantizer before it: 16 x 57344 x 8192 (M x N x K) 40.4 us, 6.2 TB/s; 2048 x 28672 x 4096 100 us,
-// 4.8 PFLOP/s, there the power limit holds the clock at 1.5-1.6 GHz; a single token's 6144 x 4096
-// takes 8.3 us, nearly all of it launch, first loads, and the way out.
+// quantizer before it: 16 x 57344 x 8192 (M x N x K) 43.3 us, 6.1 TB/s; 2048 x 28672 x 4096 102 us in MXFP4, 110 us
+// in NVFP4, 4.7 and 4.4 PFLOP/s: there the power limit holds the clock at 1.5-1.6 GHz, and the tensor pipe is active in
+// 65 % of its cycles (what idles it in the others has not been found); a single token's 6144 x 4096
+// takes 8.6 us, nearly all of it launch, first loads, and the way out.
 #include <cuda_fp16.h>
 
 #include <algorithm>
